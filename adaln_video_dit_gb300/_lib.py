@@ -16,11 +16,13 @@ LIB_PATH = os.path.join(HERE, "libadaln.so")
 ADALN_F32, ADALN_BF16 = 0, 1
 (ADALN_OK, ADALN_ERR_NULL, ADALN_ERR_DIM, ADALN_ERR_ALIGN, ADALN_ERR_DTYPE,
  ADALN_ERR_SEG, ADALN_ERR_WORKSPACE, ADALN_ERR_CUDA, ADALN_ERR_ARG,
- ADALN_ERR_TIMEOUT) = range(10)
-ADALN_DEV_SEG_RANGE, ADALN_DEV_SEG_ORDER, ADALN_DEV_TIMEOUT = 1, 2, 4
+ ADALN_ERR_TIMEOUT, ADALN_ERR_POS) = range(11)
+ADALN_DEV_SEG_RANGE, ADALN_DEV_SEG_ORDER, ADALN_DEV_TIMEOUT, ADALN_DEV_POS_RANGE = 1, 2, 4, 8
 ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE = 0, 1, 2
+ADALN_KERNEL_QK_ROPE = 3
 KERNEL_NAMES = {0: "adaln_fwd_kernel", 1: "adaln_bwd_rows_kernel",
                 2: "adaln_bwd_finalize_kernel"}
+MAX_HEADS, MAX_HEAD_DIM, MAX_ROPE_AXES = 4096, 512, 4
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -28,13 +30,27 @@ EXPORTS = ["adaln_fwd", "adaln_bwd_workspace_size", "adaln_bwd", "adaln_bwd_noal
            "adaln_get_status", "adaln_status_bind", "adaln_strerror", "adaln_trace_begin",
            "adaln_trace_end", "adaln_trace_get", "adaln_launch_shape",
            "adaln_selftest_wait_timeout", "adaln_fwd_bwd_host_scratch_size",
-           "adaln_fwd_bwd_host"]
+           "adaln_fwd_bwd_host", "adaln_qk_rope_fwd", "adaln_qk_rope_bwd_workspace_size",
+           "adaln_qk_rope_bwd"]
 
 
 class AdalnError(RuntimeError):
     def __init__(self, code, what):
         self.code = code
         super().__init__(f"{what}: {strerror(code)} (code {code})")
+
+
+class Heads(ctypes.Structure):
+    """adaln_heads_t: a [T, heads, dh] tensor by pointer and strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    """adaln_rope_t: the rotary table and positions of a call."""
+    _fields_ = [("table", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32 * MAX_ROPE_AXES),
+                ("interleaved", ctypes.c_int32)]
 
 
 def _load():
@@ -73,6 +89,16 @@ def _load():
     lib.adaln_fwd_bwd_host.restype = ci
     lib.adaln_fwd_bwd_host.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, ci, f32, vp, vp, vp,
                                        vp, vp, vp, i64, vp, ctypes.c_size_t, vp]
+    hp, rp = ctypes.POINTER(Heads), ctypes.POINTER(Rope)
+    lib.adaln_qk_rope_fwd.restype = ci
+    lib.adaln_qk_rope_fwd.argtypes = [hp, hp, i64, i32, i32, i32, ci, rp, i32, vp, vp, f32, hp,
+                                      hp, vp]
+    lib.adaln_qk_rope_bwd_workspace_size.restype = ci
+    lib.adaln_qk_rope_bwd_workspace_size.argtypes = [i64, i32, i32, i32, ci,
+                                                     ctypes.POINTER(ctypes.c_size_t)]
+    lib.adaln_qk_rope_bwd.restype = ci
+    lib.adaln_qk_rope_bwd.argtypes = [hp, hp, hp, hp, i64, i32, i32, i32, ci, rp, i32, vp, vp,
+                                      f32, hp, hp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.adaln_selftest_wait_timeout.restype = ci
     lib.adaln_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     lib.adaln_launch_shape.restype = ci
@@ -260,6 +286,136 @@ def adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_row
                                 _ptr(scratch), scratch.numel() * scratch.element_size(),
                                 _stream_ptr(stream, scratch.device))
     _check(rc, "adaln_fwd_bwd_host")
+
+
+def _heads(t, name, like=None):
+    """Check a [T, heads, dh] tensor (any strides, dh contiguous); its Heads."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, dh], got {tuple(t.shape)}")
+    if like is not None:
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return Heads(t.data_ptr(), ts, hs)
+
+
+def _rope(table, pos, axis_pairs, interleaved, T, dh, device):
+    if not (table.is_cuda and pos.is_cuda and table.device == device and pos.device == device):
+        raise ValueError(f"table and pos must be on {device}")
+    if table.dtype != torch.float32 or not table.is_contiguous():
+        raise ValueError("table must be contiguous float32")
+    if pos.dtype != torch.int32 or not pos.is_contiguous():
+        raise ValueError("pos must be contiguous int32")
+    axes, P = len(axis_pairs), sum(axis_pairs)
+    if not 1 <= axes <= MAX_ROPE_AXES or min(axis_pairs) < 0:
+        raise ValueError(f"axis_pairs must hold 1 to {MAX_ROPE_AXES} counts >= 0")
+    if table.dim() != 3 or table.shape[1] != P or table.shape[2] != 2:
+        raise ValueError(f"table must have shape [rows, {P}, 2], got {tuple(table.shape)}")
+    if pos.shape != (T, axes):
+        raise ValueError(f"pos must have shape {(T, axes)}, got {tuple(pos.shape)}")
+    return Rope(table.data_ptr(), pos.data_ptr(), table.shape[0], axes,
+                (ctypes.c_int32 * MAX_ROPE_AXES)(*axis_pairs), 1 if interleaved else 0)
+
+
+def _weight(w, name, like):
+    if w is not None:
+        _dev(w, name, like.dtype, (like.shape[2],))
+        if w.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {w.device}")
+    return _ptr(w)
+
+
+def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False, wq=None,
+                      wk=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [T, hq, dh] and k [T, hk, dh] (k may be None), after
+    an RMS norm of every head when `norm` is set (weights wq, wk [dh] in q's
+    dtype, or None for ones).  table [rows, P, 2] fp32 holds cosines and sines,
+    pos [T, axes] int32 rows of it (-1: unrotated), axis_pairs the pairs of
+    each axis (P in all).  q and k may be strided views; q_out, k_out may be q, k.
+    Returns (q_out, k_out), allocated contiguous when not given."""
+    T, hq, dh = q.shape
+    qh = _heads(q, "q")
+    dev = q.device
+    hk = 0
+    kh = koh = None
+    rope = _rope(table, pos, axis_pairs, interleaved, T, dh, dev)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+    qoh = _heads(q_out, "q_out", q)
+    if k is not None:
+        hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != dh or k.dtype != q.dtype or k.device != dev:
+            raise ValueError("q and k must agree in tokens, head width, dtype and device")
+        kh = _heads(k, "k")
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
+        koh = _heads(k_out, "k_out", k)
+    rc = raw.adaln_qk_rope_fwd(qh, kh, T, hq, hk, dh, dtype_code(q.dtype), rope,
+                               1 if norm else 0, _weight(wq, "wq", q), _weight(wk, "wk", q),
+                               float(eps), qoh, koh, _stream_ptr(stream, dev))
+    _check(rc, "adaln_qk_rope_fwd")
+    return q_out, k_out
+
+
+def adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, dtype):
+    """Workspace bytes adaln_qk_rope_bwd needs for the weights' gradients."""
+    n = ctypes.c_size_t(0)
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    _check(raw.adaln_qk_rope_bwd_workspace_size(int(T), int(hq), int(hk), int(dh), code,
+                                                ctypes.byref(n)),
+           "adaln_qk_rope_bwd_workspace_size")
+    return n.value
+
+
+def adaln_qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved=True, norm=False,
+                      q=None, k=None, wq=None, wk=None, eps=1e-6, dq=None, dk=None, dwq=None,
+                      dwk=None, workspace=None, stream=None):
+    """Backward of adaln_qk_rope_fwd (q, k: its inputs, needed with norm).
+    Returns (dq, dk, dwq, dwk); dwq, dwk are fp32 [dh], None without norm (and
+    dk, dwk without k).  `workspace` is a uint8 CUDA tensor of at least
+    adaln_qk_rope_bwd_workspace_size bytes (allocated when not given)."""
+    T, hq, dh = dq_out.shape
+    dev, dt = dq_out.device, dq_out.dtype
+    doh = _heads(dq_out, "dq_out")
+    rope = _rope(table, pos, axis_pairs, interleaved, T, dh, dev)
+    dq = torch.empty(dq_out.shape, dtype=dt, device=dev) if dq is None else dq
+    dqh = _heads(dq, "dq", dq_out)
+    hk, dkoh, dkh, qh, kh, nbytes = 0, None, None, None, None, 0
+    if dk_out is not None:
+        hk = dk_out.shape[1]
+        if dk_out.shape[0] != T or dk_out.shape[2] != dh or dk_out.dtype != dt or dk_out.device != dev:
+            raise ValueError("dq_out and dk_out must agree in tokens, head width, dtype and device")
+        dkoh = _heads(dk_out, "dk_out")
+        dk = torch.empty(dk_out.shape, dtype=dt, device=dev) if dk is None else dk
+        dkh = _heads(dk, "dk", dk_out)
+    if norm:
+        if q is None or (k is None) != (dk_out is None):
+            raise ValueError("the norm's backward needs the forward's q (and k)")
+        qh = _heads(q, "q", dq_out)
+        kh = _heads(k, "k", dk_out) if k is not None else None
+        dwq = (torch.empty(dh, device=dev, dtype=torch.float32) if dwq is None
+               else _dev(dwq, "dwq", torch.float32, (dh,)))
+        if k is not None:
+            dwk = (torch.empty(dh, device=dev, dtype=torch.float32) if dwk is None
+                   else _dev(dwk, "dwk", torch.float32, (dh,)))
+        if workspace is None:
+            workspace = torch.empty(max(16, adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, dt)),
+                                    device=dev, dtype=torch.uint8)
+        _dev(workspace, "workspace")
+        nbytes = workspace.numel() * workspace.element_size()
+    rc = raw.adaln_qk_rope_bwd(doh, dkoh, qh, kh, T, hq, hk, dh, dtype_code(dt), rope,
+                               1 if norm else 0, _weight(wq, "wq", dq_out),
+                               _weight(wk, "wk", dq_out), float(eps), dqh, dkh, _ptr(dwq),
+                               _ptr(dwk), _ptr(workspace) if norm else None, nbytes,
+                               _stream_ptr(stream, dev))
+    _check(rc, "adaln_qk_rope_bwd")
+    return dq, dk, dwq, dwk
 
 
 def adaln_get_status(stream=None, device=None):

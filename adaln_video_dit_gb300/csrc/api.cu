@@ -264,6 +264,19 @@ size_t bwd_workspace_need(int64_t T, int32_t D, int32_t nseg, adaln_dtype_t dtyp
   return (bwd_workspace_bytes(s, D, nseg) + 255) & ~(size_t)255;
 }
 
+cudaError_t status_word(unsigned** out) { return status_ptr(out); }
+
+cudaError_t sm_count(int dev, int* sms) {
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+cudaError_t traced_launch(int kernel, cudaStream_t st,
+                          const std::function<cudaError_t()>& launch) {
+  return traced(kernel, st, launch);
+}
+
+int launch_failed(cudaError_t e) { return cuda_fail(e); }
+
 int check_dims_public(int64_t T, int32_t D, int32_t nseg, adaln_dtype_t dt) {
   return check_dims(T, D, nseg, dt);
 }
@@ -332,6 +345,7 @@ int adaln_get_status(uint32_t* host_bits, void* stream) {
   if (e != cudaSuccess) return cuda_fail(e);
   if (host_bits) *host_bits = bits;
   if (bits & (ADALN_DEV_SEG_RANGE | ADALN_DEV_SEG_ORDER)) return ADALN_ERR_SEG;
+  if (bits & ADALN_DEV_POS_RANGE) return ADALN_ERR_POS;
   if (bits & ADALN_DEV_TIMEOUT) return ADALN_ERR_TIMEOUT;
   return ADALN_OK;
 }
@@ -354,6 +368,7 @@ const char* adaln_strerror(int code) {
     case ADALN_ERR_CUDA: return "a CUDA call or kernel launch failed";
     case ADALN_ERR_ARG: return "invalid argument (eps or trace capacity)";
     case ADALN_ERR_TIMEOUT: return "an internal pipeline wait gave up (device status)";
+    case ADALN_ERR_POS: return "a rotary position outside the table (device status)";
     default: return "unknown status code";
   }
 }

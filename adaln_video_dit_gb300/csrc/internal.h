@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <functional>
+
 #include "../../include/adaln.h"
 
 #ifdef __CUDACC__
@@ -230,6 +232,14 @@ enum { kPoolFwdUnits = 0, kNumSlotPools = 1 };
 int launch_slot_acquire(int pool, cudaStream_t st);
 // After the launch: the slot stays busy until the work queued on `st` ends.
 cudaError_t launch_slot_release(int pool, int slot, cudaStream_t st, bool launched);
+
+// Shared by the entry points outside api.cu: the status word of the calling
+// thread's calls, the device's SM count, a launch bracketed by the timing
+// trace, and the status code of a failed CUDA call (its error is cleared).
+cudaError_t status_word(unsigned** out);
+cudaError_t sm_count(int dev, int* sms);
+cudaError_t traced_launch(int kernel, cudaStream_t st, const std::function<cudaError_t()>& launch);
+int launch_failed(cudaError_t e);
 
 // Bounded-wait self-test (selftest.cu).
 cudaError_t launch_wait_timeout_probe(unsigned* status, uint64_t limit_ns, cudaStream_t st);

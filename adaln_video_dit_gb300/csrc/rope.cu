@@ -1,0 +1,785 @@
+// Rotary positions over several axes for queries and keys, with an optional
+// RMS norm of every head in the same pass; forward and backward.
+//
+// For one head x[0..dh) of token t, with R = 2P rotated elements, pair p made
+// of elements (2p, 2p+1) (interleaved) or (p, p+P) (halves), pair p on axis
+// a(p), and (c, s) = table[pos[t, a(p)], p] (or (1, 0) at position -1):
+//
+//   n  = x * r * w,  r = 1 / sqrt(mean(x^2) + eps)      (n = x without norm)
+//   y1 = n1 c - n2 s,  y2 = n2 c + n1 s                 (elements >= R: y = n)
+//
+// and backward, from dy (R' is the rotation by the opposite angle):
+//
+//   g  = R' dy,  dw = sum over tokens and heads of g x r,  h = g w,
+//   dx = r h - x (r^3 mean(h x))                        (dx = g without norm)
+//
+// Bound: HBM.  Forward and plain rotation read and write every element once;
+// the norm's backward reads x and dy and writes dx.  Nothing is saved by the
+// forward: r is recomputed from the x that the backward has to read anyway.
+//
+// Layout of the work: P lanes share a head, each holding two 16-byte vectors
+// of it that contain whole pairs (interleaved: vectors j and j + half, halves:
+// a vector and its partner), so a rotation never leaves its lane and a norm
+// takes log2(P) shuffles.  A warp keeps one token's cosines and sines in
+// registers and walks that token's heads, 32 / P at a time.
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace adaln {
+namespace {
+
+constexpr int kWarps = 8;  // warps of a CTA
+constexpr int kThreads = kWarps * 32;
+// Elements of a head that the scalar path's 32 lanes hold (8 pairs a lane).
+constexpr int kScalarPairs = 8;
+
+enum { kRotate = 0, kNormFwd = 1, kNormBwd = 2 };
+
+struct Tensor {
+  const char* p;
+  int64_t ts, hs;  // bytes from token to token, head to head
+};
+
+struct Side {  // queries or keys
+  Tensor x;    // forward input (kRotate: what is rotated)
+  Tensor dy;   // kNormBwd only
+  char* out;
+  int64_t out_ts, out_hs;
+  const void* w;   // [dh] norm weight, or nullptr: ones
+  float* partial;  // kNormBwd: [chunks * gridDim.x][dh], or nullptr: no dw
+  int heads;
+  int chunks;      // the heads are split into this many chunks
+  int per_chunk;   // heads of a chunk
+};
+
+struct RopeArgs {
+  Side side[2];
+  const float2* table;  // [rows][P]
+  const int32_t* pos;   // [T][axes]
+  int64_t T;
+  int rows, axes, P, dh, nvec;
+  int axis_end[4];  // pairs [axis_end[a-1], axis_end[a]) belong to axis a
+  float eps, inv_dh;
+  float sign;  // of the sine: -1 turns back
+  unsigned* status;
+};
+
+// Axis of pair p, or 4 for an unrotated one.
+__device__ __forceinline__ int axis_of(const RopeArgs& a, int p) {
+  return (p >= a.axis_end[0]) + (p >= a.axis_end[1]) + (p >= a.axis_end[2]) + (p >= a.axis_end[3]);
+}
+
+// Table rows of a token's axes, -1 where the axis does not turn the token.
+// A position outside [-1, rows) is recorded and does not turn it either.
+struct Rows {
+  int r[4];
+  __device__ __forceinline__ void load(const RopeArgs& a, int64_t t, int lane) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[i] = -1;
+      if (i < a.axes) {
+        const int p = a.pos[t * a.axes + i];
+        if (p >= 0 && p < a.rows) r[i] = p;
+        bad |= p < -1 || p >= a.rows;
+      }
+    }
+    if (bad && lane == 0) atomicOr(a.status, ADALN_DEV_POS_RANGE);
+  }
+  __device__ __forceinline__ float2 at(const RopeArgs& a, int axis, int p) const {
+    const int row = axis == 0 ? r[0] : axis == 1 ? r[1] : axis == 2 ? r[2] : axis == 3 ? r[3] : -1;
+    if (row < 0) return make_float2(1.0f, 0.0f);
+    float2 c = __ldg(a.table + (int64_t)row * a.P + p);
+    c.y *= a.sign;
+    return c;
+  }
+};
+
+// (u, v) turned by (c, s).  A pair with a zero sine takes nothing from its
+// partner, so an unrotated element passes exactly, whatever the other holds.
+__device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
+  const float a = u, b = v;
+  const float bs = cs.y == 0.0f ? 0.0f : b * cs.y, as = cs.y == 0.0f ? 0.0f : a * cs.y;
+  u = fmaf(a, cs.x, -bs);
+  v = fmaf(b, cs.x, as);
+}
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Sum over the CTA's warps of red[warp][0..dh), in warp order, into slot.
+__device__ __forceinline__ void store_partial(const float* red, float* slot, int dh) {
+  __syncthreads();
+  for (int d = threadIdx.x; d < dh; d += kThreads) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += red[w * dh + d];
+    slot[d] = s;
+  }
+}
+
+// Vector path: head rows of whole, aligned 16-byte vectors, at most 64.
+// P lanes a head, U groups of 32 / P heads in flight.
+template <class E, int P, bool HALF, int MODE, int U>
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int N = E::EPV;       // elements of a vector, pairs of a lane
+  constexpr int HPW = 32 / P;     // heads side by side in a warp
+  extern __shared__ float red[];  // kNormBwd: [kWarps][dh]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = lane & (P - 1), sub = lane / P;
+  const bool is_k = (int)blockIdx.y >= a.side[0].chunks;
+  const Side& sd = a.side[is_k];
+  const int chunk = is_k ? blockIdx.y - a.side[0].chunks : blockIdx.y;
+  const int h_end = min(sd.heads, (chunk + 1) * sd.per_chunk);
+
+  // This lane's two vectors (-1: none) and the axes of its pairs.
+  int va, vb, p0, p1;
+  const int half = (a.nvec + 1) >> 1;
+  if (HALF) {
+    const int nr = a.P / N;
+    va = j < nr ? j : 2 * nr + 2 * (j - nr);
+    vb = j < nr ? j + nr : va + 1;
+    p0 = j < nr ? N * j : a.P;
+    p1 = 0;  // one run of N pairs
+  } else {
+    va = j;
+    vb = j + half;
+    p0 = N / 2 * va;
+    p1 = N / 2 * vb;
+  }
+  if (va >= a.nvec || j >= half) va = -1;
+  if (vb >= a.nvec || j >= half) vb = -1;
+  auto pair_of = [&](int i) { return HALF ? p0 + i : (i < N / 2 ? p0 + i : p1 + i - N / 2); };
+  unsigned axes = 0;  // 3 bits a pair
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    axes |= (unsigned)(HALF && p0 >= a.P ? 4 : axis_of(a, pair_of(i))) << (3 * i);
+
+  grid_wait();
+  grid_launch_dependents();
+
+  float2 w[N];  // norm weights of vector a, then b
+  if (MODE != kRotate) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = make_float2(1.0f, 1.0f);
+    if (sd.w != nullptr) {
+      float2 f[N / 2];
+      const char* wp = static_cast<const char*>(sd.w);
+      if (va >= 0) {
+        E::unpack2(ld_global_v4(wp + va * 16), f);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = f[i];
+      }
+      if (vb >= 0) {
+        E::unpack2(ld_global_v4(wp + vb * 16), f);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[N / 2 + i] = f[i];
+      }
+    }
+  }
+  float2 dw[MODE == kNormBwd ? N : 1];
+  if (MODE == kNormBwd) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[i] = make_float2(0.0f, 0.0f);
+  }
+
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += step) {
+    Rows rows;
+    rows.load(a, t, lane);
+    float2 cs[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) cs[i] = rows.at(a, (axes >> (3 * i)) & 7, pair_of(i));
+
+    auto rotate = [&](float2(&f)[N]) {  // f: vector a's pairs of floats, then b's
+      if (HALF) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          turn(f[i].x, f[N / 2 + i].x, cs[2 * i]);
+          turn(f[i].y, f[N / 2 + i].y, cs[2 * i + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) turn(f[i].x, f[i].y, cs[i]);
+      }
+    };
+
+    for (int h0 = chunk * sd.per_chunk; h0 < h_end; h0 += U * HPW) {
+      uint4 xa[U], xb[U], ya[MODE == kNormBwd ? U : 1], yb[MODE == kNormBwd ? U : 1];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * HPW + sub;
+        const bool on = h < h_end;
+        const char* x = sd.x.p + t * sd.x.ts + h * sd.x.hs;
+        xa[u] = on && va >= 0 ? ld_global_v4(x + va * 16) : make_uint4(0, 0, 0, 0);
+        xb[u] = on && vb >= 0 ? ld_global_v4(x + vb * 16) : make_uint4(0, 0, 0, 0);
+        if (MODE == kNormBwd) {
+          const char* y = sd.dy.p + t * sd.dy.ts + h * sd.dy.hs;
+          ya[u] = on && va >= 0 ? ld_global_v4(y + va * 16) : make_uint4(0, 0, 0, 0);
+          yb[u] = on && vb >= 0 ? ld_global_v4(y + vb * 16) : make_uint4(0, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * HPW + sub;
+        float2 f[N], half_v[N / 2];
+        E::unpack2(xa[u], half_v);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) f[i] = half_v[i];
+        E::unpack2(xb[u], half_v);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) f[N / 2 + i] = half_v[i];
+
+        if (MODE == kRotate) {
+          rotate(f);
+        } else {
+          float2 ss = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) ss = fma2(f[i], f[i], ss);
+          float sx = ss.x + ss.y;
+          if (MODE == kNormFwd) {
+#pragma unroll
+            for (int o = P / 2; o > 0; o >>= 1) sx += __shfl_xor_sync(~0u, sx, o);
+            const float r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = mul2(mul2(f[i], splat2(r)), w[i]);
+            rotate(f);
+          } else {
+            float2 g[N];
+            E::unpack2(ya[u], half_v);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) g[i] = half_v[i];
+            E::unpack2(yb[u], half_v);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) g[N / 2 + i] = half_v[i];
+            rotate(g);
+            float2 hs = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) hs = fma2(mul2(g[i], w[i]), f[i], hs);
+            float sh = hs.x + hs.y;
+#pragma unroll
+            for (int o = P / 2; o > 0; o >>= 1) {
+              sx += __shfl_xor_sync(~0u, sx, o);
+              sh += __shfl_xor_sync(~0u, sh, o);
+            }
+            const float r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
+            const float k = -r * r * r * (sh * a.inv_dh);
+            // Lanes past the last head hold zeros, so they add nothing to dw
+            // (g = 0) as long as r is finite; eps = 0 would make it 0 * inf.
+            const float rd = h < h_end ? r : 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dw[i] = fma2(g[i], mul2(f[i], splat2(rd)), dw[i]);
+              f[i] = fma2(f[i], splat2(k), mul2(mul2(g[i], w[i]), splat2(r)));
+            }
+          }
+        }
+        if (h < h_end) {
+          char* o = sd.out + t * sd.out_ts + h * sd.out_hs;
+          if (va >= 0) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) half_v[i] = f[i];
+            *reinterpret_cast<uint4*>(o + va * 16) = E::pack2(half_v);
+          }
+          if (vb >= 0) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) half_v[i] = f[N / 2 + i];
+            *reinterpret_cast<uint4*>(o + vb * 16) = E::pack2(half_v);
+          }
+        }
+      }
+    }
+  }
+
+  if (MODE == kNormBwd && sd.partial != nullptr) {
+    // Lanes of the same j hold the same columns: sum them in a fixed tree.
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int o = P; o < 32; o <<= 1) {
+        dw[i].x += __shfl_xor_sync(~0u, dw[i].x, o);
+        dw[i].y += __shfl_xor_sync(~0u, dw[i].y, o);
+      }
+      const int v = i < N / 2 ? va : vb;
+      if (sub == 0 && v >= 0) {
+        float* to = red + warp * a.dh + v * N + 2 * (i < N / 2 ? i : i - N / 2);
+        to[0] = dw[i].x;
+        to[1] = dw[i].y;
+      }
+    }
+    store_partial(red, sd.partial + ((int64_t)chunk * gridDim.x + blockIdx.x) * a.dh, a.dh);
+  }
+}
+
+template <class E>
+__device__ __forceinline__ float load1(const char* p);
+template <>
+__device__ __forceinline__ float load1<BF16>(const char* p) {
+  return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+}
+template <>
+__device__ __forceinline__ float load1<F32>(const char* p) {
+  return *reinterpret_cast<const float*>(p);
+}
+__device__ __forceinline__ void store1(char* p, float v, BF16) {
+  *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void store1(char* p, float v, F32) { *reinterpret_cast<float*>(p) = v; }
+
+// Scalar path: any head width up to 512, any strides, element alignment.  A
+// warp holds one head, lane l the pairs l, l + 32, ...; pairs from P on are
+// the unrotated elements, two by two.
+template <class E, int MODE>
+__global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_constant__ RopeArgs a,
+                                                               int interleaved) {
+  extern __shared__ float red[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool is_k = (int)blockIdx.y >= a.side[0].chunks;
+  const Side& sd = a.side[is_k];
+  const int chunk = is_k ? blockIdx.y - a.side[0].chunks : blockIdx.y;
+  const int h_end = min(sd.heads, (chunk + 1) * sd.per_chunk);
+
+  int da[kScalarPairs], db[kScalarPairs];  // elements of the pair, -1: none
+#pragma unroll
+  for (int i = 0; i < kScalarPairs; ++i) {
+    const int p = lane + 32 * i;
+    da[i] = p >= a.P ? 2 * p : interleaved ? 2 * p : p;
+    db[i] = p >= a.P ? 2 * p + 1 : interleaved ? 2 * p + 1 : p + a.P;
+    if (da[i] >= a.dh) da[i] = -1;
+    if (db[i] >= a.dh) db[i] = -1;
+  }
+
+  grid_wait();
+  grid_launch_dependents();
+
+  float wa[kScalarPairs], wb[kScalarPairs], dwa[kScalarPairs], dwb[kScalarPairs];
+#pragma unroll
+  for (int i = 0; i < kScalarPairs; ++i) {
+    const char* wp = static_cast<const char*>(sd.w);
+    wa[i] = MODE != kRotate && wp && da[i] >= 0 ? load1<E>(wp + da[i] * E::SIZE) : 1.0f;
+    wb[i] = MODE != kRotate && wp && db[i] >= 0 ? load1<E>(wp + db[i] * E::SIZE) : 1.0f;
+    dwa[i] = dwb[i] = 0.0f;
+  }
+
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += step) {
+    Rows rows;
+    rows.load(a, t, lane);
+    float2 cs[kScalarPairs];
+#pragma unroll
+    for (int i = 0; i < kScalarPairs; ++i)
+      cs[i] = rows.at(a, axis_of(a, lane + 32 * i), lane + 32 * i);
+    for (int h = chunk * sd.per_chunk; h < h_end; ++h) {
+      const char* x = sd.x.p + t * sd.x.ts + h * sd.x.hs;
+      float fa[kScalarPairs], fb[kScalarPairs], sx = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kScalarPairs; ++i) {
+        fa[i] = da[i] >= 0 ? load1<E>(x + da[i] * E::SIZE) : 0.0f;
+        fb[i] = db[i] >= 0 ? load1<E>(x + db[i] * E::SIZE) : 0.0f;
+        sx = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], sx));
+      }
+      float r = 1.0f;
+      if (MODE != kRotate) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sx += __shfl_xor_sync(~0u, sx, o);
+        r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
+      }
+      if (MODE != kNormBwd) {
+#pragma unroll
+        for (int i = 0; i < kScalarPairs; ++i) {
+          if (MODE == kNormFwd) {
+            fa[i] = fa[i] * r * wa[i];
+            fb[i] = fb[i] * r * wb[i];
+          }
+          turn(fa[i], fb[i], cs[i]);
+        }
+      } else {
+        const char* y = sd.dy.p + t * sd.dy.ts + h * sd.dy.hs;
+        float ga[kScalarPairs], gb[kScalarPairs], sh = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kScalarPairs; ++i) {
+          ga[i] = da[i] >= 0 ? load1<E>(y + da[i] * E::SIZE) : 0.0f;
+          gb[i] = db[i] >= 0 ? load1<E>(y + db[i] * E::SIZE) : 0.0f;
+          turn(ga[i], gb[i], cs[i]);
+          sh = fmaf(ga[i] * wa[i], fa[i], fmaf(gb[i] * wb[i], fb[i], sh));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sh += __shfl_xor_sync(~0u, sh, o);
+        const float k = -r * r * r * (sh * a.inv_dh);
+#pragma unroll
+        for (int i = 0; i < kScalarPairs; ++i) {
+          if (da[i] >= 0) dwa[i] = fmaf(ga[i], fa[i] * r, dwa[i]);
+          if (db[i] >= 0) dwb[i] = fmaf(gb[i], fb[i] * r, dwb[i]);
+          fa[i] = fmaf(fa[i], k, ga[i] * wa[i] * r);
+          fb[i] = fmaf(fb[i], k, gb[i] * wb[i] * r);
+        }
+      }
+      // A lane writes the elements it read: in place works.
+      char* o = sd.out + t * sd.out_ts + h * sd.out_hs;
+#pragma unroll
+      for (int i = 0; i < kScalarPairs; ++i) {
+        if (da[i] >= 0) store1(o + da[i] * E::SIZE, fa[i], E());
+        if (db[i] >= 0) store1(o + db[i] * E::SIZE, fb[i], E());
+      }
+    }
+  }
+
+  if (MODE == kNormBwd && sd.partial != nullptr) {
+#pragma unroll
+    for (int i = 0; i < kScalarPairs; ++i) {
+      if (da[i] >= 0) red[warp * a.dh + da[i]] = dwa[i];
+      if (db[i] >= 0) red[warp * a.dh + db[i]] = dwb[i];
+    }
+    store_partial(red, sd.partial + ((int64_t)chunk * gridDim.x + blockIdx.x) * a.dh, a.dh);
+  }
+}
+
+// dw[d] = sum of the partial slots of a side, in a fixed order: 32 columns a
+// CTA, warp w the slots w, w + 32, ... in order, then the 32 warps in order.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* pq, int nq, float* dwq,
+                                                       const float* pk, int nk, float* dwk,
+                                                       int dh) {
+  __shared__ float red[32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d = blockIdx.x * 32 + lane;
+  const float* p = blockIdx.y == 0 ? pq : pk;
+  const int n = blockIdx.y == 0 ? nq : nk;
+  float* dw = blockIdx.y == 0 ? dwq : dwk;
+  grid_wait();
+  if (dw == nullptr) return;
+  float s = 0.0f;
+  if (d < dh) {
+#pragma unroll 4
+    for (int i = warp; i < n; i += 32) s += p[(int64_t)i * dh + d];
+  }
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && d < dh) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) t += red[w][lane];
+    dw[d] = t;
+  }
+}
+
+// ----- host side ---------------------------------------------------------------
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+cudaError_t launch(void* kernel, dim3 grid, int threads, size_t smem, void** params,
+                   cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, params);
+}
+
+constexpr int kUnroll[3] = {4, 4, 2};  // head groups in flight by mode
+
+template <class E, int P>
+void* vec_kernel(int mode, bool half) {
+  switch (mode) {
+    case kRotate:
+      return half ? (void*)rope_vec_kernel<E, P, true, kRotate, kUnroll[0]>
+                  : (void*)rope_vec_kernel<E, P, false, kRotate, kUnroll[0]>;
+    case kNormFwd:
+      return half ? (void*)rope_vec_kernel<E, P, true, kNormFwd, kUnroll[1]>
+                  : (void*)rope_vec_kernel<E, P, false, kNormFwd, kUnroll[1]>;
+    default:
+      return half ? (void*)rope_vec_kernel<E, P, true, kNormBwd, kUnroll[2]>
+                  : (void*)rope_vec_kernel<E, P, false, kNormBwd, kUnroll[2]>;
+  }
+}
+
+template <class E>
+void* pick_kernel(int lanes, int mode, bool half) {
+  if (lanes <= 4) return vec_kernel<E, 4>(mode, half);
+  if (lanes <= 8) return vec_kernel<E, 8>(mode, half);
+  if (lanes <= 16) return vec_kernel<E, 16>(mode, half);
+  return vec_kernel<E, 32>(mode, half);
+}
+
+template <class E>
+void* scalar_kernel(int mode) {
+  return mode == kRotate    ? (void*)rope_scalar_kernel<E, kRotate>
+         : mode == kNormFwd ? (void*)rope_scalar_kernel<E, kNormFwd>
+                            : (void*)rope_scalar_kernel<E, kNormBwd>;
+}
+
+struct Plan {
+  bool vec;
+  int lanes;      // lanes of a head (vector path, a power of two from 4 on)
+  int chunks[2];  // per side
+  int per_chunk[2];
+  int grid_x;
+};
+
+// Split of a call: token x chunk of heads per warp.  With many tokens a warp
+// takes all of a side's heads, so a token's angles are loaded twice in all;
+// with few, the heads are split until about every SM's warps have work.  The
+// norm's backward keeps its weight sums in registers over a loop of tokens,
+// so its grid is bounded (two CTAs an SM), the others' is not.
+cudaError_t make_plan(int64_t T, const int (&heads)[2], int dh, int mode, bool vec, int es,
+                      Plan* p) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = sm_count(dev, &sms);
+  if (e != cudaSuccess) return e;
+  p->vec = vec;
+  p->lanes = 32;
+  int unit = 1;
+  if (vec) {
+    const int want = (dh * es / 16 + 1) / 2;
+    p->lanes = want <= 4 ? 4 : want <= 8 ? 8 : want <= 16 ? 16 : 32;
+    unit = 32 / p->lanes;
+  }
+  const int64_t warps = (int64_t)sms * 16;
+  for (int s = 0; s < 2; ++s) {
+    const int groups = (heads[s] + unit - 1) / unit;
+    int64_t split = T > 0 ? (warps + 2 * T - 1) / (2 * T) : 1;
+    if (split > groups) split = groups;
+    if (split < 1) split = 1;
+    const int per = groups > 0 ? (int)((groups + split - 1) / split) * unit : unit;
+    p->per_chunk[s] = per;
+    p->chunks[s] = heads[s] > 0 ? (heads[s] + per - 1) / per : 0;
+  }
+  int64_t gx = (T + kWarps - 1) / kWarps;
+  if (mode == kNormBwd) {
+    const int chunks = p->chunks[0] + p->chunks[1];
+    const int64_t most = (2 * (int64_t)sms + chunks - 1) / chunks;
+    if (gx > most) gx = most;
+  }
+  p->grid_x = (int)(gx < 1 ? 1 : gx);
+  return cudaSuccess;
+}
+
+size_t dw_bytes(const Plan& p, int dh) {
+  return (size_t)(p.chunks[0] + p.chunks[1]) * p.grid_x * dh * sizeof(float);
+}
+
+int check_common(int64_t T, int32_t hq, int32_t hk, int32_t dh, adaln_dtype_t dt) {
+  if (dt != ADALN_F32 && dt != ADALN_BF16) return ADALN_ERR_DTYPE;
+  if (T < 0 || T > (int64_t)INT32_MAX) return ADALN_ERR_DIM;
+  if (hq < 0 || hk < 0 || hq + (int64_t)hk < 1 || hq > ADALN_MAX_HEADS || hk > ADALN_MAX_HEADS)
+    return ADALN_ERR_DIM;
+  if (dh < 1 || dh > ADALN_MAX_HEAD_DIM) return ADALN_ERR_DIM;
+  return ADALN_OK;
+}
+
+int check_rope(const adaln_rope_t* r, int32_t dh, int64_t T) {
+  if (!r) return ADALN_ERR_NULL;
+  if (r->axes < 1 || r->axes > ADALN_MAX_ROPE_AXES || r->rows < 1) return ADALN_ERR_DIM;
+  int64_t pairs = 0;
+  for (int i = 0; i < r->axes; ++i) {
+    if (r->pairs[i] < 0) return ADALN_ERR_DIM;
+    pairs += r->pairs[i];
+  }
+  if (pairs < 1 || 2 * pairs > dh) return ADALN_ERR_DIM;
+  if (T > 0 && (!r->table || !r->pos)) return ADALN_ERR_NULL;
+  if (!aligned_to(r->table, 8) || !aligned_to(r->pos, 4)) return ADALN_ERR_ALIGN;
+  return ADALN_OK;
+}
+
+// A tensor's pointer, and whether vectors fit it.
+int check_heads(const adaln_heads_t* h, int heads, int64_t T, int es, bool* vec) {
+  if (heads == 0) return ADALN_OK;
+  if (!h) return ADALN_ERR_NULL;
+  if (T > 0 && !h->ptr) return ADALN_ERR_NULL;
+  if (h->token_stride < 0 || h->head_stride < 0) return ADALN_ERR_DIM;
+  if (!aligned_to(h->ptr, es)) return ADALN_ERR_ALIGN;
+  if (!aligned_to(h->ptr, 16) || h->token_stride * es % 16 != 0 || h->head_stride * es % 16 != 0)
+    *vec = false;
+  return ADALN_OK;
+}
+
+Tensor tensor_of(const adaln_heads_t* h, int es) {
+  if (!h) return Tensor{nullptr, 0, 0};
+  return Tensor{static_cast<const char*>(h->ptr), h->token_stride * es, h->head_stride * es};
+}
+
+// Whether the head's layout suits the vector path (its pointers aside).
+bool vec_layout(int dh, int es, int pairs, bool half) {
+  return dh * es % 16 == 0 && dh * es / 16 <= 64 && (!half || pairs * es % 16 == 0);
+}
+
+int run(int mode, const adaln_heads_t* const (&x)[2], const adaln_heads_t* const (&dy)[2],
+        const adaln_heads_t* const (&out)[2], int64_t T, const int (&heads)[2], int32_t dh,
+        adaln_dtype_t dtype, const adaln_rope_t* rope, const void* const (&w)[2], float eps,
+        float sign, float* const (&dw)[2], void* workspace, size_t workspace_bytes, bool vec,
+        cudaStream_t st) {
+  const int es = dtype == ADALN_BF16 ? 2 : 4;
+  RopeArgs a = {};
+  for (int i = 0, at = 0; i < 4; ++i) {
+    if (i < rope->axes) at += rope->pairs[i];
+    a.axis_end[i] = at;
+    a.P = at;
+  }
+  Plan p;
+  cudaError_t e = make_plan(T, heads, dh, mode, vec, es, &p);
+  unsigned* status = nullptr;
+  if (e == cudaSuccess) e = status_word(&status);
+  if (e != cudaSuccess) return launch_failed(e);
+  const bool want_dw = mode == kNormBwd && (dw[0] || dw[1]);
+  if (want_dw && workspace_bytes < dw_bytes(p, dh)) return ADALN_ERR_WORKSPACE;
+
+  float* partial = want_dw ? static_cast<float*>(workspace) : nullptr;
+  for (int s = 0; s < 2; ++s) {
+    Side& sd = a.side[s];
+    sd.x = tensor_of(x[s], es);
+    sd.dy = tensor_of(dy[s], es);
+    const Tensor o = tensor_of(out[s], es);
+    sd.out = const_cast<char*>(o.p);
+    sd.out_ts = o.ts;
+    sd.out_hs = o.hs;
+    sd.w = w[s];
+    sd.heads = heads[s];
+    sd.chunks = p.chunks[s];
+    sd.per_chunk = p.per_chunk[s];
+    sd.partial = partial && dw[s] ? partial + (size_t)(s ? p.chunks[0] : 0) * p.grid_x * dh
+                                  : nullptr;
+  }
+  a.table = reinterpret_cast<const float2*>(rope->table);
+  a.pos = rope->pos;
+  a.T = T;
+  a.rows = rope->rows;
+  a.axes = rope->axes;
+  a.dh = dh;
+  a.nvec = dh * es / 16;
+  a.eps = eps;
+  a.inv_dh = 1.0f / (float)dh;
+  a.sign = sign;
+  a.status = status;
+
+  const bool half = !rope->interleaved;
+  int interleaved = rope->interleaved != 0;
+  void* kernel;
+  if (p.vec)
+    kernel = dtype == ADALN_BF16 ? pick_kernel<BF16>(p.lanes, mode, half)
+                                 : pick_kernel<F32>(p.lanes, mode, half);
+  else
+    kernel = dtype == ADALN_BF16 ? scalar_kernel<BF16>(mode) : scalar_kernel<F32>(mode);
+  void* params[2] = {&a, &interleaved};
+  const dim3 grid((unsigned)p.grid_x, (unsigned)(p.chunks[0] + p.chunks[1]));
+  const size_t smem = mode == kNormBwd ? (size_t)kWarps * dh * sizeof(float) : 0;
+  if (T > 0) {
+    e = traced_launch(ADALN_KERNEL_QK_ROPE, st,
+                      [&] { return launch(kernel, grid, kThreads, smem, params, st); });
+    if (e != cudaSuccess) return launch_failed(e);
+  }
+  if (want_dw) {
+    const float* pq = a.side[0].partial;
+    const float* pk = a.side[1].partial;
+    // No tokens (or no heads): the sums are empty.
+    int nq = T > 0 ? p.chunks[0] * p.grid_x : 0, nk = T > 0 ? p.chunks[1] * p.grid_x : 0;
+    float *dwq = dw[0], *dwk = dw[1];
+    int d = dh;
+    void* params2[7] = {&pq, &nq, &dwq, &pk, &nk, &dwk, &d};
+    e = traced_launch(ADALN_KERNEL_QK_ROPE, st, [&] {
+      return launch((void*)rope_dw_kernel, dim3((unsigned)(dh + 31) / 32, 2), 1024, 0, params2,
+                    st);
+    });
+    if (e != cudaSuccess) return launch_failed(e);
+  }
+  return ADALN_OK;
+}
+
+}  // namespace
+}  // namespace adaln
+
+using namespace adaln;
+
+extern "C" {
+
+int adaln_qk_rope_fwd(const adaln_heads_t* q, const adaln_heads_t* k, int64_t T, int32_t hq,
+                      int32_t hk, int32_t dh, adaln_dtype_t dtype, const adaln_rope_t* rope,
+                      int32_t norm, const void* wq, const void* wk, float eps,
+                      const adaln_heads_t* q_out, const adaln_heads_t* k_out, void* stream) {
+  int rc = check_common(T, hq, hk, dh, dtype);
+  if (rc == ADALN_OK) rc = check_rope(rope, dh, T);
+  if (rc != ADALN_OK) return rc;
+  const int es = dtype == ADALN_BF16 ? 2 : 4;
+  int pairs = 0;
+  for (int i = 0; i < rope->axes; ++i) pairs += rope->pairs[i];
+  bool vec = vec_layout(dh, es, pairs, !rope->interleaved);
+  if ((rc = check_heads(q, hq, T, es, &vec)) || (rc = check_heads(k, hk, T, es, &vec)) ||
+      (rc = check_heads(q_out, hq, T, es, &vec)) || (rc = check_heads(k_out, hk, T, es, &vec)))
+    return rc;
+  if (norm) {
+    if (!std::isfinite(eps) || eps < 0.0f) return ADALN_ERR_ARG;
+    if (!aligned_to(wq, es) || !aligned_to(wk, es)) return ADALN_ERR_ALIGN;
+    if (!aligned_to(wq, 16) || !aligned_to(wk, 16)) vec = false;
+  }
+  if (T == 0) return ADALN_OK;
+  return run(norm ? kNormFwd : kRotate, {q, k}, {nullptr, nullptr}, {q_out, k_out}, T, {hq, hk},
+             dh, dtype, rope, {wq, wk}, eps, 1.0f, {nullptr, nullptr}, nullptr, 0, vec,
+             static_cast<cudaStream_t>(stream));
+}
+
+int adaln_qk_rope_bwd_workspace_size(int64_t T, int32_t hq, int32_t hk, int32_t dh,
+                                     adaln_dtype_t dtype, size_t* bytes) {
+  const int rc = check_common(T, hq, hk, dh, dtype);
+  if (rc != ADALN_OK) return rc;
+  if (!bytes) return ADALN_ERR_NULL;
+  // The larger of the two paths' needs (which one runs depends on alignment).
+  const int es = dtype == ADALN_BF16 ? 2 : 4;
+  size_t most = 0;
+  for (int vec = 0; vec < 2; ++vec) {
+    if (vec && !vec_layout(dh, es, 0, false)) continue;
+    Plan p;
+    const cudaError_t e = make_plan(T, {hq, hk}, dh, kNormBwd, vec != 0, es, &p);
+    if (e != cudaSuccess) return launch_failed(e);
+    const size_t need = (dw_bytes(p, dh) + 255) & ~(size_t)255;
+    most = need > most ? need : most;
+  }
+  *bytes = most;
+  return ADALN_OK;
+}
+
+int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t* dk_out,
+                      const adaln_heads_t* q, const adaln_heads_t* k, int64_t T, int32_t hq,
+                      int32_t hk, int32_t dh, adaln_dtype_t dtype, const adaln_rope_t* rope,
+                      int32_t norm, const void* wq, const void* wk, float eps,
+                      const adaln_heads_t* dq, const adaln_heads_t* dk, float* dwq, float* dwk,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_common(T, hq, hk, dh, dtype);
+  if (rc == ADALN_OK) rc = check_rope(rope, dh, T);
+  if (rc != ADALN_OK) return rc;
+  const int es = dtype == ADALN_BF16 ? 2 : 4;
+  int pairs = 0;
+  for (int i = 0; i < rope->axes; ++i) pairs += rope->pairs[i];
+  bool vec = vec_layout(dh, es, pairs, !rope->interleaved);
+  if ((rc = check_heads(dq_out, hq, T, es, &vec)) || (rc = check_heads(dk_out, hk, T, es, &vec)) ||
+      (rc = check_heads(dq, hq, T, es, &vec)) || (rc = check_heads(dk, hk, T, es, &vec)))
+    return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!norm) {
+    // The rotation's transpose is the rotation by the opposite angle.
+    if (dwq || dwk) return ADALN_ERR_ARG;
+    if (T == 0) return ADALN_OK;
+    return run(kRotate, {dq_out, dk_out}, {nullptr, nullptr}, {dq, dk}, T, {hq, hk}, dh, dtype,
+               rope, {nullptr, nullptr}, 0.0f, -1.0f, {nullptr, nullptr}, nullptr, 0, vec, st);
+  }
+  if ((rc = check_heads(q, hq, T, es, &vec)) || (rc = check_heads(k, hk, T, es, &vec))) return rc;
+  if (!std::isfinite(eps) || eps < 0.0f) return ADALN_ERR_ARG;
+  if (!aligned_to(wq, es) || !aligned_to(wk, es) || !aligned_to(dwq, 4) || !aligned_to(dwk, 4))
+    return ADALN_ERR_ALIGN;
+  if (!aligned_to(wq, 16) || !aligned_to(wk, 16)) vec = false;
+  if ((dwq || dwk) && !workspace) return ADALN_ERR_NULL;
+  if (!aligned_to(workspace, 16)) return ADALN_ERR_ALIGN;
+  if (T == 0 && !dwq && !dwk) return ADALN_OK;
+  return run(kNormBwd, {q, k}, {dq_out, dk_out}, {dq, dk}, T, {hq, hk}, dh, dtype, rope, {wq, wk},
+             eps, -1.0f, {dwq, dwk}, workspace, workspace_bytes, vec, st);
+}
+
+}  // extern "C"

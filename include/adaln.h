@@ -78,6 +78,9 @@ extern "C" {
 #define ADALN_MAX_D_BF16 8192
 #define ADALN_MAX_D_F32 4096
 #define ADALN_MAX_NSEG (1 << 24)
+#define ADALN_MAX_HEADS 4096
+#define ADALN_MAX_HEAD_DIM 512
+#define ADALN_MAX_ROPE_AXES 4
 
 typedef enum {
   ADALN_F32 = 0,  /* IEEE binary32 */
@@ -94,13 +97,15 @@ typedef enum {
   ADALN_ERR_WORKSPACE = 6, /* workspace smaller than required */
   ADALN_ERR_CUDA = 7,      /* a CUDA runtime call or launch failed */
   ADALN_ERR_ARG = 8,       /* eps negative or not finite; bad trace argument */
-  ADALN_ERR_TIMEOUT = 9    /* device status: an internal pipeline wait gave up */
+  ADALN_ERR_TIMEOUT = 9,   /* device status: an internal pipeline wait gave up */
+  ADALN_ERR_POS = 10       /* device status: a rotary position outside the table */
 } adaln_status_t;
 
 /* Bits of the device status word (adaln_get_status). */
 #define ADALN_DEV_SEG_RANGE 1u   /* a seg_id was outside [0, nseg) */
 #define ADALN_DEV_SEG_ORDER 2u   /* seg_id decreased from one row to the next */
 #define ADALN_DEV_TIMEOUT 4u     /* a bounded wait on a copy pipeline expired */
+#define ADALN_DEV_POS_RANGE 8u   /* a rotary position was outside [-1, rows) */
 
 /*
  * Forward (section 2.B, forward pass): per-row statistics reduced on chip and
@@ -212,10 +217,86 @@ ADALN_API int adaln_fwd_bwd_host(const void* x, const void* dy, const void* shif
               int64_t chunk_rows, void* scratch, size_t scratch_bytes, void* stream);
 
 /*
+ * Queries and keys of the attention that a DiT block runs on modulated
+ * tokens: rotary positions over up to four axes (time, height, width, ...),
+ * with an optional RMS norm of every head in the same pass.  For one head x
+ * of token t, R = 2P rotated elements, pair p on axis a(p) (the axes own
+ * pairs[0], pairs[1], ... consecutive pairs, P in all), and
+ * (c, s) = table[pos[t, a(p)], p]:
+ *
+ *   n  = x * w / sqrt(mean(x^2) + eps)                (n = x when norm = 0)
+ *   y1 = n1 c - n2 s,   y2 = n2 c + n1 s              (y = n from element R on)
+ *
+ * where a pair's elements are (2p, 2p+1) (interleaved) or (p, p+P) (halves).
+ * A position of -1 leaves that axis's pairs of the token unrotated (text
+ * tokens of a joint stream).  A pair whose sine is zero takes nothing from
+ * its partner.  Arithmetic is fp32, each output rounded once.
+ */
+typedef struct {
+  void* ptr;            /* token 0, head 0, element 0 */
+  int64_t token_stride; /* elements from a token to the next, >= 0 */
+  int64_t head_stride;  /* elements from a head to the next, >= 0 */
+} adaln_heads_t;        /* [T, heads, dh]; a head's elements are contiguous */
+
+typedef struct {
+  const float* table;   /* device, fp32 [rows, P, 2]: cosine, sine; 8-byte aligned */
+  const int32_t* pos;   /* device, int32 [T, axes]: a row of the table, or -1 */
+  int32_t rows;         /* >= 1 */
+  int32_t axes;         /* 1 .. ADALN_MAX_ROPE_AXES */
+  int32_t pairs[ADALN_MAX_ROPE_AXES]; /* pairs of each axis; 1 <= P, 2P <= dh */
+  int32_t interleaved;  /* pairs of neighbours, else of the two halves */
+} adaln_rope_t;
+
+/*
+ * Forward, one launch.  q [T, hq, dh] and k [T, hk, dh] (hk or hq may be 0,
+ * its pointers NULL) may be views of a packed projection; q_out, k_out may be
+ * the inputs themselves (in place), but may not overlap them otherwise.
+ * wq, wk [dh] have the element type `dtype`; NULL means ones.  Head rows of
+ * whole 16-byte vectors at 16-byte aligned addresses (and at most 64 of them;
+ * for halves, P elements also a whole number of vectors) take a vector path,
+ * everything else a scalar one with the same results up to fp32 rounding.
+ * A position outside [-1, rows) is treated as -1 and recorded in the status
+ * word (ADALN_DEV_POS_RANGE).
+ *
+ * Errors: ADALN_ERR_DTYPE; ADALN_ERR_DIM for T < 0, dh outside
+ * [1, ADALN_MAX_HEAD_DIM], head counts outside [0, ADALN_MAX_HEADS] or both 0,
+ * axes, rows or pairs out of range, or a negative stride; ADALN_ERR_NULL;
+ * ADALN_ERR_ALIGN for a pointer below its element's alignment; ADALN_ERR_ARG
+ * for a bad eps (with norm).
+ */
+ADALN_API int adaln_qk_rope_fwd(const adaln_heads_t* q, const adaln_heads_t* k, int64_t T,
+              int32_t hq, int32_t hk, int32_t dh, adaln_dtype_t dtype,
+              const adaln_rope_t* rope, int32_t norm, const void* wq, const void* wk,
+              float eps, const adaln_heads_t* q_out, const adaln_heads_t* k_out,
+              void* stream);
+
+/*
+ * Backward.  Without norm: dq, dk are dq_out, dk_out turned back (one launch;
+ * q, k, workspace unused; dwq and dwk must be NULL).  With norm: also reads q
+ * and k, the forward's inputs (it saves nothing), and, where dwq / dwk are not
+ * NULL, writes the fp32 gradients [dh] of the weights, summed over tokens and
+ * heads in a fixed order (a second launch; bitwise reproducible for a given
+ * device and sizes).  dq, dk may be dq_out, dk_out or q, k themselves.
+ * `workspace` holds the partial sums: at least
+ * adaln_qk_rope_bwd_workspace_size bytes, 16-byte aligned, the caller's;
+ * needed only with dwq or dwk.  T = 0 zeroes dwq and dwk.
+ * Errors as for the forward; ADALN_ERR_WORKSPACE for a short workspace,
+ * ADALN_ERR_ARG for a dwq or dwk without norm.
+ */
+ADALN_API int adaln_qk_rope_bwd_workspace_size(int64_t T, int32_t hq, int32_t hk, int32_t dh,
+              adaln_dtype_t dtype, size_t* bytes);
+ADALN_API int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t* dk_out,
+              const adaln_heads_t* q, const adaln_heads_t* k, int64_t T, int32_t hq,
+              int32_t hk, int32_t dh, adaln_dtype_t dtype, const adaln_rope_t* rope,
+              int32_t norm, const void* wq, const void* wk, float eps,
+              const adaln_heads_t* dq, const adaln_heads_t* dk, float* dwq, float* dwk,
+              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the status word: the one the
  * calling thread bound (adaln_status_bind), else the current device's.
  * *host_bits (if non-NULL) receives the ADALN_DEV_* bits.  Returns ADALN_OK,
- * ADALN_ERR_SEG, ADALN_ERR_TIMEOUT or ADALN_ERR_CUDA.  The device's word is
+ * ADALN_ERR_SEG, ADALN_ERR_POS, ADALN_ERR_TIMEOUT or ADALN_ERR_CUDA.  The device's word is
  * shared by all calls on the device that use it since it was last cleared.
  */
 ADALN_API int adaln_get_status(uint32_t* host_bits, void* stream);
@@ -244,12 +325,14 @@ ADALN_API const char* adaln_strerror(int code);
  * thread) is bracketed by a pair of CUDA events recorded on its stream, up to
  * `capacity` launches.  adaln_trace_end() synchronises those events and sums
  * the elapsed time per kernel; adaln_trace_get() reads the sums.
- * Kernel ids: ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE.
+ * Kernel ids: ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE;
+ * ADALN_KERNEL_QK_ROPE counts every launch of the rotary calls.
  */
 #define ADALN_KERNEL_FWD 0
 #define ADALN_KERNEL_BWD_ROWS 1
 #define ADALN_KERNEL_BWD_FINALIZE 2
-#define ADALN_NUM_KERNELS 3
+#define ADALN_KERNEL_QK_ROPE 3
+#define ADALN_NUM_KERNELS 4
 ADALN_API int adaln_trace_begin(int capacity);
 ADALN_API int adaln_trace_end(void);
 ADALN_API int adaln_trace_get(int kernel_id, int64_t* launches, double* total_ms);

@@ -1,0 +1,86 @@
+"""Host-side argument checks of the rotary entry points: refused before any
+CUDA call (no GPU is touched; addresses are never dereferenced)."""
+import ctypes
+
+import pytest
+
+A, B, ODD = 0x10000, 0x20000, 0x10001
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from adaln_video_dit_gb300 import build
+    build.build()
+    from adaln_video_dit_gb300 import _lib
+    return _lib
+
+
+def rope_of(lib, **kw):
+    a = dict(table=A, pos=B, rows=9, axes=3, pairs=(22, 21, 21, 0), interleaved=1)
+    a.update(kw)
+    a["pairs"] = (ctypes.c_int32 * 4)(*a["pairs"])
+    return lib.Rope(*a.values())
+
+
+def rope_fwd(lib, rope=None, **kw):
+    h = lib.Heads(A, 1024, 128)
+    a = dict(q=h, k=h, T=10, hq=8, hk=2, dh=128, dt=lib.ADALN_BF16, rope=rope or rope_of(lib),
+             norm=1, wq=A, wk=A, eps=1e-6, qo=h, ko=h)
+    a.update(kw)
+    return lib.raw.adaln_qk_rope_fwd(*a.values(), None)
+
+
+def rope_bwd(lib, rope=None, **kw):
+    h = lib.Heads(A, 1024, 128)
+    a = dict(dqo=h, dko=h, q=h, k=h, T=10, hq=8, hk=2, dh=128, dt=lib.ADALN_BF16,
+             rope=rope or rope_of(lib), norm=1, wq=A, wk=A, eps=1e-6, dq=h, dk=h, dwq=A, dwk=A,
+             ws=B, wsb=1 << 30)
+    a.update(kw)
+    return lib.raw.adaln_qk_rope_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [rope_fwd, rope_bwd])
+def test_rope_refusals(lib, call):
+    H = lib.Heads
+    assert call(lib, dt=2) == lib.ADALN_ERR_DTYPE
+    for bad in (dict(T=-1), dict(T=2 ** 31), dict(dh=0), dict(dh=513), dict(hq=-1),
+                dict(hq=4097), dict(hq=0, hk=0), dict(dh=126), dict(q=H(A, -8, 128))):
+        assert call(lib, **bad) == lib.ADALN_ERR_DIM, bad
+    for bad in (dict(axes=0), dict(axes=5), dict(rows=0), dict(pairs=(65, -1, 0, 0)),
+                dict(pairs=(0, 0, 0, 0)), dict(pairs=(2 ** 31 - 1,) * 3 + (0,))):
+        assert call(lib, rope=rope_of(lib, **bad)) == lib.ADALN_ERR_DIM, bad
+    for bad in (dict(q=None), dict(k=None), dict(q=H(None, 1024, 128))):
+        assert call(lib, **bad) == lib.ADALN_ERR_NULL, bad
+    for bad in (dict(table=None), dict(pos=None)):
+        assert call(lib, rope=rope_of(lib, **bad)) == lib.ADALN_ERR_NULL
+    for bad in (dict(q=H(ODD, 1024, 128)), dict(wk=ODD), dict(k=H(A + 2, 1024, 128),
+                                                                dt=lib.ADALN_F32)):
+        assert call(lib, **bad) == lib.ADALN_ERR_ALIGN, bad
+    assert call(lib, rope=rope_of(lib, table=A + 4)) == lib.ADALN_ERR_ALIGN
+    assert call(lib, rope=rope_of(lib, pos=A + 2)) == lib.ADALN_ERR_ALIGN
+    for eps in (-1e-6, float("nan"), float("inf")):
+        assert call(lib, eps=eps) == lib.ADALN_ERR_ARG
+
+
+def test_rope_only_what_is_missing_is_refused(lib):
+    none = lib.Heads(None, 0, 0)
+    rope = rope_of(lib, table=None, pos=None)
+    assert rope_fwd(lib, rope=rope, T=0, q=none, k=none, qo=none, ko=none) == lib.ADALN_OK
+    assert rope_fwd(lib, T=0, hk=0, k=None, ko=None) == lib.ADALN_OK
+    assert rope_bwd(lib, norm=0, q=None, k=None) == lib.ADALN_ERR_ARG  # no weights, no gradients
+    assert rope_bwd(lib, norm=0, T=0, q=None, k=None, dwq=None, dwk=None, ws=None) == lib.ADALN_OK
+    assert rope_bwd(lib, ws=None) == lib.ADALN_ERR_NULL
+    assert rope_bwd(lib, ws=A + 8) == lib.ADALN_ERR_ALIGN
+    assert rope_bwd(lib, dwk=A + 2) == lib.ADALN_ERR_ALIGN
+    n = lib.raw.adaln_qk_rope_bwd_workspace_size
+    assert n(1, 1, 1, 0, 0, None) == lib.ADALN_ERR_DIM
+    assert n(1, 1, 1, 8, 0, None) == lib.ADALN_ERR_NULL
+
+
+def test_rope_binding_rejects_host_tensors(lib):
+    import torch
+    x = torch.zeros(4, 2, 8)
+    with pytest.raises(ValueError):
+        lib.adaln_qk_rope_fwd(x, None, torch.zeros(3, 4, 2), torch.zeros(4, 1, dtype=torch.int32),
+                              (4,))
+    assert lib.strerror(lib.ADALN_ERR_POS) != lib.strerror(12345)
