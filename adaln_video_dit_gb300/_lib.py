@@ -19,7 +19,8 @@ ADALN_F32, ADALN_BF16 = 0, 1
  ADALN_ERR_TIMEOUT, ADALN_ERR_POS) = range(11)
 ADALN_DEV_SEG_RANGE, ADALN_DEV_SEG_ORDER, ADALN_DEV_TIMEOUT, ADALN_DEV_POS_RANGE = 1, 2, 4, 8
 ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE = 0, 1, 2
-ADALN_KERNEL_QK_ROPE = 3
+ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN = 3, 4
+ACTS = {"silu": 0, "gelu_tanh": 1, "gelu": 2}
 KERNEL_NAMES = {0: "adaln_fwd_kernel", 1: "adaln_bwd_rows_kernel",
                 2: "adaln_bwd_finalize_kernel"}
 MAX_HEADS, MAX_HEAD_DIM, MAX_ROPE_AXES = 4096, 512, 4
@@ -31,7 +32,8 @@ EXPORTS = ["adaln_fwd", "adaln_bwd_workspace_size", "adaln_bwd", "adaln_bwd_noal
            "adaln_trace_end", "adaln_trace_get", "adaln_launch_shape",
            "adaln_selftest_wait_timeout", "adaln_fwd_bwd_host_scratch_size",
            "adaln_fwd_bwd_host", "adaln_qk_rope_fwd", "adaln_qk_rope_bwd_workspace_size",
-           "adaln_qk_rope_bwd"]
+           "adaln_qk_rope_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size",
+           "adaln_ffn_fwd", "adaln_ffn_bwd"]
 
 
 class AdalnError(RuntimeError):
@@ -99,6 +101,17 @@ def _load():
     lib.adaln_qk_rope_bwd.restype = ci
     lib.adaln_qk_rope_bwd.argtypes = [hp, hp, hp, hp, i64, i32, i32, i32, ci, rp, i32, vp, vp,
                                       f32, hp, hp, vp, vp, vp, ctypes.c_size_t, vp]
+    sp = ctypes.POINTER(ctypes.c_size_t)
+    lib.adaln_ffn_saved_size.restype = ci
+    lib.adaln_ffn_saved_size.argtypes = [i64, i32, i32, ci, sp]
+    lib.adaln_ffn_workspace_size.restype = ci
+    lib.adaln_ffn_workspace_size.argtypes = [i64, i32, i32, ci, sp, sp]
+    lib.adaln_ffn_fwd.restype = ci
+    lib.adaln_ffn_fwd.argtypes = [vp, vp, vp, vp, i64, i32, i32, ci, ci, vp, vp, vp,
+                                  ctypes.c_size_t, vp]
+    lib.adaln_ffn_bwd.restype = ci
+    lib.adaln_ffn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, ci, ci, vp, vp, vp, vp,
+                                  vp, ctypes.c_size_t, vp]
     lib.adaln_selftest_wait_timeout.restype = ci
     lib.adaln_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     lib.adaln_launch_shape.restype = ci
@@ -416,6 +429,96 @@ def adaln_qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved=True, 
                                _stream_ptr(stream, dev))
     _check(rc, "adaln_qk_rope_bwd")
     return dq, dk, dwq, dwk
+
+
+def adaln_ffn_saved_size(T, D, F, dtype=torch.bfloat16):
+    """Bytes that adaln_ffn_fwd saves for adaln_ffn_bwd."""
+    n = ctypes.c_size_t(0)
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    _check(raw.adaln_ffn_saved_size(int(T), int(D), int(F), code, ctypes.byref(n)),
+           "adaln_ffn_saved_size")
+    return n.value
+
+
+def adaln_ffn_workspace_size(T, D, F, dtype=torch.bfloat16):
+    """Workspace bytes of (adaln_ffn_fwd, adaln_ffn_bwd) on the current device."""
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    _check(raw.adaln_ffn_workspace_size(int(T), int(D), int(F), code, ctypes.byref(f),
+                                        ctypes.byref(b)), "adaln_ffn_workspace_size")
+    return f.value, b.value
+
+
+def _act(act):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _ffn_args(x, wg, wu, wd):
+    T, D = x.shape
+    F = wg.shape[0]
+    _dev(x, "x")
+    _dev(wg, "wg", x.dtype, (F, D))
+    _dev(wu, "wu", x.dtype, (F, D))
+    _dev(wd, "wd", x.dtype, (D, F))
+    return T, D, F
+
+
+def _bytes(t, n, name, device):
+    """A uint8 CUDA buffer of at least n bytes (allocated when not given)."""
+    if t is None:
+        return torch.empty(max(16, n), device=device, dtype=torch.uint8)
+    return _dev(t, name, torch.uint8)
+
+
+def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, workspace=None,
+                  stream=None):
+    """y = (act(x wg') * (x wu')) wd' for bf16 x [T, D], wg, wu [F, D], wd [D, F];
+    act "silu", "gelu_tanh" or "gelu".  With `save` (or a `saved` buffer of
+    adaln_ffn_saved_size bytes) also keeps what adaln_ffn_bwd needs.
+    Returns (y, saved), saved None without."""
+    T, D, F = _ffn_args(x, wg, wu, wd)
+    code, dt = _act(act), dtype_code(x.dtype)
+    y = torch.empty_like(x) if y is None else _dev(y, "y", x.dtype, (T, D))
+    if save or saved is not None:
+        need = adaln_ffn_saved_size(T, D, F, dt)
+        saved = _bytes(saved, need, "saved", x.device)
+        if saved.numel() < need:
+            raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
+    if workspace is None:
+        workspace = _bytes(None, adaln_ffn_workspace_size(T, D, F, dt)[0], "workspace", x.device)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = raw.adaln_ffn_fwd(_ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), T, D, F, dt, code, _ptr(y),
+                           _ptr(saved), _ptr(workspace), workspace.numel(),
+                           _stream_ptr(stream, x.device))
+    _check(rc, "adaln_ffn_fwd")
+    return y, saved
+
+
+def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=None, dwd=None,
+                  workspace=None, stream=None):
+    """Backward of adaln_ffn_fwd, from its inputs and what it saved.  Returns
+    (dx, dwg, dwu, dwd), all bf16."""
+    T, D, F = _ffn_args(x, wg, wu, wd)
+    code, dt = _act(act), dtype_code(x.dtype)
+    _dev(dy, "dy", x.dtype, (T, D))
+    need = adaln_ffn_saved_size(T, D, F, dt)
+    _dev(saved, "saved", torch.uint8)
+    if saved.numel() < need:
+        raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
+    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", x.dtype, (T, D))
+    dwg = torch.empty_like(wg) if dwg is None else _dev(dwg, "dwg", x.dtype, (F, D))
+    dwu = torch.empty_like(wu) if dwu is None else _dev(dwu, "dwu", x.dtype, (F, D))
+    dwd = torch.empty_like(wd) if dwd is None else _dev(dwd, "dwd", x.dtype, (D, F))
+    if workspace is None:
+        workspace = _bytes(None, adaln_ffn_workspace_size(T, D, F, dt)[1], "workspace", x.device)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = raw.adaln_ffn_bwd(_ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), _ptr(saved), T, D, F,
+                           dt, code, _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), _ptr(workspace),
+                           workspace.numel(), _stream_ptr(stream, x.device))
+    _check(rc, "adaln_ffn_bwd")
+    return dx, dwg, dwu, dwd
 
 
 def adaln_get_status(stream=None, device=None):

@@ -144,6 +144,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 // last microseconds; the bound only turns an internal error into a status
 // bit and an orderly exit instead of a hang.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// Upper bound on the waits for copies in flight after a wait has given up.
+constexpr uint64_t kDrainLimitNs = 100000000ull;
 
 // As mbar_try_wait, but the thread may be suspended (instead of spinning)
 // until the phase completes or about `hint_ns` nanoseconds have passed.
@@ -206,6 +208,13 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy() {
 
 __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// Programmatic dependent launch: wait for the stream's previous kernel (before
+// any access to global memory), and let the next one be scheduled.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,865 @@
+// Gated feed-forward block on the tensor cores, forward and backward.
+//
+//   g = x Wg',  u = x Wu',  h = act(g) * u,  y = h Wd'
+//   dh = dy Wd, dg = dh * u * act'(g), du = dh * act(g)
+//   dx = dg Wg + du Wu,  dWg = dg' x,  dWu = du' x,  dWd = dy' h
+//
+// with x, y, dy, dx [T, D]; Wg, Wu [F, D]; Wd [D, F], all bf16 and row-major
+// (so an operand is either K-major or MN-major in memory, and the matrix
+// instructions take both: nothing is transposed).  Sums are fp32 in tensor
+// memory.  The forward needs 6 T D F operations, the backward 12 T D F.
+//
+// Two kernels make the forward: both projections with the activation and the
+// product in their epilogue (g and u meet in one tile: the even CTA of a pair
+// stages rows of Wg, the odd one rows of Wu, so an accumulator holds 128
+// columns of g and the same 128 of u), then the product with Wd.  The backward
+// makes dh with the gate's gradient in its epilogue, then dx and the three
+// weight gradients in one launch.
+//
+// Roundings to bf16: h, dg and du, once each, because the matrix instructions
+// take 16-bit operands; and the outputs.  g and u themselves are kept for the
+// backward as fp32 cut to 24 bits (16 bits of one array and the next 8 of
+// another: 2^-15 relative), not as bf16: with 8 bits of mantissa their rounding
+// would enter dg, du and h beside those arrays' own.
+//
+// A kernel is persistent, one CTA pair per two SMs: a 256 x 256 tile a pair, k
+// steps of 64 through a ring of TMA-filled stages; per CTA one producer warp,
+// one issuing warp (even CTA) and eight epilogue warps, two accumulators in
+// tensor memory so that a tile's epilogue runs under the next tile's products.
+#include <cmath>
+#include <mutex>
+
+#include "internal.h"
+#include "tc.cuh"
+
+namespace adaln {
+namespace {
+
+enum { kPlain = 0, kGate = 1, kGateBwd = 2 };
+
+constexpr int kStages = 6;
+constexpr int kBK = 64;                    // k values of a stage
+constexpr int kTileBytes = 128 * kBK * 2;  // one CTA's share of an operand stage
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr int kTM = 256, kTN = 256;        // tile of a CTA pair
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kGroupM = 8;                 // tile rows walked together (L2 reuse)
+constexpr int kMaxProblems = 4;
+
+struct Problem {       // C[M, N] = sum over its K segments of A B
+  CUtensorMap a[2], b[2];
+  void* out;           // bf16 [M, N]
+  float* partial;      // fp32 [splits][M][N] when splits > 1
+  int M, N;
+  int kb0, kb;         // k blocks of segment 0, of both
+  int tiles_m, tiles_n, splits;
+  int first;           // first unit of the problem
+  int a_mn, b_mn;      // operand layouts
+};
+
+struct GemmArgs {
+  Problem p[kMaxProblems];
+  int problems, units;
+  // Gate epilogues ([T, F] each).
+  __nv_bfloat16 *h, *dg, *du;
+  uint16_t *g_hi, *u_hi;  // saved pre-activations: upper 16 bits, next 8
+  uint8_t *g_lo, *u_lo;
+  unsigned* status;
+};
+
+struct Unit {
+  const Problem* p;
+  int m, n;        // tile
+  int k0, k1;      // k blocks
+  int split;
+};
+
+__device__ __forceinline__ Unit unit_of(const GemmArgs& a, int u) {
+  int i = 0;
+  while (i + 1 < a.problems && u >= a.p[i + 1].first) ++i;
+  Unit r;
+  r.p = &a.p[i];
+  u -= r.p->first;
+  r.split = u % r.p->splits;
+  const int tile = u / r.p->splits;
+  const int per_group = kGroupM * r.p->tiles_n;
+  const int m0 = tile / per_group * kGroupM;
+  const int rows = min(kGroupM, r.p->tiles_m - m0);
+  const int in = tile % per_group;
+  r.m = m0 + in % rows;
+  r.n = in / rows;
+  r.k0 = (int)((int64_t)r.p->kb * r.split / r.p->splits);
+  r.k1 = (int)((int64_t)r.p->kb * (r.split + 1) / r.p->splits);
+  return r;
+}
+
+// ----- activations --------------------------------------------------------------
+// p such that act(g) = g p, and act'(g).  The sigmoid form of the tanh
+// approximation (0.5 (1 + tanh z) = 1 / (1 + exp(-2 z))) keeps its relative
+// accuracy for negative g.  The fast exponential and division are good to a
+// few fp32 units, far below the bf16 rounding that follows.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ void gate(float g, float& p, float& d) {
+  if (ACT == ADALN_ACT_SILU) {
+    p = sigmoid(g);
+    d = p * (1.0f + g * (1.0f - p));
+  } else if (ACT == ADALN_ACT_GELU_TANH) {
+    const float k = 0.7978845608028654f, c = 0.044715f;
+    const float g2 = g * g;
+    p = sigmoid(2.0f * k * g * (1.0f + c * g2));
+    const float q = p * (1.0f - p);
+    d = q > 0.0f ? p + 2.0f * k * g * q * (1.0f + 3.0f * c * g2) : p;
+  } else {
+    p = 0.5f * erfcf(-0.7071067811865476f * g);
+    d = p + g * 0.3989422804014327f * __expf(-0.5f * g * g);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// 32 consecutive bf16 values of a row, those below column `n` (n a multiple
+// of 8 from the row's start; `left` = n minus the first column).
+__device__ __forceinline__ void store_row32(void* p, const uint32_t (&w)[16], int left) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (8 * i < left)
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// Save 32 fp32 values of a row as their upper 16 bits and their next 8.
+__device__ __forceinline__ void save_row32(uint16_t* hi, uint8_t* lo, const uint32_t (&v)[32],
+                                           int left) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = __byte_perm(v[2 * i], v[2 * i + 1], 0x7632);
+  store_row32(hi, w, left);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (8 * i < left) {
+      const uint32_t a = __byte_perm(v[8 * i], v[8 * i + 1], 0x51),
+                     b = __byte_perm(v[8 * i + 2], v[8 * i + 3], 0x51),
+                     c = __byte_perm(v[8 * i + 4], v[8 * i + 5], 0x51),
+                     d = __byte_perm(v[8 * i + 6], v[8 * i + 7], 0x51);
+      reinterpret_cast<uint2*>(lo)[i] =
+          make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410));
+    }
+  }
+}
+
+// The 8 values saved at (hi, lo).
+__device__ __forceinline__ void load_saved8(const uint4& h, const uint2& l, float (&f)[8]) {
+  const uint32_t w[4] = {h.x, h.y, h.z, h.w}, b[2] = {l.x, l.y};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t lo = (b[i / 4] >> (8 * (i % 4))) & 0xff;
+    const uint32_t up = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffff;
+    f[i] = __uint_as_float(up << 16 | lo << 8);
+  }
+}
+
+// ----- epilogues: one warp's 32 rows x half of the tile's columns -----------------
+// `row` is this lane's row of the output, `half` the column half.
+
+__device__ __forceinline__ void epilogue_plain(const Unit& u, uint32_t acc, int row, int half) {
+  const Problem& p = *u.p;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int col = u.n * kTN + half * 128 + c * 32;
+    if (col >= p.N) break;
+    __syncwarp();
+    uint32_t r[32];
+    tmem_ld32(acc + half * 128 + c * 32, r);
+    tc_wait_ld();
+    const int left = row < p.M ? p.N - col : 0;  // columns of this row to write
+    if (p.splits > 1) {
+      float4* o = reinterpret_cast<float4*>(p.partial + ((int64_t)u.split * p.M + row) * p.N + col);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (4 * i < left)
+          o[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                             __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      store_row32(static_cast<__nv_bfloat16*>(p.out) + (int64_t)row * p.N + col, w, left);
+    }
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Unit& u, uint32_t acc,
+                                              int row, int half) {
+  const Problem& p = *u.p;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int col = u.n * 128 + half * 64 + c * 32;
+    if (col >= p.N) break;
+    __syncwarp();
+    uint32_t g[32], v[32];
+    tmem_ld32(acc + half * 64 + c * 32, g);
+    tmem_ld32(acc + 128 + half * 64 + c * 32, v);
+    tc_wait_ld();
+    const int left = row < p.M ? p.N - col : 0;
+    const int64_t at = (int64_t)row * p.N + col;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float h[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float x = __uint_as_float(g[2 * i + j]);
+        float s, d;
+        gate<ACT>(x, s, d);
+        h[j] = x * s * __uint_as_float(v[2 * i + j]);
+      }
+      w[i] = pack_bf16(h[0], h[1]);
+    }
+    store_row32(a.h + at, w, left);
+    if (a.g_hi != nullptr) {
+      save_row32(a.g_hi + at, a.g_lo + at, g, left);
+      save_row32(a.u_hi + at, a.u_lo + at, v, left);
+    }
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void epilogue_gate_bwd(const GemmArgs& a, const Unit& u, uint32_t acc,
+                                                  int row, int half) {
+  const Problem& p = *u.p;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int col = u.n * kTN + half * 128 + c * 32;
+    if (col >= p.N) break;
+    __syncwarp();
+    const int64_t at = (int64_t)row * p.N + col;
+    const int left = row < p.M ? p.N - col : 0;
+    uint4 gh[4], uh[4];
+    uint2 gl[4], ul[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = 8 * i < left;
+      gh[i] = in ? reinterpret_cast<const uint4*>(a.g_hi + at)[i] : make_uint4(0, 0, 0, 0);
+      uh[i] = in ? reinterpret_cast<const uint4*>(a.u_hi + at)[i] : make_uint4(0, 0, 0, 0);
+      gl[i] = in ? reinterpret_cast<const uint2*>(a.g_lo + at)[i] : make_uint2(0, 0);
+      ul[i] = in ? reinterpret_cast<const uint2*>(a.u_lo + at)[i] : make_uint2(0, 0);
+    }
+    uint32_t r[32];
+    tmem_ld32(acc + half * 128 + c * 32, r);
+    tc_wait_ld();
+    uint32_t wg[16], wu[16], wh[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float g[8], v[8];
+      load_saved8(gh[i], gl[i], g);
+      load_saved8(uh[i], ul[i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float dg[2], du[2], h[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = g[2 * j + e], w = v[2 * j + e], dh = __uint_as_float(r[8 * i + 2 * j + e]);
+          float s, d;
+          gate<ACT>(x, s, d);
+          dg[e] = dh * w * d;
+          du[e] = dh * (x * s);
+          h[e] = x * s * w;
+        }
+        wg[4 * i + j] = pack_bf16(dg[0], dg[1]);
+        wu[4 * i + j] = pack_bf16(du[0], du[1]);
+        wh[4 * i + j] = pack_bf16(h[0], h[1]);
+      }
+    }
+    store_row32(a.dg + at, wg, left);
+    store_row32(a.du + at, wu, left);
+    store_row32(a.h + at, wh, left);
+  }
+}
+
+template <int KIND, int ACT>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ GemmArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t bars = ring + kStages * kStageBytes;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+  auto acc_full = [&](int i) { return bars + 8 * (2 * kStages + i); };
+  auto acc_empty = [&](int i) { return bars + 8 * (2 * kStages + 2 + i); };
+  const uint32_t drain = bars + 8 * (2 * kStages + 4);
+  const uint32_t tmem_ptr = bars + 8 * (2 * kStages + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(
+      smem_raw + (bars - smem_addr(smem_raw)) + 8 * (2 * kStages + 6));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full(i), 1);
+      mbar_init(acc_empty(i), 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 2) tmem_alloc<2>(tmem_ptr, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_ptr) : "memory");
+
+  grid_wait();
+  grid_launch_dependents();
+
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (mbar_wait_bounded(bar, parity, abort_flag)) return true;
+    *abort_flag = 1;
+    atomicOr(a.status, ADALN_DEV_TIMEOUT);
+    return false;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // Producer: this CTA's 128 rows of A and of B, a stage at a time.
+    int s = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int ui = cluster; ok && ui < a.units; ui += clusters) {
+      const Unit u = unit_of(a, ui);
+      const Problem& p = *u.p;
+      const int m = u.m * kTM + (int)rank * 128;
+      const int n = KIND == kGate ? u.n * 128 : u.n * kTN + (int)rank * 128;
+      for (int kb = u.k0; kb < u.k1; ++kb) {
+        if (!wait(empty(s), parity ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+        const int seg = kb >= p.kb0;
+        const int k = (kb - (seg ? p.kb0 : 0)) * kBK;
+        const CUtensorMap* ma = &p.a[seg];
+        const CUtensorMap* mb = &p.b[KIND == kGate ? (int)rank : seg];
+        const uint32_t da = ring + s * kStageBytes, db = da + kTileBytes;
+        if (p.a_mn) {
+          tma_load_pair(da, ma, m, k, full(s));
+          tma_load_pair(da + kTileBytes / 2, ma, m + 64, k, full(s));
+        } else {
+          tma_load_pair(da, ma, k, m, full(s));
+        }
+        if (p.b_mn) {
+          tma_load_pair(db, mb, n, k, full(s));
+          tma_load_pair(db + kTileBytes / 2, mb, n + 64, k, full(s));
+        } else {
+          tma_load_pair(db, mb, k, n, full(s));
+        }
+        if (++s == kStages) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+    }
+    if (!ok) {
+      // Copies may be in flight into this CTA: let them land before it can
+      // exit.  The last phase armed of each stage, waited for with a limit.
+      for (int i = 0; i < kStages; ++i)
+        mbar_wait_bounded(full(i), i < s ? parity : parity ^ 1, nullptr, kDrainLimitNs);
+    }
+  } else if (warp == 1 && rank == 0 && lane == 0) {
+    // Issuer of the pair's matrix instructions.
+    int s = 0, acc = 0;
+    uint32_t parity = 0, acc_parity = 0;
+    bool ok = true;
+    for (int ui = cluster; ok && ui < a.units; ui += clusters) {
+      const Unit u = unit_of(a, ui);
+      const bool a_mn = u.p->a_mn, b_mn = u.p->b_mn;
+      const uint32_t idesc = instr_desc(kTM, kTN, a_mn, b_mn);
+      const uint32_t step_a = k_step_bytes(a_mn) >> 4, step_b = k_step_bytes(b_mn) >> 4;
+      if (!(ok = wait(acc_empty(acc), acc_parity ^ 1))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * kTN;
+      for (int kb = u.k0; kb < u.k1; ++kb) {
+        if (!(ok = wait(full(s), parity))) break;
+        tc_fence_after();
+        const uint64_t da = smem_desc(ring + s * kStageBytes, a_mn, kTileBytes / 2);
+        const uint64_t db = smem_desc(ring + s * kStageBytes + kTileBytes, b_mn, kTileBytes / 2);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          tc_mma<2>(d, da + k * step_a, db + k * step_b, idesc, kb > u.k0 || k > 0);
+        tc_commit<2>(empty(s));
+        if (++s == kStages) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+      if (!ok) break;
+      tc_commit<2>(acc_full(acc));
+      acc ^= 1;
+      if (acc == 0) acc_parity ^= 1;
+    }
+    if (!ok) {  // matrix instructions may be in flight: wait for them, with a limit
+      tc_commit<2>(drain);
+      mbar_wait_bounded(drain, 0, nullptr, kDrainLimitNs);
+    }
+  } else if (warp >= 2) {
+    // Epilogue.  A warp reads the 32 lanes of tensor memory of its quarter.
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    int acc = 0;
+    uint32_t acc_parity = 0;
+    for (int ui = cluster; ui < a.units; ui += clusters) {
+      const Unit u = unit_of(a, ui);
+      if (!__all_sync(~0u, wait(acc_full(acc), acc_parity))) break;
+      tc_fence_after();
+      const int row = u.m * kTM + (int)rank * 128 + quarter * 32 + lane;
+      const uint32_t at = tmem + acc * kTN + ((uint32_t)(quarter * 32) << 16);
+      if (KIND == kPlain)
+        epilogue_plain(u, at, row, half);
+      else if (KIND == kGate)
+        epilogue_gate<ACT>(a, u, at, row, half);
+      else
+        epilogue_gate_bwd<ACT>(a, u, at, row, half);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty(acc), 0));
+      acc ^= 1;
+      if (acc == 0) acc_parity ^= 1;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  // The pair's copies, commits and arrivals reach both CTAs: neither leaves
+  // before the other is done.
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) tmem_free<2>(tmem, 512);
+}
+
+// out = the sum of the split partials, in split order, rounded to bf16.
+__global__ void __launch_bounds__(256) ffn_join_kernel(const float* partial, int splits,
+                                                       int64_t vecs, __nv_bfloat16* out) {
+  grid_wait();
+  grid_launch_dependents();
+  const float4* p = reinterpret_cast<const float4*>(partial);
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < vecs; i += gridDim.x * 256ll) {
+    float4 s = p[i];
+    for (int k = 1; k < splits; ++k) {
+      const float4 v = p[i + k * vecs];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+  }
+}
+
+// ----- host side ------------------------------------------------------------------
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeFn* out) {
+  static std::mutex mu;
+  static EncodeFn fn = nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                           cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+    fn = reinterpret_cast<EncodeFn>(p);
+  }
+  *out = fn;
+  return cudaSuccess;
+}
+
+// Tensor map of a row-major bf16 matrix [rows, cols], read in boxes of 64
+// columns (128 bytes, swizzled) x box_rows.  What lies outside reads as zero.
+cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows) {
+  EncodeFn fn;
+  const cudaError_t e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides,
+                        box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Operand of a product: a row-major matrix whose rows run along k (K-major)
+// or along m or n (MN-major).
+struct Operand {
+  const void* p;
+  int64_t rows, cols;
+  bool mn;
+};
+cudaError_t operand_map(CUtensorMap* m, const Operand& o) {
+  return make_map(m, o.p, o.rows, o.cols, o.mn ? kBK : 128);
+}
+
+template <int KIND>
+void* gemm_kernel(int act) {
+  if constexpr (KIND == kPlain) return (void*)ffn_gemm_kernel<kPlain, 0>;
+  else switch (act) {
+    case ADALN_ACT_SILU: return (void*)ffn_gemm_kernel<KIND, ADALN_ACT_SILU>;
+    case ADALN_ACT_GELU_TANH: return (void*)ffn_gemm_kernel<KIND, ADALN_ACT_GELU_TANH>;
+    default: return (void*)ffn_gemm_kernel<KIND, ADALN_ACT_GELU>;
+  }
+}
+void* kernel_of(int kind, int act) {
+  return kind == kPlain ? gemm_kernel<kPlain>(act)
+         : kind == kGate ? gemm_kernel<kGate>(act) : gemm_kernel<kGateBwd>(act);
+}
+
+cudaError_t launch_cluster(void* kernel, int grid, int threads, int smem, int cluster, void** params,
+                           cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, kernel, params);
+}
+
+// CTA pairs that the device holds at once (one CTA an SM), after allowing the
+// kernels their shared memory on it.  Asked once per device.
+constexpr int kMaxDev = 64;
+cudaError_t pairs_of_device(int* pairs) {
+  static std::mutex mu;
+  static int known[kMaxDev] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!known[dev]) {
+    for (int kind = 0; kind < 3; ++kind)
+      for (int act = 0; act < 3; ++act) {
+        e = cudaFuncSetAttribute(kernel_of(kind, act), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmem);
+        if (e != cudaSuccess) return e;
+      }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel_of(kPlain, 0), &cfg);
+    if (e != cudaSuccess) return e;
+    known[dev] = n > 0 ? n : 1;
+  }
+  *pairs = known[dev];
+  return cudaSuccess;
+}
+
+int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// k splits of a product of `tiles` tiles and kb k blocks on `pairs` CTA pairs,
+// with `other` k blocks of work per pair beside it: the fewest rounds of k
+// blocks, a unit costing about 6 blocks of start and end.  A split costs its
+// fp32 partials written and read again, about 0.3 k blocks a unit.
+int choose_splits(int tiles, int kb, int pairs, int64_t other) {
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 32 && (s == 1 || kb / s >= 8); ++s) {
+    const double rounds = (double)div_up((int64_t)tiles * s, pairs);
+    double cost = rounds * (div_up(kb, s) + 6);
+    // Beside other work only the longest unit and the total matter.
+    if (other > 0) {
+      const double mean = (double)tiles * (kb + 6.0 * s) / pairs + (double)other;
+      cost = mean > 2.0 * (div_up(kb, s) + 6) ? mean : 2.0 * (div_up(kb, s) + 6);
+    }
+    if (s > 1) cost += 4 + 0.3 * s * tiles / pairs;
+    if (s == 1 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct Split {
+  int splits;
+  size_t bytes;  // of the fp32 partials
+};
+Split split_of(int64_t M, int N, int kb, int pairs, int64_t other) {
+  const int tiles = div_up(M, kTM) * div_up(N, kTN);
+  Split s;
+  s.splits = choose_splits(tiles, kb, pairs, other);
+  s.bytes = s.splits > 1 ? (size_t)s.splits * M * N * 4 : 0;
+  return s;
+}
+
+cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2], int segs, int64_t M,
+                        int N, int tn, int64_t k0, int64_t k1, void* out) {
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    const bool have_a = i < segs, have_b = b[i].p != nullptr;
+    e = operand_map(&p->a[i], have_a ? a[i] : a[0]);
+    if (e == cudaSuccess) e = operand_map(&p->b[i], have_b ? b[i] : b[0]);
+  }
+  p->out = out;
+  p->partial = nullptr;
+  p->M = (int)M;
+  p->N = N;
+  p->kb0 = div_up(k0, kBK);
+  p->kb = p->kb0 + (segs > 1 ? div_up(k1, kBK) : 0);
+  p->tiles_m = div_up(M, kTM);
+  p->tiles_n = div_up(N, tn);
+  p->splits = 1;
+  p->first = 0;
+  p->a_mn = a[0].mn;
+  p->b_mn = b[0].mn;
+  return e;
+}
+
+cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, cudaStream_t st) {
+  int at = 0;
+  for (int i = 0; i < a.problems; ++i) {
+    a.p[i].first = at;
+    at += a.p[i].tiles_m * a.p[i].tiles_n * a.p[i].splits;
+  }
+  a.units = at;
+  const int grid = 2 * (at < pairs ? at : pairs);
+  void* params[1] = {&a};
+  return traced_launch(ADALN_KERNEL_FFN, st, [&] {
+    return launch_cluster(kernel_of(kind, act), grid, kThreads, kSmem, 2, params, st);
+  });
+}
+
+cudaError_t launch_join(const Problem& p, cudaStream_t st) {
+  const float* partial = p.partial;
+  int splits = p.splits;
+  int64_t vecs = (int64_t)p.M * p.N / 4;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+  void* params[4] = {&partial, &splits, &vecs, &out};
+  const int64_t blocks = (vecs + 255) / 256;
+  const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
+  return traced_launch(ADALN_KERNEL_FFN, st, [&] {
+    return launch_cluster((void*)ffn_join_kernel, grid, 256, 0, 1, params, st);
+  });
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int check(int64_t T, int32_t D, int32_t F, adaln_dtype_t dt, int act) {
+  if (dt != ADALN_BF16) return ADALN_ERR_DTYPE;
+  if (T < 0 || T > ADALN_FFN_MAX_T) return ADALN_ERR_DIM;
+  if (D < 8 || D > ADALN_FFN_MAX_DIM || D % 8 != 0) return ADALN_ERR_DIM;
+  if (F < 8 || F > ADALN_FFN_MAX_DIM || F % 8 != 0) return ADALN_ERR_DIM;
+  if (act != ADALN_ACT_SILU && act != ADALN_ACT_GELU_TANH && act != ADALN_ACT_GELU)
+    return ADALN_ERR_ARG;
+  return ADALN_OK;
+}
+
+// The saved pre-activations: upper halves of g, of u, next bytes of g, of u.
+struct Saved {
+  size_t u_hi, g_lo, u_lo, bytes;
+};
+Saved saved_layout(int64_t T, int32_t F) {
+  const size_t n = (size_t)T * F;
+  Saved s;
+  s.u_hi = round256(2 * n);
+  s.g_lo = s.u_hi + round256(2 * n);
+  s.u_lo = s.g_lo + round256(n);
+  s.bytes = s.u_lo + round256(n);
+  return s;
+}
+
+struct FwdPlan {
+  Split y;
+  size_t bytes;
+};
+FwdPlan fwd_plan(int64_t T, int32_t D, int32_t F, int pairs) {
+  FwdPlan p;
+  p.y = split_of(T, D, div_up(F, kBK), pairs, 0);
+  p.bytes = round256((size_t)T * F * 2) + round256(p.y.bytes);
+  return p;
+}
+
+struct BwdPlan {
+  Split dx;
+  size_t bytes;
+};
+BwdPlan bwd_plan(int64_t T, int32_t D, int32_t F, int pairs) {
+  BwdPlan p;
+  const int64_t weight_tiles = 2 * (int64_t)div_up(F, kTM) * div_up(D, kTN) +
+                               (int64_t)div_up(D, kTM) * div_up(F, kTN);
+  const int64_t other = weight_tiles * (div_up(T, kBK) + 6) / pairs;
+  p.dx = split_of(T, D, 2 * div_up(F, kBK), pairs, other > 0 ? other : 1);
+  p.bytes = 3 * round256((size_t)T * F * 2) + round256(p.dx.bytes);
+  return p;
+}
+
+}  // namespace
+}  // namespace adaln
+
+using namespace adaln;
+
+extern "C" {
+
+int adaln_ffn_saved_size(int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype, size_t* bytes) {
+  const int rc = check(T, D, F, dtype, ADALN_ACT_SILU);
+  if (rc != ADALN_OK) return rc;
+  if (!bytes) return ADALN_ERR_NULL;
+  *bytes = saved_layout(T, F).bytes;
+  return ADALN_OK;
+}
+
+int adaln_ffn_workspace_size(int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype, size_t* fwd_bytes,
+                             size_t* bwd_bytes) {
+  const int rc = check(T, D, F, dtype, ADALN_ACT_SILU);
+  if (rc != ADALN_OK) return rc;
+  if (!fwd_bytes && !bwd_bytes) return ADALN_ERR_NULL;
+  int pairs = 0;
+  const cudaError_t e = pairs_of_device(&pairs);
+  if (e != cudaSuccess) return launch_failed(e);
+  if (fwd_bytes) *fwd_bytes = fwd_plan(T, D, F, pairs).bytes;
+  if (bwd_bytes) *bwd_bytes = bwd_plan(T, D, F, pairs).bytes;
+  return ADALN_OK;
+}
+
+int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd, int64_t T,
+                  int32_t D, int32_t F, adaln_dtype_t dtype, adaln_act_t act, void* y, void* saved,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check(T, D, F, dtype, act);
+  if (rc != ADALN_OK) return rc;
+  if (T == 0) return ADALN_OK;
+  if (!x || !wg || !wu || !wd || !y || !workspace) return ADALN_ERR_NULL;
+  if (!aligned16(x) || !aligned16(wg) || !aligned16(wu) || !aligned16(wd) || !aligned16(y) ||
+      !aligned16(saved) || !aligned16(workspace))
+    return ADALN_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int pairs = 0;
+  cudaError_t e = pairs_of_device(&pairs);
+  if (e != cudaSuccess) return launch_failed(e);
+  const FwdPlan plan = fwd_plan(T, D, F, pairs);
+  if (workspace_bytes < plan.bytes) return ADALN_ERR_WORKSPACE;
+  GemmArgs a = {};
+  if ((e = status_word(&a.status)) != cudaSuccess) return launch_failed(e);
+
+  char* ws = static_cast<char*>(workspace);
+  a.h = reinterpret_cast<__nv_bfloat16*>(ws);
+  if (saved) {
+    const Saved s = saved_layout(T, F);
+    char* p = static_cast<char*>(saved);
+    a.g_hi = reinterpret_cast<uint16_t*>(p);
+    a.u_hi = reinterpret_cast<uint16_t*>(p + s.u_hi);
+    a.g_lo = reinterpret_cast<uint8_t*>(p + s.g_lo);
+    a.u_lo = reinterpret_cast<uint8_t*>(p + s.u_lo);
+  }
+  const Operand none = {};
+  a.problems = 1;
+  e = set_problem(&a.p[0], {{x, T, D, false}, none}, {{wg, F, D, false}, {wu, F, D, false}}, 1, T, F,
+                  128, D, 0, nullptr);
+  if (e == cudaSuccess) e = launch_gemm(a, kGate, act, pairs, st);
+  if (e != cudaSuccess) return launch_failed(e);
+
+  e = set_problem(&a.p[0], {{a.h, T, F, false}, none}, {{wd, D, F, false}, none}, 1, T, D, kTN, F, 0, y);
+  a.p[0].splits = plan.y.splits;
+  a.p[0].partial = reinterpret_cast<float*>(ws + round256((size_t)T * F * 2));
+  if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, st);
+  if (e == cudaSuccess && plan.y.splits > 1) e = launch_join(a.p[0], st);
+  return e == cudaSuccess ? ADALN_OK : launch_failed(e);
+}
+
+int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu, const void* wd,
+                  const void* saved, int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype,
+                  adaln_act_t act, void* dx, void* dwg, void* dwu, void* dwd, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  const int rc = check(T, D, F, dtype, act);
+  if (rc != ADALN_OK) return rc;
+  if (!dwg || !dwu || !dwd) return ADALN_ERR_NULL;
+  if (T > 0 && (!dy || !x || !wg || !wu || !wd || !saved || !dx || !workspace))
+    return ADALN_ERR_NULL;
+  if (!aligned16(dwg) || !aligned16(dwu) || !aligned16(dwd)) return ADALN_ERR_ALIGN;
+  if (T > 0 && (!aligned16(dy) || !aligned16(x) || !aligned16(wg) || !aligned16(wu) ||
+                !aligned16(wd) || !aligned16(saved) || !aligned16(dx) || !aligned16(workspace)))
+    return ADALN_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (T == 0) {  // empty sums
+    void* const out[3] = {dwg, dwu, dwd};
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+      e = cudaMemsetAsync(out[i], 0, (size_t)D * F * 2, st);
+    return e == cudaSuccess ? ADALN_OK : launch_failed(e);
+  }
+  int pairs = 0;
+  if ((e = pairs_of_device(&pairs)) != cudaSuccess) return launch_failed(e);
+  const BwdPlan plan = bwd_plan(T, D, F, pairs);
+  if (workspace_bytes < plan.bytes) return ADALN_ERR_WORKSPACE;
+  GemmArgs a = {};
+  if ((e = status_word(&a.status)) != cudaSuccess) return launch_failed(e);
+
+  const size_t tf = round256((size_t)T * F * 2);
+  char* ws = static_cast<char*>(workspace);
+  a.h = reinterpret_cast<__nv_bfloat16*>(ws);
+  a.dg = reinterpret_cast<__nv_bfloat16*>(ws + tf);
+  a.du = reinterpret_cast<__nv_bfloat16*>(ws + 2 * tf);
+  const Saved s = saved_layout(T, F);
+  char* sv = const_cast<char*>(static_cast<const char*>(saved));
+  a.g_hi = reinterpret_cast<uint16_t*>(sv);
+  a.u_hi = reinterpret_cast<uint16_t*>(sv + s.u_hi);
+  a.g_lo = reinterpret_cast<uint8_t*>(sv + s.g_lo);
+  a.u_lo = reinterpret_cast<uint8_t*>(sv + s.u_lo);
+
+  const Operand none = {};
+  a.problems = 1;
+  e = set_problem(&a.p[0], {{dy, T, D, false}, none}, {{wd, D, F, true}, none}, 1, T, F, kTN, D, 0,
+                  nullptr);
+  if (e == cudaSuccess) e = launch_gemm(a, kGateBwd, act, pairs, st);
+  if (e != cudaSuccess) return launch_failed(e);
+
+  // dx first: its units are the longest.
+  const Operand dgk = {a.dg, T, F, false}, duk = {a.du, T, F, false};
+  const Operand dgm = {a.dg, T, F, true}, dum = {a.du, T, F, true};
+  const Operand xm = {x, T, D, true}, dym = {dy, T, D, true}, hm = {a.h, T, F, true};
+  a.problems = 4;
+  e = set_problem(&a.p[0], {dgk, duk}, {{wg, F, D, true}, {wu, F, D, true}}, 2, T, D, kTN, F, F, dx);
+  a.p[0].splits = plan.dx.splits;
+  a.p[0].partial = reinterpret_cast<float*>(ws + 3 * tf);
+  if (e == cudaSuccess) e = set_problem(&a.p[1], {dgm, none}, {xm, none}, 1, F, D, kTN, T, 0, dwg);
+  if (e == cudaSuccess) e = set_problem(&a.p[2], {dum, none}, {xm, none}, 1, F, D, kTN, T, 0, dwu);
+  if (e == cudaSuccess) e = set_problem(&a.p[3], {dym, none}, {hm, none}, 1, D, F, kTN, T, 0, dwd);
+  if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, st);
+  if (e == cudaSuccess && plan.dx.splits > 1) e = launch_join(a.p[0], st);
+  return e == cudaSuccess ? ADALN_OK : launch_failed(e);
+}
+
+}  // extern "C"

@@ -106,11 +106,6 @@ __device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
   v = fmaf(b, cs.x, as);
 }
 
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // Sum over the CTA's warps of red[warp][0..dh), in warp order, into slot.
 __device__ __forceinline__ void store_partial(const float* red, float* slot, int dh) {
   __syncthreads();

@@ -81,6 +81,8 @@ extern "C" {
 #define ADALN_MAX_HEADS 4096
 #define ADALN_MAX_HEAD_DIM 512
 #define ADALN_MAX_ROPE_AXES 4
+#define ADALN_FFN_MAX_T (1 << 24)
+#define ADALN_FFN_MAX_DIM (1 << 18)
 
 typedef enum {
   ADALN_F32 = 0,  /* IEEE binary32 */
@@ -293,6 +295,59 @@ ADALN_API int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t
               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Gated feed-forward block of a transformer layer, on the tensor cores:
+ *
+ *   y = (act(x Wg') * (x Wu')) Wd'
+ *
+ * x, y, dy, dx [T, D]; Wg, Wu and their gradients [F, D]; Wd and its gradient
+ * [D, F]; all bf16 (dtype must be ADALN_BF16), row-major and contiguous,
+ * 16-byte aligned.  D and F are multiples of 8 up to ADALN_FFN_MAX_DIM, T is
+ * at most ADALN_FFN_MAX_T.  Sums are fp32; the hidden product h and, in the
+ * backward, the gradients of the two projections are rounded to bf16 once,
+ * like the outputs.
+ */
+typedef enum {
+  ADALN_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+  ADALN_ACT_GELU_TANH = 1, /* the tanh approximation of GELU */
+  ADALN_ACT_GELU = 2       /* g Phi(g) */
+} adaln_act_t;
+
+/*
+ * Device bytes: of what a forward saves for its backward (x Wg' and x Wu' at
+ * 24 bits a value: 6 T F bytes), and of each call's workspace on the current
+ * device (either pointer of the second may be NULL).
+ */
+ADALN_API int adaln_ffn_saved_size(int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype,
+              size_t* bytes);
+ADALN_API int adaln_ffn_workspace_size(int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype,
+              size_t* fwd_bytes, size_t* bwd_bytes);
+
+/*
+ * Forward: two launches (a third where few rows make it worth splitting the
+ * sum over F).  `saved` receives what the backward needs, adaln_ffn_saved_size
+ * bytes; NULL for inference.  `workspace` is scratch of
+ * adaln_ffn_workspace_size bytes.  T = 0 does nothing.
+ *
+ * Errors: ADALN_ERR_DTYPE, ADALN_ERR_DIM, ADALN_ERR_ARG (unknown act),
+ * ADALN_ERR_NULL, ADALN_ERR_ALIGN (16 bytes), ADALN_ERR_WORKSPACE (short),
+ * ADALN_ERR_CUDA.
+ */
+ADALN_API int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd,
+              int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype, adaln_act_t act,
+              void* y, void* saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward, from dy, the forward's inputs and what it saved: dx and the three
+ * weight gradients, in the weights' type.  No atomics: bitwise reproducible
+ * for a given device and sizes.  T = 0 zeroes the weight gradients.  Errors
+ * as for the forward.
+ */
+ADALN_API int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
+              const void* wd, const void* saved, int64_t T, int32_t D, int32_t F,
+              adaln_dtype_t dtype, adaln_act_t act, void* dx, void* dwg, void* dwu,
+              void* dwd, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the status word: the one the
  * calling thread bound (adaln_status_bind), else the current device's.
  * *host_bits (if non-NULL) receives the ADALN_DEV_* bits.  Returns ADALN_OK,
@@ -326,13 +381,15 @@ ADALN_API const char* adaln_strerror(int code);
  * `capacity` launches.  adaln_trace_end() synchronises those events and sums
  * the elapsed time per kernel; adaln_trace_get() reads the sums.
  * Kernel ids: ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE;
- * ADALN_KERNEL_QK_ROPE counts every launch of the rotary calls.
+ * ADALN_KERNEL_QK_ROPE and ADALN_KERNEL_FFN count every launch of the rotary
+ * and of the feed-forward calls.
  */
 #define ADALN_KERNEL_FWD 0
 #define ADALN_KERNEL_BWD_ROWS 1
 #define ADALN_KERNEL_BWD_FINALIZE 2
 #define ADALN_KERNEL_QK_ROPE 3
-#define ADALN_NUM_KERNELS 4
+#define ADALN_KERNEL_FFN 4
+#define ADALN_NUM_KERNELS 5
 ADALN_API int adaln_trace_begin(int capacity);
 ADALN_API int adaln_trace_end(void);
 ADALN_API int adaln_trace_get(int kernel_id, int64_t* launches, double* total_ms);
