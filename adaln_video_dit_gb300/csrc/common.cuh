@@ -185,6 +185,23 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same bound without the sleep hint, for waits on the critical path of a
+// pipeline: a suspended thread's wake-up and the timer's read each cost about
+// as much as a stage takes, so the timer is read every 256 tries only.
+__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity,
+                                               const volatile int* abort) {
+  uint64_t t0 = 0;
+  for (int i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255) == 0) {
+      if (*abort) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+
 // One bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned)
 // from global memory into this CTA's shared memory; completion is signalled
 // to barrier `bar` as transaction bytes.

@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(
       smem_raw + (bars - smem_addr(smem_raw)) + 8 * (2 * kStages + 6));
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x & 1;  // within the pair
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -328,44 +328,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
 
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (mbar_wait_bounded(bar, parity, abort_flag)) return true;
+    if (mbar_wait_spin(bar, parity, abort_flag)) return true;
     *abort_flag = 1;
     atomicOr(a.status, ADALN_DEV_TIMEOUT);
     return false;
   };
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // Producer: this CTA's 128 rows of A and of B, a stage at a time.
     int s = 0;
     uint32_t parity = 0;
     bool ok = true;
     for (int ui = cluster; ok && ui < a.units; ui += clusters) {
       const Unit u = unit_of(a, ui);
+      // In registers before the loop: after each asm with a memory clobber
+      // the parameters would be read again.
       const Problem& p = *u.p;
       const int m = u.m * kTM + (int)rank * 128;
       const int n = KIND == kGate ? u.n * 128 : u.n * kTN + (int)rank * 128;
+      const int kb0 = p.kb0;
+      const bool a_mn = p.a_mn, b_mn = p.b_mn;
+      const CUtensorMap* const maps_a = p.a;
+      const CUtensorMap* const maps_b = p.b + (KIND == kGate ? (int)rank : 0);
       for (int kb = u.k0; kb < u.k1; ++kb) {
-        if (!wait(empty(s), parity ^ 1)) {
+        if (!__all_sync(~0u, wait(empty(s), parity ^ 1))) {
           ok = false;
           break;
         }
-        if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
-        const int seg = kb >= p.kb0;
-        const int k = (kb - (seg ? p.kb0 : 0)) * kBK;
-        const CUtensorMap* ma = &p.a[seg];
-        const CUtensorMap* mb = &p.b[KIND == kGate ? (int)rank : seg];
+        const int seg = kb >= kb0;
+        const int k = (kb - (seg ? kb0 : 0)) * kBK;
+        const CUtensorMap* ma = maps_a + seg;
+        const CUtensorMap* mb = maps_b + seg;
         const uint32_t da = ring + s * kStageBytes, db = da + kTileBytes;
-        if (p.a_mn) {
-          tma_load_pair(da, ma, m, k, full(s));
-          tma_load_pair(da + kTileBytes / 2, ma, m + 64, k, full(s));
-        } else {
-          tma_load_pair(da, ma, k, m, full(s));
-        }
-        if (p.b_mn) {
-          tma_load_pair(db, mb, n, k, full(s));
-          tma_load_pair(db + kTileBytes / 2, mb, n + 64, k, full(s));
-        } else {
-          tma_load_pair(db, mb, k, n, full(s));
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+          if (a_mn) {
+            tma_load_pair(da, ma, m, k, full(s));
+            tma_load_pair(da + kTileBytes / 2, ma, m + 64, k, full(s));
+          } else {
+            tma_load_pair(da, ma, k, m, full(s));
+          }
+          if (b_mn) {
+            tma_load_pair(db, mb, n, k, full(s));
+            tma_load_pair(db + kTileBytes / 2, mb, n + 64, k, full(s));
+          } else {
+            tma_load_pair(db, mb, k, n, full(s));
+          }
         }
         if (++s == kStages) {
           s = 0;
@@ -379,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kStages; ++i)
         mbar_wait_bounded(full(i), i < s ? parity : parity ^ 1, nullptr, kDrainLimitNs);
     }
-  } else if (warp == 1 && rank == 0 && lane == 0) {
+  } else if (warp == 1 && rank == 0) {
     // Issuer of the pair's matrix instructions.
     int s = 0, acc = 0;
     uint32_t parity = 0, acc_parity = 0;
@@ -389,30 +397,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool a_mn = u.p->a_mn, b_mn = u.p->b_mn;
       const uint32_t idesc = instr_desc(kTM, kTN, a_mn, b_mn);
       const uint32_t step_a = k_step_bytes(a_mn) >> 4, step_b = k_step_bytes(b_mn) >> 4;
-      if (!(ok = wait(acc_empty(acc), acc_parity ^ 1))) break;
+      if (!(ok = __all_sync(~0u, wait(acc_empty(acc), acc_parity ^ 1)))) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kTN;
       for (int kb = u.k0; kb < u.k1; ++kb) {
-        if (!(ok = wait(full(s), parity))) break;
+        if (!(ok = __all_sync(~0u, wait(full(s), parity)))) break;
         tc_fence_after();
         const uint64_t da = smem_desc(ring + s * kStageBytes, a_mn, kTileBytes / 2);
         const uint64_t db = smem_desc(ring + s * kStageBytes + kTileBytes, b_mn, kTileBytes / 2);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          tc_mma<2>(d, da + k * step_a, db + k * step_b, idesc, kb > u.k0 || k > 0);
-        tc_commit<2>(empty(s));
+          for (int k = 0; k < kBK / 16; ++k)
+            tc_mma<2>(d, da + k * step_a, db + k * step_b, idesc, kb > u.k0 || k > 0);
+          tc_commit<2>(empty(s));
+          if (kb + 1 == u.k1) tc_commit<2>(acc_full(acc));
+        }
         if (++s == kStages) {
           s = 0;
           parity ^= 1;
         }
       }
-      if (!ok) break;
-      tc_commit<2>(acc_full(acc));
       acc ^= 1;
       if (acc == 0) acc_parity ^= 1;
     }
     if (!ok) {  // matrix instructions may be in flight: wait for them, with a limit
-      tc_commit<2>(drain);
+      if (elect_one()) tc_commit<2>(drain);
       mbar_wait_bounded(drain, 0, nullptr, kDrainLimitNs);
     }
   } else if (warp >= 2) {

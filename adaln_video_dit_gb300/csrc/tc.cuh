@@ -29,6 +29,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped) {
                : "memory");
 }
 
+// One lane of a converged warp.  Copies and matrix instructions are issued by
+// a whole warp walking the loop with one lane elected at each issue, not by a
+// lane on its own: their operands live in uniform registers, which the compiler
+// can only use where control flow is uniform (a lone lane's TMA issue measured
+// 235 cycles, half of what a stage's products take).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ----- TMA ----------------------------------------------------------------------
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
