@@ -35,22 +35,39 @@
 namespace adaln {
 namespace {
 
-enum { kPlain = 0, kGate = 1, kGateBwd = 2 };
+// Epilogues: the product alone; the gate; the gate, saving g and u; the
+// gate's gradient.
+enum { kPlain = 0, kGate = 1, kGateSave = 2, kGateBwd = 3, kKinds = 4 };
 
-constexpr int kStages = 6;
 constexpr int kBK = 64;                    // k values of a stage
 constexpr int kTileBytes = 128 * kBK * 2;  // one CTA's share of an operand stage
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kTM = 256, kTN = 256;        // tile of a CTA pair
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+// Outputs leave (and the saved values come) through blocks of 32 rows x 32
+// columns in shared memory, copied by TMA: a lane holds a row of its
+// accumulator, and 32 lanes writing 16 bytes each to 32 rows of global memory
+// cost a cache-line lookup per lane (the stores of g, u and h alone took half
+// as long again as the products at D = 1536).
+constexpr int kBlock16 = 32 * 32 * 2, kBlock8 = 32 * 32;
+// A warp's shared memory: kPlain, kGate: two blocks in turn; kGateSave: h, the
+// upper halves and the next bytes of g and u; kGateBwd: the last four, twice.
+ADALN_HD constexpr int staging_bytes(int kind) {
+  return kind == kGateSave ? 3 * kBlock16 + 2 * kBlock8
+         : kind == kGateBwd ? 2 * (2 * kBlock16 + 2 * kBlock8) : 2 * kBlock16;
+}
+// Ring stages that fit beside it.
+ADALN_HD constexpr int stages_of(int kind) { return kind == kGateBwd ? 4 : kind == kGateSave ? 5 : 6; }
+constexpr int smem_of(int kind) {
+  return 1024 + stages_of(kind) * kStageBytes + kEpiWarps * staging_bytes(kind) + 256;
+}
 constexpr int kGroupM = 8;                 // tile rows walked together (L2 reuse)
 constexpr int kMaxProblems = 4;
 
 struct Problem {       // C[M, N] = sum over its K segments of A B
   CUtensorMap a[2], b[2];
-  void* out;           // bf16 [M, N]
+  CUtensorMap out;     // bf16 [M, N]
   float* partial;      // fp32 [splits][M][N] when splits > 1
   int M, N;
   int kb0, kb;         // k blocks of segment 0, of both
@@ -62,10 +79,9 @@ struct Problem {       // C[M, N] = sum over its K segments of A B
 struct GemmArgs {
   Problem p[kMaxProblems];
   int problems, units;
-  // Gate epilogues ([T, F] each).
-  __nv_bfloat16 *h, *dg, *du;
-  uint16_t *g_hi, *u_hi;  // saved pre-activations: upper 16 bits, next 8
-  uint8_t *g_lo, *u_lo;
+  // Gate epilogues ([T, F] each): products, and the saved g and u (upper 16
+  // bits, next 8).
+  CUtensorMap h, dg, du, g_hi, u_hi, g_lo, u_lo;
   unsigned* status;
 };
 
@@ -124,62 +140,73 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// 32 consecutive bf16 values of a row, those below column `n` (n a multiple
-// of 8 from the row's start; `left` = n minus the first column).
-__device__ __forceinline__ void store_row32(void* p, const uint32_t (&w)[16], int left) {
+// Byte offset of 16-byte piece `i` of row `r` in a block of 64-byte rows (the
+// 64-byte swizzle) and of 32-byte rows (the 32-byte one) of a tensor map.
+__device__ __forceinline__ uint32_t at16(int r, int i) { return r * 64 + ((i ^ (r >> 1 & 3)) << 4); }
+__device__ __forceinline__ uint32_t at8(int r, int i) { return r * 32 + ((i ^ (r >> 2 & 1)) << 4); }
+
+// This lane's row of 32 values into a block: 16 words of bf16 pairs.
+__device__ __forceinline__ void put_row16(uint32_t block, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (8 * i < left)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    st_shared_v4(block + at16(lane, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// Save 32 fp32 values of a row as their upper 16 bits and their next 8.
-__device__ __forceinline__ void save_row32(uint16_t* hi, uint8_t* lo, const uint32_t (&v)[32],
-                                           int left) {
-  uint32_t w[16];
+// 32 fp32 values of a row as their upper 16 bits and their next 8.
+__device__ __forceinline__ void put_saved(uint32_t hi, uint32_t lo, int lane,
+                                          const uint32_t (&v)[32]) {
+  uint32_t w[16], b[8];
 #pragma unroll
   for (int i = 0; i < 16; ++i) w[i] = __byte_perm(v[2 * i], v[2 * i + 1], 0x7632);
-  store_row32(hi, w, left);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (8 * i < left) {
-      const uint32_t a = __byte_perm(v[8 * i], v[8 * i + 1], 0x51),
-                     b = __byte_perm(v[8 * i + 2], v[8 * i + 3], 0x51),
-                     c = __byte_perm(v[8 * i + 4], v[8 * i + 5], 0x51),
-                     d = __byte_perm(v[8 * i + 6], v[8 * i + 7], 0x51);
-      reinterpret_cast<uint2*>(lo)[i] =
-          make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410));
-    }
-  }
+  for (int i = 0; i < 8; ++i)
+    b[i] = __byte_perm(__byte_perm(v[4 * i], v[4 * i + 1], 0x51),
+                       __byte_perm(v[4 * i + 2], v[4 * i + 3], 0x51), 0x5410);
+  put_row16(hi, lane, w);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    st_shared_v4(lo + at8(lane, i), b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
 }
 
-// The 8 values saved at (hi, lo).
-__device__ __forceinline__ void load_saved8(const uint4& h, const uint2& l, float (&f)[8]) {
-  const uint32_t w[4] = {h.x, h.y, h.z, h.w}, b[2] = {l.x, l.y};
+// And back: value i from word i / 2 of the upper halves, byte i of the rest.
+__device__ __forceinline__ float saved_value(const uint32_t (&w)[16], const uint32_t (&b)[8], int i) {
+  return __uint_as_float((i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) |
+                         (b[i / 4] >> (8 * (i % 4)) & 0xff) << 8);
+}
+__device__ __forceinline__ void get_saved(uint32_t hi, uint32_t lo, int lane, uint32_t (&w)[16],
+                                          uint32_t (&b)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t lo = (b[i / 4] >> (8 * (i % 4))) & 0xff;
-    const uint32_t up = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffff;
-    f[i] = __uint_as_float(up << 16 | lo << 8);
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = ld_shared_v4(hi + at16(lane, i));
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = ld_shared_v4(lo + at8(lane, i));
+    b[4 * i] = v.x, b[4 * i + 1] = v.y, b[4 * i + 2] = v.z, b[4 * i + 3] = v.w;
   }
 }
 
 // ----- epilogues: one warp's 32 rows x half of the tile's columns -----------------
-// `row` is this lane's row of the output, `half` the column half.
+// `row0` is the warp's first row of the output, `half` its column half, `acc`
+// its lanes of the accumulator, `buf` its staging memory.
 
-__device__ __forceinline__ void epilogue_plain(const Unit& u, uint32_t acc, int row, int half) {
+__device__ __forceinline__ void epilogue_plain(const Unit& u, uint32_t acc, int row0, int half,
+                                               uint32_t buf, int lane, int& turn) {
   const Problem& p = *u.p;
+  const int M = p.M, N = p.N, splits = p.splits;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const int col = u.n * kTN + half * 128 + c * 32;
-    if (col >= p.N) break;
+    if (col >= N) break;
     __syncwarp();
     uint32_t r[32];
     tmem_ld32(acc + half * 128 + c * 32, r);
     tc_wait_ld();
-    const int left = row < p.M ? p.N - col : 0;  // columns of this row to write
-    if (p.splits > 1) {
-      float4* o = reinterpret_cast<float4*>(p.partial + ((int64_t)u.split * p.M + row) * p.N + col);
+    if (splits > 1) {
+      const int left = row0 + lane < M ? N - col : 0;  // columns of this row to write
+      float4* o = reinterpret_cast<float4*>(p.partial +
+                                            ((int64_t)u.split * M + row0 + lane) * N + col);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (4 * i < left)
@@ -190,26 +217,35 @@ __device__ __forceinline__ void epilogue_plain(const Unit& u, uint32_t acc, int 
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         w[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-      store_row32(static_cast<__nv_bfloat16*>(p.out) + (int64_t)row * p.N + col, w, left);
+      const uint32_t block = buf + turn * kBlock16;
+      turn ^= 1;
+      bulk_wait_read<1>();  // the copy before the last one used this block
+      __syncwarp();
+      put_row16(block, lane, w);
+      fence_async_shared();
+      __syncwarp();
+      if (elect_one()) {
+        if (row0 < M) tma_store(&p.out, col, row0, block);
+        bulk_commit();
+      }
     }
   }
 }
 
-template <int ACT>
+template <int ACT, bool SAVE>
 __device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Unit& u, uint32_t acc,
-                                              int row, int half) {
-  const Problem& p = *u.p;
+                                              int row0, int half, uint32_t buf, int lane,
+                                              int& turn) {
+  const int M = u.p->M, N = u.p->N;
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const int col = u.n * 128 + half * 64 + c * 32;
-    if (col >= p.N) break;
+    if (col >= N) break;
     __syncwarp();
     uint32_t g[32], v[32];
     tmem_ld32(acc + half * 64 + c * 32, g);
     tmem_ld32(acc + 128 + half * 64 + c * 32, v);
     tc_wait_ld();
-    const int left = row < p.M ? p.N - col : 0;
-    const int64_t at = (int64_t)row * p.N + col;
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -223,73 +259,98 @@ __device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Unit& u, 
       }
       w[i] = pack_bf16(h[0], h[1]);
     }
-    store_row32(a.h + at, w, left);
-    if (a.g_hi != nullptr) {
-      save_row32(a.g_hi + at, a.g_lo + at, g, left);
-      save_row32(a.u_hi + at, a.u_lo + at, v, left);
+    bulk_wait_read<SAVE ? 0 : 1>();
+    __syncwarp();
+    const uint32_t block = SAVE ? buf : buf + turn * kBlock16;
+    turn ^= 1;
+    const uint32_t gh = buf + kBlock16, uh = gh + kBlock16, gl = uh + kBlock16, ul = gl + kBlock8;
+    put_row16(block, lane, w);
+    if (SAVE) {
+      put_saved(gh, gl, lane, g);
+      put_saved(uh, ul, lane, v);
+    }
+    fence_async_shared();
+    __syncwarp();
+    if (elect_one()) {
+      if (row0 < M) {
+        tma_store(&a.h, col, row0, block);
+        if (SAVE) {
+          tma_store(&a.g_hi, col, row0, gh);
+          tma_store(&a.u_hi, col, row0, uh);
+          tma_store(&a.g_lo, col, row0, gl);
+          tma_store(&a.u_lo, col, row0, ul);
+        }
+      }
+      bulk_commit();
     }
   }
 }
 
+// The saved g and u of a chunk of the gate's gradient, into half `b` of the
+// warp's staging memory.
+__device__ __forceinline__ void load_saved(const GemmArgs& a, int col, int row0, uint32_t buf,
+                                           uint32_t bar) {
+  mbar_arrive_expect_tx(bar, 2 * kBlock16 + 2 * kBlock8);
+  tma_load(buf, &a.g_hi, col, row0, bar);
+  tma_load(buf + kBlock16, &a.u_hi, col, row0, bar);
+  tma_load(buf + 2 * kBlock16, &a.g_lo, col, row0, bar);
+  tma_load(buf + 2 * kBlock16 + kBlock8, &a.u_lo, col, row0, bar);
+}
+
+// One chunk of the gate's gradient: the accumulator's dh with the g and u in
+// `buf`, whose place dg, du and h (over the two byte blocks) take.
 template <int ACT>
-__device__ __forceinline__ void epilogue_gate_bwd(const GemmArgs& a, const Unit& u, uint32_t acc,
-                                                  int row, int half) {
-  const Problem& p = *u.p;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const int col = u.n * kTN + half * 128 + c * 32;
-    if (col >= p.N) break;
-    __syncwarp();
-    const int64_t at = (int64_t)row * p.N + col;
-    const int left = row < p.M ? p.N - col : 0;
-    uint4 gh[4], uh[4];
-    uint2 gl[4], ul[4];
+__device__ __forceinline__ void chunk_gate_bwd(const GemmArgs& a, uint32_t acc, int col, int row0,
+                                               int M, uint32_t buf, int lane) {
+  const uint32_t gh = buf, uh = buf + kBlock16, gl = buf + 2 * kBlock16, ul = gl + kBlock8;
+  uint32_t gw[16], gb[8], uw[16], ub[8], r[32];
+  tmem_ld32(acc, r);
+  get_saved(gh, gl, lane, gw, gb);
+  get_saved(uh, ul, lane, uw, ub);
+  tc_wait_ld();
+  __syncwarp();  // h goes where other lanes' bytes were
+  uint32_t h[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = 8 * i < left;
-      gh[i] = in ? reinterpret_cast<const uint4*>(a.g_hi + at)[i] : make_uint4(0, 0, 0, 0);
-      uh[i] = in ? reinterpret_cast<const uint4*>(a.u_hi + at)[i] : make_uint4(0, 0, 0, 0);
-      gl[i] = in ? reinterpret_cast<const uint2*>(a.g_lo + at)[i] : make_uint2(0, 0);
-      ul[i] = in ? reinterpret_cast<const uint2*>(a.u_lo + at)[i] : make_uint2(0, 0);
+  for (int i = 0; i < 16; ++i) {
+    float dg[2], du[2], hv[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = saved_value(gw, gb, 2 * i + e), w = saved_value(uw, ub, 2 * i + e);
+      const float dh = __uint_as_float(r[2 * i + e]);
+      float s, d;
+      gate<ACT>(x, s, d);
+      dg[e] = dh * w * d;
+      du[e] = dh * (x * s);
+      hv[e] = x * s * w;
     }
-    uint32_t r[32];
-    tmem_ld32(acc + half * 128 + c * 32, r);
-    tc_wait_ld();
-    uint32_t wg[16], wu[16], wh[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float g[8], v[8];
-      load_saved8(gh[i], gl[i], g);
-      load_saved8(uh[i], ul[i], v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float dg[2], du[2], h[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = g[2 * j + e], w = v[2 * j + e], dh = __uint_as_float(r[8 * i + 2 * j + e]);
-          float s, d;
-          gate<ACT>(x, s, d);
-          dg[e] = dh * w * d;
-          du[e] = dh * (x * s);
-          h[e] = x * s * w;
-        }
-        wg[4 * i + j] = pack_bf16(dg[0], dg[1]);
-        wu[4 * i + j] = pack_bf16(du[0], du[1]);
-        wh[4 * i + j] = pack_bf16(h[0], h[1]);
-      }
+    gw[i] = pack_bf16(dg[0], dg[1]);
+    uw[i] = pack_bf16(du[0], du[1]);
+    h[i] = pack_bf16(hv[0], hv[1]);
+  }
+  put_row16(gh, lane, gw);
+  put_row16(uh, lane, uw);
+  put_row16(gl, lane, h);
+  fence_async_shared();
+  __syncwarp();
+  if (elect_one()) {
+    if (row0 < M) {
+      tma_store(&a.dg, col, row0, gh);
+      tma_store(&a.du, col, row0, uh);
+      tma_store(&a.h, col, row0, gl);
     }
-    store_row32(a.dg + at, wg, left);
-    store_row32(a.du + at, wu, left);
-    store_row32(a.h + at, wh, left);
+    bulk_commit();
   }
 }
 
 template <int KIND, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ GemmArgs a) {
+  constexpr int kStages = stages_of(KIND);
+  constexpr bool kIsGate = KIND == kGate || KIND == kGateSave;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u;
-  const uint32_t bars = ring + kStages * kStageBytes;
+  const uint32_t staging = ring + kStages * kStageBytes;
+  const uint32_t bars = staging + kEpiWarps * staging_bytes(KIND);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
   auto acc_full = [&](int i) { return bars + 8 * (2 * kStages + i); };
@@ -298,6 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_ptr = bars + 8 * (2 * kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(
       smem_raw + (bars - smem_addr(smem_raw)) + 8 * (2 * kStages + 6));
+  // kGateBwd: saved values landed, two per epilogue warp.
+  auto saved_full = [&](int w, int b) { return bars + 8 * (2 * kStages + 7 + 2 * w + b); };
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;  // within the pair
@@ -313,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(acc_empty(i), 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
+    if (KIND == kGateBwd)
+      for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(saved_full(i >> 1, i & 1), 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -345,11 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the parameters would be read again.
       const Problem& p = *u.p;
       const int m = u.m * kTM + (int)rank * 128;
-      const int n = KIND == kGate ? u.n * 128 : u.n * kTN + (int)rank * 128;
+      const int n = kIsGate ? u.n * 128 : u.n * kTN + (int)rank * 128;
       const int kb0 = p.kb0;
       const bool a_mn = p.a_mn, b_mn = p.b_mn;
       const CUtensorMap* const maps_a = p.a;
-      const CUtensorMap* const maps_b = p.b + (KIND == kGate ? (int)rank : 0);
+      const CUtensorMap* const maps_b = p.b + (kIsGate ? (int)rank : 0);
       for (int kb = u.k0; kb < u.k1; ++kb) {
         if (!__all_sync(~0u, wait(empty(s), parity ^ 1))) {
           ok = false;
@@ -427,26 +492,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 2) {
     // Epilogue.  A warp reads the 32 lanes of tensor memory of its quarter.
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    int acc = 0;
+    const uint32_t buf = staging + (warp - 2) * staging_bytes(KIND);
+    const int row_in = (int)rank * 128 + quarter * 32, lanes = quarter * 32;
+    int acc = 0, turn = 0;
     uint32_t acc_parity = 0;
-    for (int ui = cluster; ui < a.units; ui += clusters) {
+    bool ok = true;
+    // kGateBwd: chunks of 32 columns, in the order of the units; chunk c of a
+    // unit exists if it starts before the last column.  One is loaded ahead.
+    auto col_of = [&](const Unit& u, int c) { return u.n * kTN + half * 128 + c * 32; };
+    int chunk = 0, ahead = cluster, ahead_c = 0;
+    auto load_ahead = [&](int b) {  // the chunk at or after (ahead, ahead_c), if any
+      for (; ahead < a.units; ahead += clusters, ahead_c = 0) {
+        const Unit u = unit_of(a, ahead);
+        if (ahead_c < 4 && col_of(u, ahead_c) < u.p->N) {
+          if (elect_one())
+            load_saved(a, col_of(u, ahead_c), u.m * kTM + row_in,
+                       buf + b * (staging_bytes(KIND) / 2), saved_full(warp - 2, b));
+          ++ahead_c;
+          return;
+        }
+      }
+    };
+    if (KIND == kGateBwd) load_ahead(0);
+    for (int ui = cluster; ok && ui < a.units; ui += clusters) {
       const Unit u = unit_of(a, ui);
-      if (!__all_sync(~0u, wait(acc_full(acc), acc_parity))) break;
+      if (!(ok = __all_sync(~0u, wait(acc_full(acc), acc_parity)))) break;
       tc_fence_after();
-      const int row = u.m * kTM + (int)rank * 128 + quarter * 32 + lane;
-      const uint32_t at = tmem + acc * kTN + ((uint32_t)(quarter * 32) << 16);
-      if (KIND == kPlain)
-        epilogue_plain(u, at, row, half);
-      else if (KIND == kGate)
-        epilogue_gate<ACT>(a, u, at, row, half);
-      else
-        epilogue_gate_bwd<ACT>(a, u, at, row, half);
+      const int row0 = u.m * kTM + row_in;
+      const uint32_t at = tmem + acc * kTN + ((uint32_t)lanes << 16);
+      if constexpr (KIND == kPlain) {
+        epilogue_plain(u, at, row0, half, buf, lane, turn);
+      } else if constexpr (kIsGate) {
+        epilogue_gate<ACT, KIND == kGateSave>(a, u, at, row0, half, buf, lane, turn);
+      } else {
+        const int M = u.p->M, N = u.p->N;
+#pragma unroll 1
+        for (int c = 0; c < 4 && col_of(u, c) < N; ++c, ++chunk) {
+          const int b = chunk & 1;
+          // The other half is free once the copies out of it are done.
+          bulk_wait_read<0>();
+          __syncwarp();
+          load_ahead(b ^ 1);
+          if (!(ok = __all_sync(~0u, wait(saved_full(warp - 2, b), chunk >> 1 & 1)))) break;
+          chunk_gate_bwd<ACT>(a, at + half * 128 + c * 32, col_of(u, c), row0, M,
+                              buf + b * (staging_bytes(KIND) / 2), lane);
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty(acc), 0));
       acc ^= 1;
       if (acc == 0) acc_parity ^= 1;
     }
+    bulk_wait();
+    if (KIND == kGateBwd && !ok)  // loads may be in flight: wait for them, with a limit
+      for (int i = chunk; i < chunk + 2; ++i)
+        mbar_wait_bounded(saved_full(warp - 2, i & 1), i >> 1 & 1, nullptr, kDrainLimitNs);
   }
   __syncwarp();
   tc_fence_before();
@@ -500,18 +601,25 @@ cudaError_t encode_fn(EncodeFn* out) {
   return cudaSuccess;
 }
 
-// Tensor map of a row-major bf16 matrix [rows, cols], read in boxes of 64
-// columns (128 bytes, swizzled) x box_rows.  What lies outside reads as zero.
-cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows) {
+// Tensor map of a row-major matrix [rows, cols] of `es`-byte elements (2:
+// bf16, 1: bytes), rows `pitch` elements apart, in boxes of box_cols x
+// box_rows whose rows of 128, 64 or 32 bytes are swizzled at that width.  What
+// lies outside reads as zero and is not written.
+cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch,
+                     int es, int box_cols, int box_rows) {
   EncodeFn fn;
   const cudaError_t e = encode_fn(&fn);
   if (e != cudaSuccess) return e;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides,
-                        box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t strides[1] = {(cuuint64_t)pitch * es};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  const CUtensorMapSwizzle swizzle = box_cols * es == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                           : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUresult r =
+      fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+         const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -523,7 +631,12 @@ struct Operand {
   bool mn;
 };
 cudaError_t operand_map(CUtensorMap* m, const Operand& o) {
-  return make_map(m, o.p, o.rows, o.cols, o.mn ? kBK : 128);
+  return make_map(m, o.p, o.rows, o.cols, o.cols, 2, 64, o.mn ? kBK : 128);
+}
+// Blocks of 32 x 32 of an epilogue.
+cudaError_t block_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch,
+                      int es) {
+  return make_map(m, p, rows, cols, pitch, es, 32, 32);
 }
 
 template <int KIND>
@@ -536,8 +649,10 @@ void* gemm_kernel(int act) {
   }
 }
 void* kernel_of(int kind, int act) {
-  return kind == kPlain ? gemm_kernel<kPlain>(act)
-         : kind == kGate ? gemm_kernel<kGate>(act) : gemm_kernel<kGateBwd>(act);
+  return kind == kPlain      ? gemm_kernel<kPlain>(act)
+         : kind == kGate     ? gemm_kernel<kGate>(act)
+         : kind == kGateSave ? gemm_kernel<kGateSave>(act)
+                             : gemm_kernel<kGateBwd>(act);
 }
 
 cudaError_t launch_cluster(void* kernel, int grid, int threads, int smem, int cluster, void** params,
@@ -570,16 +685,16 @@ cudaError_t pairs_of_device(int* pairs) {
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
   if (!known[dev]) {
-    for (int kind = 0; kind < 3; ++kind)
+    for (int kind = 0; kind < kKinds; ++kind)
       for (int act = 0; act < 3; ++act) {
         e = cudaFuncSetAttribute(kernel_of(kind, act), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmem);
+                                 smem_of(kind));
         if (e != cudaSuccess) return e;
       }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem_of(kPlain);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -641,7 +756,7 @@ cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2]
     e = operand_map(&p->a[i], have_a ? a[i] : a[0]);
     if (e == cudaSuccess) e = operand_map(&p->b[i], have_b ? b[i] : b[0]);
   }
-  p->out = out;
+  if (e == cudaSuccess && out) e = block_map(&p->out, out, M, N, N, 2);
   p->partial = nullptr;
   p->M = (int)M;
   p->N = N;
@@ -666,15 +781,15 @@ cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, cudaStream_t 
   const int grid = 2 * (at < pairs ? at : pairs);
   void* params[1] = {&a};
   return traced_launch(ADALN_KERNEL_FFN, st, [&] {
-    return launch_cluster(kernel_of(kind, act), grid, kThreads, kSmem, 2, params, st);
+    return launch_cluster(kernel_of(kind, act), grid, kThreads, smem_of(kind), 2, params, st);
   });
 }
 
-cudaError_t launch_join(const Problem& p, cudaStream_t st) {
+cudaError_t launch_join(const Problem& p, void* to, cudaStream_t st) {
   const float* partial = p.partial;
   int splits = p.splits;
   int64_t vecs = (int64_t)p.M * p.N / 4;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(to);
   void* params[4] = {&partial, &splits, &vecs, &out};
   const int64_t blocks = (vecs + 255) / 256;
   const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
@@ -697,18 +812,29 @@ int check(int64_t T, int32_t D, int32_t F, adaln_dtype_t dt, int act) {
   return ADALN_OK;
 }
 
-// The saved pre-activations: upper halves of g, of u, next bytes of g, of u.
+// The saved g and u: their upper halves [T, F], then their next bytes, whose
+// rows are padded to 16 bytes for the copies.
 struct Saved {
   size_t u_hi, g_lo, u_lo, bytes;
+  int64_t pitch;
 };
 Saved saved_layout(int64_t T, int32_t F) {
-  const size_t n = (size_t)T * F;
   Saved s;
-  s.u_hi = round256(2 * n);
-  s.g_lo = s.u_hi + round256(2 * n);
-  s.u_lo = s.g_lo + round256(n);
-  s.bytes = s.u_lo + round256(n);
+  s.pitch = (F + 15) & ~15;
+  s.u_hi = round256((size_t)T * F * 2);
+  s.g_lo = 2 * s.u_hi;
+  s.u_lo = s.g_lo + round256((size_t)T * s.pitch);
+  s.bytes = s.u_lo + round256((size_t)T * s.pitch);
   return s;
+}
+cudaError_t saved_maps(GemmArgs* a, const void* saved, int64_t T, int32_t F) {
+  const Saved s = saved_layout(T, F);
+  const char* p = static_cast<const char*>(saved);
+  cudaError_t e = block_map(&a->g_hi, p, T, F, F, 2);
+  if (e == cudaSuccess) e = block_map(&a->u_hi, p + s.u_hi, T, F, F, 2);
+  if (e == cudaSuccess) e = block_map(&a->g_lo, p + s.g_lo, T, F, s.pitch, 1);
+  if (e == cudaSuccess) e = block_map(&a->u_lo, p + s.u_lo, T, F, s.pitch, 1);
+  return e;
 }
 
 struct FwdPlan {
@@ -784,27 +910,21 @@ int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd,
   if ((e = status_word(&a.status)) != cudaSuccess) return launch_failed(e);
 
   char* ws = static_cast<char*>(workspace);
-  a.h = reinterpret_cast<__nv_bfloat16*>(ws);
-  if (saved) {
-    const Saved s = saved_layout(T, F);
-    char* p = static_cast<char*>(saved);
-    a.g_hi = reinterpret_cast<uint16_t*>(p);
-    a.u_hi = reinterpret_cast<uint16_t*>(p + s.u_hi);
-    a.g_lo = reinterpret_cast<uint8_t*>(p + s.g_lo);
-    a.u_lo = reinterpret_cast<uint8_t*>(p + s.u_lo);
-  }
+  e = block_map(&a.h, ws, T, F, F, 2);
+  if (e == cudaSuccess && saved) e = saved_maps(&a, saved, T, F);
+  if (e != cudaSuccess) return launch_failed(e);
   const Operand none = {};
   a.problems = 1;
   e = set_problem(&a.p[0], {{x, T, D, false}, none}, {{wg, F, D, false}, {wu, F, D, false}}, 1, T, F,
                   128, D, 0, nullptr);
-  if (e == cudaSuccess) e = launch_gemm(a, kGate, act, pairs, st);
+  if (e == cudaSuccess) e = launch_gemm(a, saved ? kGateSave : kGate, act, pairs, st);
   if (e != cudaSuccess) return launch_failed(e);
 
-  e = set_problem(&a.p[0], {{a.h, T, F, false}, none}, {{wd, D, F, false}, none}, 1, T, D, kTN, F, 0, y);
+  e = set_problem(&a.p[0], {{ws, T, F, false}, none}, {{wd, D, F, false}, none}, 1, T, D, kTN, F, 0, y);
   a.p[0].splits = plan.y.splits;
   a.p[0].partial = reinterpret_cast<float*>(ws + round256((size_t)T * F * 2));
   if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, st);
-  if (e == cudaSuccess && plan.y.splits > 1) e = launch_join(a.p[0], st);
+  if (e == cudaSuccess && plan.y.splits > 1) e = launch_join(a.p[0], y, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
 
@@ -838,15 +958,12 @@ int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
 
   const size_t tf = round256((size_t)T * F * 2);
   char* ws = static_cast<char*>(workspace);
-  a.h = reinterpret_cast<__nv_bfloat16*>(ws);
-  a.dg = reinterpret_cast<__nv_bfloat16*>(ws + tf);
-  a.du = reinterpret_cast<__nv_bfloat16*>(ws + 2 * tf);
-  const Saved s = saved_layout(T, F);
-  char* sv = const_cast<char*>(static_cast<const char*>(saved));
-  a.g_hi = reinterpret_cast<uint16_t*>(sv);
-  a.u_hi = reinterpret_cast<uint16_t*>(sv + s.u_hi);
-  a.g_lo = reinterpret_cast<uint8_t*>(sv + s.g_lo);
-  a.u_lo = reinterpret_cast<uint8_t*>(sv + s.u_lo);
+  char *h = ws, *dg = ws + tf, *du = ws + 2 * tf;
+  e = saved_maps(&a, saved, T, F);
+  if (e == cudaSuccess) e = block_map(&a.h, h, T, F, F, 2);
+  if (e == cudaSuccess) e = block_map(&a.dg, dg, T, F, F, 2);
+  if (e == cudaSuccess) e = block_map(&a.du, du, T, F, F, 2);
+  if (e != cudaSuccess) return launch_failed(e);
 
   const Operand none = {};
   a.problems = 1;
@@ -856,9 +973,9 @@ int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
   if (e != cudaSuccess) return launch_failed(e);
 
   // dx first: its units are the longest.
-  const Operand dgk = {a.dg, T, F, false}, duk = {a.du, T, F, false};
-  const Operand dgm = {a.dg, T, F, true}, dum = {a.du, T, F, true};
-  const Operand xm = {x, T, D, true}, dym = {dy, T, D, true}, hm = {a.h, T, F, true};
+  const Operand dgk = {dg, T, F, false}, duk = {du, T, F, false};
+  const Operand dgm = {dg, T, F, true}, dum = {du, T, F, true};
+  const Operand xm = {x, T, D, true}, dym = {dy, T, D, true}, hm = {h, T, F, true};
   a.problems = 4;
   e = set_problem(&a.p[0], {dgk, duk}, {{wg, F, D, true}, {wu, F, D, true}}, 2, T, D, kTN, F, F, dx);
   a.p[0].splits = plan.dx.splits;
@@ -867,7 +984,7 @@ int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
   if (e == cudaSuccess) e = set_problem(&a.p[2], {dum, none}, {xm, none}, 1, F, D, kTN, T, 0, dwu);
   if (e == cudaSuccess) e = set_problem(&a.p[3], {dym, none}, {hm, none}, 1, D, F, kTN, T, 0, dwd);
   if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, st);
-  if (e == cudaSuccess && plan.dx.splits > 1) e = launch_join(a.p[0], st);
+  if (e == cudaSuccess && plan.dx.splits > 1) e = launch_join(a.p[0], dx, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
 

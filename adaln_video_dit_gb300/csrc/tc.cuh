@@ -9,11 +9,6 @@
 namespace adaln {
 
 // ----- cluster ------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -66,6 +61,35 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(m), "r"(x), "r"(y), "r"(bar & 0xFEFFFFFFu)
       : "memory");
+}
+
+// Box of shared memory to a 2-D tensor map at (x, y); what lies outside the
+// tensor is not written.  Grouped per issuing thread: bulk_commit closes a
+// group; bulk_wait_read<N> waits until the shared memory of all groups but the
+// last N may be reused, bulk_wait until all are written.
+__device__ __forceinline__ void tma_store(const CUtensorMap* m, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// Make this thread's shared-memory writes visible to the copies.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 // ----- tensor memory --------------------------------------------------------------
