@@ -45,20 +45,20 @@ constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kTM = 256, kTN = 256;        // tile of a CTA pair
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-// Outputs leave (and the saved values come) through blocks of 32 rows x 32
-// columns in shared memory, copied by TMA: a lane holds a row of its
-// accumulator, and 32 lanes writing 16 bytes each to 32 rows of global memory
-// cost a cache-line lookup per lane (the stores of g, u and h alone took half
-// as long again as the products at D = 1536).
-constexpr int kBlock16 = 32 * 32 * 2, kBlock8 = 32 * 32;
-// A warp's shared memory: kPlain, kGate: two blocks in turn; kGateSave: h, the
-// upper halves and the next bytes of g and u; kGateBwd: the last four, twice.
-ADALN_HD constexpr int staging_bytes(int kind) {
-  return kind == kGateSave ? 3 * kBlock16 + 2 * kBlock8
-         : kind == kGateBwd ? 2 * (2 * kBlock16 + 2 * kBlock8) : 2 * kBlock16;
-}
-// Ring stages that fit beside it.
-ADALN_HD constexpr int stages_of(int kind) { return kind == kGateBwd ? 4 : kind == kGateSave ? 5 : 6; }
+// Outputs leave through blocks of 32 rows x 32 columns in shared memory, copied
+// by TMA: a lane holds a row of its accumulator, and 32 lanes writing 16 bytes
+// each to 32 rows of global memory cost a cache-line lookup per lane (the stores
+// of g, u and h alone took half as long again as the products at D = 1536).
+constexpr int kBlock = 32 * 32 * 2;
+// A warp's shared memory: dg, du and h for kGateBwd, two blocks in turn for the
+// others; and the ring stages that fit beside it.
+ADALN_HD constexpr int staging_bytes(int kind) { return (kind == kGateBwd ? 3 : 2) * kBlock; }
+ADALN_HD constexpr int stages_of(int kind) { return kind == kGateBwd ? 5 : 6; }
+// The saved g and u are only ever read by the backward's epilogue, so they lie
+// in its order: for each 32 x 32 block twelve rows of 32 lanes x 16 bytes (g:
+// four of upper halves, two of the next bytes; then u), each one coalesced
+// access of a warp.
+constexpr int kSavedVecs = 12, kSavedBlock = kSavedVecs * 512;
 constexpr int smem_of(int kind) {
   return 1024 + stages_of(kind) * kStageBytes + kEpiWarps * staging_bytes(kind) + 256;
 }
@@ -79,9 +79,9 @@ struct Problem {       // C[M, N] = sum over its K segments of A B
 struct GemmArgs {
   Problem p[kMaxProblems];
   int problems, units;
-  // Gate epilogues ([T, F] each): products, and the saved g and u (upper 16
-  // bits, next 8).
-  CUtensorMap h, dg, du, g_hi, u_hi, g_lo, u_lo;
+  // Gate epilogues ([T, F] each).
+  CUtensorMap h, dg, du;
+  uint4* saved;
   unsigned* status;
 };
 
@@ -140,51 +140,43 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Byte offset of 16-byte piece `i` of row `r` in a block of 64-byte rows (the
-// 64-byte swizzle) and of 32-byte rows (the 32-byte one) of a tensor map.
-__device__ __forceinline__ uint32_t at16(int r, int i) { return r * 64 + ((i ^ (r >> 1 & 3)) << 4); }
-__device__ __forceinline__ uint32_t at8(int r, int i) { return r * 32 + ((i ^ (r >> 2 & 1)) << 4); }
-
-// This lane's row of 32 values into a block: 16 words of bf16 pairs.
-__device__ __forceinline__ void put_row16(uint32_t block, int lane, const uint32_t (&w)[16]) {
+// This lane's row of 32 values, as 16 words of bf16 pairs, into a block (rows
+// of 64 bytes, swizzled as a tensor map of that width has them).
+__device__ __forceinline__ void put_row(uint32_t block, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    st_shared_v4(block + at16(lane, i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    st_shared_v4(block + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4), w[4 * i], w[4 * i + 1],
+                 w[4 * i + 2], w[4 * i + 3]);
+}
+
+// Where block (row0 / 32, col / 32) of the saved g and u starts, for this lane.
+__device__ __forceinline__ uint4* saved_at(uint4* saved, int row0, int col, int N, int lane) {
+  return saved + ((int64_t)(row0 >> 5) * ((N + 31) >> 5) + (col >> 5)) * (kSavedBlock / 16) + lane;
 }
 
 // 32 fp32 values of a row as their upper 16 bits and their next 8.
-__device__ __forceinline__ void put_saved(uint32_t hi, uint32_t lo, int lane,
-                                          const uint32_t (&v)[32]) {
-  uint32_t w[16], b[8];
+__device__ __forceinline__ void save_row(uint4* to, const uint32_t (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = __byte_perm(v[2 * i], v[2 * i + 1], 0x7632);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    b[i] = __byte_perm(__byte_perm(v[4 * i], v[4 * i + 1], 0x51),
-                       __byte_perm(v[4 * i + 2], v[4 * i + 3], 0x51), 0x5410);
-  put_row16(hi, lane, w);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    st_shared_v4(lo + at8(lane, i), b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
-}
-
-// And back: value i from word i / 2 of the upper halves, byte i of the rest.
-__device__ __forceinline__ float saved_value(const uint32_t (&w)[16], const uint32_t (&b)[8], int i) {
-  return __uint_as_float((i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) |
-                         (b[i / 4] >> (8 * (i % 4)) & 0xff) << 8);
-}
-__device__ __forceinline__ void get_saved(uint32_t hi, uint32_t lo, int lane, uint32_t (&w)[16],
-                                          uint32_t (&b)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = ld_shared_v4(hi + at16(lane, i));
-    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-  }
+  for (int i = 0; i < 4; ++i)
+    st_global_cs_v4(to + 32 * i, make_uint4(__byte_perm(v[8 * i], v[8 * i + 1], 0x7632),
+                                            __byte_perm(v[8 * i + 2], v[8 * i + 3], 0x7632),
+                                            __byte_perm(v[8 * i + 4], v[8 * i + 5], 0x7632),
+                                            __byte_perm(v[8 * i + 6], v[8 * i + 7], 0x7632)));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint4 v = ld_shared_v4(lo + at8(lane, i));
-    b[4 * i] = v.x, b[4 * i + 1] = v.y, b[4 * i + 2] = v.z, b[4 * i + 3] = v.w;
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t* x = &v[16 * i + 4 * j];
+      b[j] = __byte_perm(__byte_perm(x[0], x[1], 0x51), __byte_perm(x[2], x[3], 0x51), 0x5410);
+    }
+    st_global_cs_v4(to + 32 * (4 + i), make_uint4(b[0], b[1], b[2], b[3]));
   }
+}
+// And back: value e (0..7) of upper halves w, their next bytes in b0 (0..3), b1.
+__device__ __forceinline__ float saved_value(const uint4& w, uint32_t b0, uint32_t b1, int e) {
+  const uint32_t x = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w, b = e < 4 ? b0 : b1;
+  return __uint_as_float((e % 2 ? x & 0xffff0000u : x << 16) | (b >> (8 * (e % 4)) & 0xff) << 8);
 }
 
 // ----- epilogues: one warp's 32 rows x half of the tile's columns -----------------
@@ -217,11 +209,11 @@ __device__ __forceinline__ void epilogue_plain(const Unit& u, uint32_t acc, int 
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         w[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-      const uint32_t block = buf + turn * kBlock16;
+      const uint32_t block = buf + turn * kBlock;
       turn ^= 1;
       bulk_wait_read<1>();  // the copy before the last one used this block
       __syncwarp();
-      put_row16(block, lane, w);
+      put_row(block, lane, w);
       fence_async_shared();
       __syncwarp();
       if (elect_one()) {
@@ -259,84 +251,86 @@ __device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Unit& u, 
       }
       w[i] = pack_bf16(h[0], h[1]);
     }
-    bulk_wait_read<SAVE ? 0 : 1>();
-    __syncwarp();
-    const uint32_t block = SAVE ? buf : buf + turn * kBlock16;
+    const uint32_t block = buf + turn * kBlock;
     turn ^= 1;
-    const uint32_t gh = buf + kBlock16, uh = gh + kBlock16, gl = uh + kBlock16, ul = gl + kBlock8;
-    put_row16(block, lane, w);
-    if (SAVE) {
-      put_saved(gh, gl, lane, g);
-      put_saved(uh, ul, lane, v);
-    }
+    bulk_wait_read<1>();  // the copy before the last one used this block
+    __syncwarp();
+    put_row(block, lane, w);
     fence_async_shared();
     __syncwarp();
     if (elect_one()) {
-      if (row0 < M) {
-        tma_store(&a.h, col, row0, block);
-        if (SAVE) {
-          tma_store(&a.g_hi, col, row0, gh);
-          tma_store(&a.u_hi, col, row0, uh);
-          tma_store(&a.g_lo, col, row0, gl);
-          tma_store(&a.u_lo, col, row0, ul);
-        }
-      }
+      if (row0 < M) tma_store(&a.h, col, row0, block);
       bulk_commit();
     }
+    if (SAVE && row0 < M) {
+      uint4* to = saved_at(a.saved, row0, col, N, lane);
+      save_row(to, g);
+      save_row(to + 32 * (kSavedVecs / 2), v);
+    }
   }
 }
 
-// The saved g and u of a chunk of the gate's gradient, into half `b` of the
-// warp's staging memory.
-__device__ __forceinline__ void load_saved(const GemmArgs& a, int col, int row0, uint32_t buf,
-                                           uint32_t bar) {
-  mbar_arrive_expect_tx(bar, 2 * kBlock16 + 2 * kBlock8);
-  tma_load(buf, &a.g_hi, col, row0, bar);
-  tma_load(buf + kBlock16, &a.u_hi, col, row0, bar);
-  tma_load(buf + 2 * kBlock16, &a.g_lo, col, row0, bar);
-  tma_load(buf + 2 * kBlock16 + kBlock8, &a.u_lo, col, row0, bar);
-}
+// The saved values of one chunk, a lane's twelve vectors.
+struct SavedRow {
+  uint4 v[kSavedVecs];
+  __device__ __forceinline__ void load(const uint4* p, int i) {
+    if (p != nullptr) v[i] = __ldcs(p + 32 * i);
+  }
+};
 
-// One chunk of the gate's gradient: the accumulator's dh with the g and u in
-// `buf`, whose place dg, du and h (over the two byte blocks) take.
+// One chunk of the gate's gradient: dh from the accumulator with g and u from
+// `in`, which takes the next chunk's values (at `next`, or none) as soon as
+// its own are used.
 template <int ACT>
 __device__ __forceinline__ void chunk_gate_bwd(const GemmArgs& a, uint32_t acc, int col, int row0,
-                                               int M, uint32_t buf, int lane) {
-  const uint32_t gh = buf, uh = buf + kBlock16, gl = buf + 2 * kBlock16, ul = gl + kBlock8;
-  uint32_t gw[16], gb[8], uw[16], ub[8], r[32];
+                                               int M, uint32_t buf, int lane, SavedRow& in,
+                                               const uint4* next) {
+  uint32_t r[32], wg[16], wu[16], wh[16];
+  __syncwarp();
   tmem_ld32(acc, r);
-  get_saved(gh, gl, lane, gw, gb);
-  get_saved(uh, ul, lane, uw, ub);
   tc_wait_ld();
-  __syncwarp();  // h goes where other lanes' bytes were
-  uint32_t h[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float dg[2], du[2], hv[2];
+  for (int j = 0; j < 4; ++j) {  // 8 columns
+    const uint4 gb = in.v[4 + j / 2], ub = in.v[10 + j / 2];
+    const uint32_t g0 = j % 2 ? gb.z : gb.x, g1 = j % 2 ? gb.w : gb.y;
+    const uint32_t u0 = j % 2 ? ub.z : ub.x, u1 = j % 2 ? ub.w : ub.y;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x = saved_value(gw, gb, 2 * i + e), w = saved_value(uw, ub, 2 * i + e);
-      const float dh = __uint_as_float(r[2 * i + e]);
-      float s, d;
-      gate<ACT>(x, s, d);
-      dg[e] = dh * w * d;
-      du[e] = dh * (x * s);
-      hv[e] = x * s * w;
+    for (int i = 0; i < 4; ++i) {
+      float dg[2], du[2], h[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = saved_value(in.v[j], g0, g1, 2 * i + e);
+        const float w = saved_value(in.v[6 + j], u0, u1, 2 * i + e);
+        const float dh = __uint_as_float(r[8 * j + 2 * i + e]);
+        float s, d;
+        gate<ACT>(x, s, d);
+        dg[e] = dh * w * d;
+        du[e] = dh * (x * s);
+        h[e] = x * s * w;
+      }
+      wg[4 * j + i] = pack_bf16(dg[0], dg[1]);
+      wu[4 * j + i] = pack_bf16(du[0], du[1]);
+      wh[4 * j + i] = pack_bf16(h[0], h[1]);
     }
-    gw[i] = pack_bf16(dg[0], dg[1]);
-    uw[i] = pack_bf16(du[0], du[1]);
-    h[i] = pack_bf16(hv[0], hv[1]);
+    in.load(next, j);
+    in.load(next, 6 + j);
+    if (j % 2) {
+      in.load(next, 4 + j / 2);
+      in.load(next, 10 + j / 2);
+    }
   }
-  put_row16(gh, lane, gw);
-  put_row16(uh, lane, uw);
-  put_row16(gl, lane, h);
+  bulk_wait_read<0>();  // the previous chunk's copies used these blocks
+  __syncwarp();
+  put_row(buf, lane, wg);
+  put_row(buf + kBlock, lane, wu);
+  put_row(buf + 2 * kBlock, lane, wh);
   fence_async_shared();
   __syncwarp();
   if (elect_one()) {
     if (row0 < M) {
-      tma_store(&a.dg, col, row0, gh);
-      tma_store(&a.du, col, row0, uh);
-      tma_store(&a.h, col, row0, gl);
+      tma_store(&a.dg, col, row0, buf);
+      tma_store(&a.du, col, row0, buf + kBlock);
+      tma_store(&a.h, col, row0, buf + 2 * kBlock);
     }
     bulk_commit();
   }
@@ -359,8 +353,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_ptr = bars + 8 * (2 * kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(
       smem_raw + (bars - smem_addr(smem_raw)) + 8 * (2 * kStages + 6));
-  // kGateBwd: saved values landed, two per epilogue warp.
-  auto saved_full = [&](int w, int b) { return bars + 8 * (2 * kStages + 7 + 2 * w + b); };
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;  // within the pair
@@ -376,8 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(acc_empty(i), 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
-    if (KIND == kGateBwd)
-      for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(saved_full(i >> 1, i & 1), 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -498,22 +488,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_parity = 0;
     bool ok = true;
     // kGateBwd: chunks of 32 columns, in the order of the units; chunk c of a
-    // unit exists if it starts before the last column.  One is loaded ahead.
+    // unit exists if it starts before the last column.  The saved values are
+    // read one chunk ahead: `ahead` walks the same order.
     auto col_of = [&](const Unit& u, int c) { return u.n * kTN + half * 128 + c * 32; };
-    int chunk = 0, ahead = cluster, ahead_c = 0;
-    auto load_ahead = [&](int b) {  // the chunk at or after (ahead, ahead_c), if any
+    int ahead = cluster, ahead_c = 0;
+    auto next_saved = [&]() -> const uint4* {  // of the chunk at or after (ahead, ahead_c)
       for (; ahead < a.units; ahead += clusters, ahead_c = 0) {
         const Unit u = unit_of(a, ahead);
-        if (ahead_c < 4 && col_of(u, ahead_c) < u.p->N) {
-          if (elect_one())
-            load_saved(a, col_of(u, ahead_c), u.m * kTM + row_in,
-                       buf + b * (staging_bytes(KIND) / 2), saved_full(warp - 2, b));
+        const int col = col_of(u, ahead_c), row0 = u.m * kTM + row_in;
+        if (ahead_c < 4 && col < u.p->N) {
           ++ahead_c;
-          return;
+          return row0 < u.p->M ? saved_at(a.saved, row0, col, u.p->N, lane) : nullptr;
         }
       }
+      return nullptr;
     };
-    if (KIND == kGateBwd) load_ahead(0);
+    SavedRow in = {};
+    if (KIND == kGateBwd) {
+      const uint4* p = next_saved();
+#pragma unroll
+      for (int i = 0; i < kSavedVecs; ++i) in.load(p, i);
+    }
     for (int ui = cluster; ok && ui < a.units; ui += clusters) {
       const Unit u = unit_of(a, ui);
       if (!(ok = __all_sync(~0u, wait(acc_full(acc), acc_parity)))) break;
@@ -527,16 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int M = u.p->M, N = u.p->N;
 #pragma unroll 1
-        for (int c = 0; c < 4 && col_of(u, c) < N; ++c, ++chunk) {
-          const int b = chunk & 1;
-          // The other half is free once the copies out of it are done.
-          bulk_wait_read<0>();
-          __syncwarp();
-          load_ahead(b ^ 1);
-          if (!(ok = __all_sync(~0u, wait(saved_full(warp - 2, b), chunk >> 1 & 1)))) break;
-          chunk_gate_bwd<ACT>(a, at + half * 128 + c * 32, col_of(u, c), row0, M,
-                              buf + b * (staging_bytes(KIND) / 2), lane);
-        }
+        for (int c = 0; c < 4 && col_of(u, c) < N; ++c)
+          chunk_gate_bwd<ACT>(a, at + half * 128 + c * 32, col_of(u, c), row0, M, buf, lane, in,
+                              next_saved());
       }
       tc_fence_before();
       __syncwarp();
@@ -545,9 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (acc == 0) acc_parity ^= 1;
     }
     bulk_wait();
-    if (KIND == kGateBwd && !ok)  // loads may be in flight: wait for them, with a limit
-      for (int i = chunk; i < chunk + 2; ++i)
-        mbar_wait_bounded(saved_full(warp - 2, i & 1), i >> 1 & 1, nullptr, kDrainLimitNs);
   }
   __syncwarp();
   tc_fence_before();
@@ -601,24 +586,21 @@ cudaError_t encode_fn(EncodeFn* out) {
   return cudaSuccess;
 }
 
-// Tensor map of a row-major matrix [rows, cols] of `es`-byte elements (2:
-// bf16, 1: bytes), rows `pitch` elements apart, in boxes of box_cols x
-// box_rows whose rows of 128, 64 or 32 bytes are swizzled at that width.  What
+// Tensor map of a row-major bf16 matrix [rows, cols] in boxes of box_cols (64
+// or 32: rows of 128 or 64 bytes, swizzled at that width) x box_rows.  What
 // lies outside reads as zero and is not written.
-cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch,
-                     int es, int box_cols, int box_rows) {
+cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_cols,
+                     int box_rows) {
   EncodeFn fn;
   const cudaError_t e = encode_fn(&fn);
   if (e != cudaSuccess) return e;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)pitch * es};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
-  const CUtensorMapSwizzle swizzle = box_cols * es == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                           : CU_TENSOR_MAP_SWIZZLE_32B;
   const CUresult r =
-      fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-         const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+      fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, one,
+         CU_TENSOR_MAP_INTERLEAVE_NONE,
+         box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -631,12 +613,11 @@ struct Operand {
   bool mn;
 };
 cudaError_t operand_map(CUtensorMap* m, const Operand& o) {
-  return make_map(m, o.p, o.rows, o.cols, o.cols, 2, 64, o.mn ? kBK : 128);
+  return make_map(m, o.p, o.rows, o.cols, 64, o.mn ? kBK : 128);
 }
 // Blocks of 32 x 32 of an epilogue.
-cudaError_t block_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch,
-                      int es) {
-  return make_map(m, p, rows, cols, pitch, es, 32, 32);
+cudaError_t block_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
+  return make_map(m, p, rows, cols, 32, 32);
 }
 
 template <int KIND>
@@ -756,7 +737,7 @@ cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2]
     e = operand_map(&p->a[i], have_a ? a[i] : a[0]);
     if (e == cudaSuccess) e = operand_map(&p->b[i], have_b ? b[i] : b[0]);
   }
-  if (e == cudaSuccess && out) e = block_map(&p->out, out, M, N, N, 2);
+  if (e == cudaSuccess && out) e = block_map(&p->out, out, M, N);
   p->partial = nullptr;
   p->M = (int)M;
   p->N = N;
@@ -812,29 +793,8 @@ int check(int64_t T, int32_t D, int32_t F, adaln_dtype_t dt, int act) {
   return ADALN_OK;
 }
 
-// The saved g and u: their upper halves [T, F], then their next bytes, whose
-// rows are padded to 16 bytes for the copies.
-struct Saved {
-  size_t u_hi, g_lo, u_lo, bytes;
-  int64_t pitch;
-};
-Saved saved_layout(int64_t T, int32_t F) {
-  Saved s;
-  s.pitch = (F + 15) & ~15;
-  s.u_hi = round256((size_t)T * F * 2);
-  s.g_lo = 2 * s.u_hi;
-  s.u_lo = s.g_lo + round256((size_t)T * s.pitch);
-  s.bytes = s.u_lo + round256((size_t)T * s.pitch);
-  return s;
-}
-cudaError_t saved_maps(GemmArgs* a, const void* saved, int64_t T, int32_t F) {
-  const Saved s = saved_layout(T, F);
-  const char* p = static_cast<const char*>(saved);
-  cudaError_t e = block_map(&a->g_hi, p, T, F, F, 2);
-  if (e == cudaSuccess) e = block_map(&a->u_hi, p + s.u_hi, T, F, F, 2);
-  if (e == cudaSuccess) e = block_map(&a->g_lo, p + s.g_lo, T, F, s.pitch, 1);
-  if (e == cudaSuccess) e = block_map(&a->u_lo, p + s.u_lo, T, F, s.pitch, 1);
-  return e;
+size_t saved_bytes(int64_t T, int32_t F) {
+  return (size_t)div_up(T, 32) * div_up(F, 32) * kSavedBlock;
 }
 
 struct FwdPlan {
@@ -873,7 +833,7 @@ int adaln_ffn_saved_size(int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype, s
   const int rc = check(T, D, F, dtype, ADALN_ACT_SILU);
   if (rc != ADALN_OK) return rc;
   if (!bytes) return ADALN_ERR_NULL;
-  *bytes = saved_layout(T, F).bytes;
+  *bytes = saved_bytes(T, F);
   return ADALN_OK;
 }
 
@@ -910,8 +870,8 @@ int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd,
   if ((e = status_word(&a.status)) != cudaSuccess) return launch_failed(e);
 
   char* ws = static_cast<char*>(workspace);
-  e = block_map(&a.h, ws, T, F, F, 2);
-  if (e == cudaSuccess && saved) e = saved_maps(&a, saved, T, F);
+  a.saved = static_cast<uint4*>(saved);
+  e = block_map(&a.h, ws, T, F);
   if (e != cudaSuccess) return launch_failed(e);
   const Operand none = {};
   a.problems = 1;
@@ -959,10 +919,10 @@ int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
   const size_t tf = round256((size_t)T * F * 2);
   char* ws = static_cast<char*>(workspace);
   char *h = ws, *dg = ws + tf, *du = ws + 2 * tf;
-  e = saved_maps(&a, saved, T, F);
-  if (e == cudaSuccess) e = block_map(&a.h, h, T, F, F, 2);
-  if (e == cudaSuccess) e = block_map(&a.dg, dg, T, F, F, 2);
-  if (e == cudaSuccess) e = block_map(&a.du, du, T, F, F, 2);
+  a.saved = static_cast<uint4*>(const_cast<void*>(saved));  // read only here
+  e = block_map(&a.h, h, T, F);
+  if (e == cudaSuccess) e = block_map(&a.dg, dg, T, F);
+  if (e == cudaSuccess) e = block_map(&a.du, du, T, F);
   if (e != cudaSuccess) return launch_failed(e);
 
   const Operand none = {};

@@ -19,8 +19,11 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// Relaxed: for hand-overs of tensor memory, which tcgen05.wait::ld and the
+// tcgen05 fences order.  A release at cluster scope would wait here until this
+// thread's global stores are performed.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mapped) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped)
                : "memory");
 }
 

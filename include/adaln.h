@@ -314,7 +314,8 @@ typedef enum {
 
 /*
  * Device bytes: of what a forward saves for its backward (x Wg' and x Wu' at
- * 24 bits a value: about 6 T F bytes), and of each call's workspace on the current
+ * 24 bits a value, in blocks of 32 tokens: 6 F bytes
+ * a token), and of each call's workspace on the current
  * device (either pointer of the second may be NULL).
  */
 ADALN_API int adaln_ffn_saved_size(int64_t T, int32_t D, int32_t F, adaln_dtype_t dtype,
