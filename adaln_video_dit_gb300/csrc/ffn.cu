@@ -65,15 +65,19 @@ constexpr int smem_of(int kind) {
 constexpr int kGroupM = 8;                 // tile rows walked together (L2 reuse)
 constexpr int kMaxProblems = 4;
 
-struct Problem {       // C[M, N] = sum over its K segments of A B
-  CUtensorMap a[2], b[2];
-  CUtensorMap out;     // bf16 [M, N]
-  float* partial;      // fp32 [splits][M][N] when splits > 1
+// C[M, N] = sum over its K segments of A B.
+struct Dims {        // what the roles of a CTA read of a problem
   int M, N;
   int kb0, kb;         // k blocks of segment 0, of both
   int tiles_m, tiles_n, splits;
   int first;           // first unit of the problem
   int a_mn, b_mn;      // operand layouts
+};
+struct Problem {
+  CUtensorMap a[2], b[2];
+  CUtensorMap out;     // bf16 [M, N]
+  float* partial;      // fp32 [splits][M][N] when splits > 1
+  Dims s;
 };
 
 struct GemmArgs {
@@ -86,28 +90,35 @@ struct GemmArgs {
 };
 
 struct Unit {
-  const Problem* p;
+  int i;           // problem
   int m, n;        // tile
   int k0, k1;      // k blocks
   int split;
 };
 
-__device__ __forceinline__ Unit unit_of(const GemmArgs& a, int u) {
-  int i = 0;
-  while (i + 1 < a.problems && u >= a.p[i + 1].first) ++i;
+// `shapes` is the problems' copy in shared memory (reads of the kernel's
+// parameters with an index cost several hundred cycles each).
+__device__ __forceinline__ Unit unit_of(const Dims* shapes, int problems, int u) {
   Unit r;
-  r.p = &a.p[i];
-  u -= r.p->first;
-  r.split = u % r.p->splits;
-  const int tile = u / r.p->splits;
-  const int per_group = kGroupM * r.p->tiles_n;
-  const int m0 = tile / per_group * kGroupM;
-  const int rows = min(kGroupM, r.p->tiles_m - m0);
-  const int in = tile % per_group;
-  r.m = m0 + in % rows;
+  r.i = 0;
+  while (r.i + 1 < problems && u >= shapes[r.i + 1].first) ++r.i;
+  const Dims& s = shapes[r.i];
+  u -= s.first;
+  r.split = 0;
+  int tile = u;
+  r.k0 = 0;
+  r.k1 = s.kb;
+  if (s.splits > 1) {
+    tile = u / s.splits;
+    r.split = u - tile * s.splits;
+    r.k0 = (int)((int64_t)s.kb * r.split / s.splits);
+    r.k1 = (int)((int64_t)s.kb * (r.split + 1) / s.splits);
+  }
+  const int per_group = kGroupM * s.tiles_n;
+  const int group = tile / per_group, in = tile - group * per_group;
+  const int rows = min(kGroupM, s.tiles_m - group * kGroupM);
   r.n = in / rows;
-  r.k0 = (int)((int64_t)r.p->kb * r.split / r.p->splits);
-  r.k1 = (int)((int64_t)r.p->kb * (r.split + 1) / r.p->splits);
+  r.m = group * kGroupM + in - r.n * rows;
   return r;
 }
 
@@ -183,10 +194,10 @@ __device__ __forceinline__ float saved_value(const uint4& w, uint32_t b0, uint32
 // `row0` is the warp's first row of the output, `half` its column half, `acc`
 // its lanes of the accumulator, `buf` its staging memory.
 
-__device__ __forceinline__ void epilogue_plain(const Unit& u, uint32_t acc, int row0, int half,
-                                               uint32_t buf, int lane, int& turn) {
-  const Problem& p = *u.p;
-  const int M = p.M, N = p.N, splits = p.splits;
+__device__ __forceinline__ void epilogue_plain(const Problem& p, const Dims& s, const Unit& u,
+                                               uint32_t acc, int row0, int half, uint32_t buf,
+                                               int lane, int& turn) {
+  const int M = s.M, N = s.N, splits = s.splits;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const int col = u.n * kTN + half * 128 + c * 32;
@@ -225,10 +236,10 @@ __device__ __forceinline__ void epilogue_plain(const Unit& u, uint32_t acc, int 
 }
 
 template <int ACT, bool SAVE>
-__device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Unit& u, uint32_t acc,
-                                              int row0, int half, uint32_t buf, int lane,
-                                              int& turn) {
-  const int M = u.p->M, N = u.p->N;
+__device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Dims& s, const Unit& u,
+                                              uint32_t acc, int row0, int half, uint32_t buf,
+                                              int lane, int& turn) {
+  const int M = s.M, N = s.N;
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const int col = u.n * 128 + half * 64 + c * 32;
@@ -245,9 +256,9 @@ __device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Unit& u, 
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float x = __uint_as_float(g[2 * i + j]);
-        float s, d;
-        gate<ACT>(x, s, d);
-        h[j] = x * s * __uint_as_float(v[2 * i + j]);
+        float p, d;
+        gate<ACT>(x, p, d);
+        h[j] = x * p * __uint_as_float(v[2 * i + j]);
       }
       w[i] = pack_bf16(h[0], h[1]);
     }
@@ -342,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kStages = stages_of(KIND);
   constexpr bool kIsGate = KIND == kGate || KIND == kGateSave;
   extern __shared__ unsigned char smem_raw[];
+  __shared__ Dims shapes[kMaxProblems];
   const uint32_t ring = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t staging = ring + kStages * kStageBytes;
   const uint32_t bars = staging + kEpiWarps * staging_bytes(KIND);
@@ -371,6 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  if (threadIdx.x >= 32 && threadIdx.x < 32 + kMaxProblems)
+    shapes[threadIdx.x - 32] = a.p[threadIdx.x - 32].s;
   if (warp == 2) tmem_alloc<2>(tmem_ptr, 512);
   tc_fence_before();
   __syncthreads();
@@ -382,6 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_wait();
   grid_launch_dependents();
 
+  const int units = a.units, problems = a.problems;
+  auto unit = [&](int ui) { return unit_of(shapes, problems, min(ui, units - 1)); };
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (mbar_wait_spin(bar, parity, abort_flag)) return true;
     *abort_flag = 1;
@@ -394,15 +410,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t parity = 0;
     bool ok = true;
-    for (int ui = cluster; ok && ui < a.units; ui += clusters) {
-      const Unit u = unit_of(a, ui);
+    Unit next = unit(cluster);
+    for (int ui = cluster; ok && ui < units; ui += clusters) {
+      const Unit u = next;
       // In registers before the loop: after each asm with a memory clobber
-      // the parameters would be read again.
-      const Problem& p = *u.p;
+      // they would be read again.
+      const Problem& p = a.p[u.i];
+      const Dims& sh = shapes[u.i];
       const int m = u.m * kTM + (int)rank * 128;
       const int n = kIsGate ? u.n * 128 : u.n * kTN + (int)rank * 128;
-      const int kb0 = p.kb0;
-      const bool a_mn = p.a_mn, b_mn = p.b_mn;
+      const int kb0 = sh.kb0;
+      const bool a_mn = sh.a_mn, b_mn = sh.b_mn;
       const CUtensorMap* const maps_a = p.a;
       const CUtensorMap* const maps_b = p.b + (kIsGate ? (int)rank : 0);
       for (int kb = u.k0; kb < u.k1; ++kb) {
@@ -430,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_pair(db, mb, k, n, full(s));
           }
         }
+        if (kb == u.k0) next = unit(ui + clusters);  // decoded under the copies
         if (++s == kStages) {
           s = 0;
           parity ^= 1;
@@ -447,9 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0, acc = 0;
     uint32_t parity = 0, acc_parity = 0;
     bool ok = true;
-    for (int ui = cluster; ok && ui < a.units; ui += clusters) {
-      const Unit u = unit_of(a, ui);
-      const bool a_mn = u.p->a_mn, b_mn = u.p->b_mn;
+    Unit next = unit(cluster);
+    for (int ui = cluster; ok && ui < units; ui += clusters) {
+      const Unit u = next;
+      const bool a_mn = shapes[u.i].a_mn, b_mn = shapes[u.i].b_mn;
       const uint32_t idesc = instr_desc(kTM, kTN, a_mn, b_mn);
       const uint32_t step_a = k_step_bytes(a_mn) >> 4, step_b = k_step_bytes(b_mn) >> 4;
       if (!(ok = __all_sync(~0u, wait(acc_empty(acc), acc_parity ^ 1)))) break;
@@ -467,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit<2>(empty(s));
           if (kb + 1 == u.k1) tc_commit<2>(acc_full(acc));
         }
+        if (kb == u.k0) next = unit(ui + clusters);  // decoded under the products
         if (++s == kStages) {
           s = 0;
           parity ^= 1;
@@ -487,44 +508,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0, turn = 0;
     uint32_t acc_parity = 0;
     bool ok = true;
-    // kGateBwd: chunks of 32 columns, in the order of the units; chunk c of a
-    // unit exists if it starts before the last column.  The saved values are
-    // read one chunk ahead: `ahead` walks the same order.
+    // kGateBwd: this warp's chunks of 32 columns of a unit: chunk c exists if it
+    // starts before the last column.  The saved values are read one chunk
+    // ahead, into the next unit that has one.
     auto col_of = [&](const Unit& u, int c) { return u.n * kTN + half * 128 + c * 32; };
-    int ahead = cluster, ahead_c = 0;
-    auto next_saved = [&]() -> const uint4* {  // of the chunk at or after (ahead, ahead_c)
-      for (; ahead < a.units; ahead += clusters, ahead_c = 0) {
-        const Unit u = unit_of(a, ahead);
-        const int col = col_of(u, ahead_c), row0 = u.m * kTM + row_in;
-        if (ahead_c < 4 && col < u.p->N) {
-          ++ahead_c;
-          return row0 < u.p->M ? saved_at(a.saved, row0, col, u.p->N, lane) : nullptr;
-        }
+    auto saved_of = [&](const Unit& u) -> const uint4* {  // of the unit's first chunk
+      const Dims& s = shapes[u.i];
+      const int row0 = u.m * kTM + row_in;
+      return row0 < s.M ? saved_at(a.saved, row0, col_of(u, 0), s.N, lane) : nullptr;
+    };
+    // First unit from `ui` on with a chunk for this warp (>= units: none).
+    auto seek = [&](int ui, Unit& u) {
+      for (; ui < units; ui += clusters) {
+        u = unit(ui);
+        if (col_of(u, 0) < shapes[u.i].N) break;
       }
-      return nullptr;
+      return ui;
     };
     SavedRow in = {};
+    const uint4* at_saved = nullptr;  // of the next unit's first chunk
     if (KIND == kGateBwd) {
-      const uint4* p = next_saved();
+      Unit u;
+      if (seek(cluster, u) < units) at_saved = saved_of(u);
 #pragma unroll
-      for (int i = 0; i < kSavedVecs; ++i) in.load(p, i);
+      for (int i = 0; i < kSavedVecs; ++i) in.load(at_saved, i);
     }
-    for (int ui = cluster; ok && ui < a.units; ui += clusters) {
-      const Unit u = unit_of(a, ui);
+    Unit next = unit(cluster);
+    for (int ui = cluster; ok && ui < units; ui += clusters) {
+      const Unit u = next;
+      next = unit(ui + clusters);
+      const Dims& sh = shapes[u.i];
+      const uint4* here = at_saved;
+      if (KIND == kGateBwd && col_of(u, 0) < sh.N) {
+        Unit v;
+        at_saved = seek(ui + clusters, v) < units ? saved_of(v) : nullptr;
+      }
       if (!(ok = __all_sync(~0u, wait(acc_full(acc), acc_parity)))) break;
       tc_fence_after();
       const int row0 = u.m * kTM + row_in;
       const uint32_t at = tmem + acc * kTN + ((uint32_t)lanes << 16);
       if constexpr (KIND == kPlain) {
-        epilogue_plain(u, at, row0, half, buf, lane, turn);
+        epilogue_plain(a.p[u.i], sh, u, at, row0, half, buf, lane, turn);
       } else if constexpr (kIsGate) {
-        epilogue_gate<ACT, KIND == kGateSave>(a, u, at, row0, half, buf, lane, turn);
+        epilogue_gate<ACT, KIND == kGateSave>(a, sh, u, at, row0, half, buf, lane, turn);
       } else {
-        const int M = u.p->M, N = u.p->N;
+        const int M = sh.M, N = sh.N;
 #pragma unroll 1
-        for (int c = 0; c < 4 && col_of(u, c) < N; ++c)
+        for (int c = 0; c < 4 && col_of(u, c) < N; ++c) {
+          const bool last = c == 3 || col_of(u, c + 1) >= N;
+          if (here != nullptr) here += kSavedBlock / 16;
           chunk_gate_bwd<ACT>(a, at + half * 128 + c * 32, col_of(u, c), row0, M, buf, lane, in,
-                              next_saved());
+                              last ? at_saved : here);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -739,24 +774,26 @@ cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2]
   }
   if (e == cudaSuccess && out) e = block_map(&p->out, out, M, N);
   p->partial = nullptr;
-  p->M = (int)M;
-  p->N = N;
-  p->kb0 = div_up(k0, kBK);
-  p->kb = p->kb0 + (segs > 1 ? div_up(k1, kBK) : 0);
-  p->tiles_m = div_up(M, kTM);
-  p->tiles_n = div_up(N, tn);
-  p->splits = 1;
-  p->first = 0;
-  p->a_mn = a[0].mn;
-  p->b_mn = b[0].mn;
+  Dims& s = p->s;
+  s.M = (int)M;
+  s.N = N;
+  s.kb0 = div_up(k0, kBK);
+  s.kb = s.kb0 + (segs > 1 ? div_up(k1, kBK) : 0);
+  s.tiles_m = div_up(M, kTM);
+  s.tiles_n = div_up(N, tn);
+  s.splits = 1;
+  s.first = 0;
+  s.a_mn = a[0].mn;
+  s.b_mn = b[0].mn;
   return e;
 }
 
 cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, cudaStream_t st) {
   int at = 0;
   for (int i = 0; i < a.problems; ++i) {
-    a.p[i].first = at;
-    at += a.p[i].tiles_m * a.p[i].tiles_n * a.p[i].splits;
+    Dims& s = a.p[i].s;
+    s.first = at;
+    at += s.tiles_m * s.tiles_n * s.splits;
   }
   a.units = at;
   const int grid = 2 * (at < pairs ? at : pairs);
@@ -768,8 +805,8 @@ cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, cudaStream_t 
 
 cudaError_t launch_join(const Problem& p, void* to, cudaStream_t st) {
   const float* partial = p.partial;
-  int splits = p.splits;
-  int64_t vecs = (int64_t)p.M * p.N / 4;
+  int splits = p.s.splits;
+  int64_t vecs = (int64_t)p.s.M * p.s.N / 4;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(to);
   void* params[4] = {&partial, &splits, &vecs, &out};
   const int64_t blocks = (vecs + 255) / 256;
@@ -881,7 +918,7 @@ int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd,
   if (e != cudaSuccess) return launch_failed(e);
 
   e = set_problem(&a.p[0], {{ws, T, F, false}, none}, {{wd, D, F, false}, none}, 1, T, D, kTN, F, 0, y);
-  a.p[0].splits = plan.y.splits;
+  a.p[0].s.splits = plan.y.splits;
   a.p[0].partial = reinterpret_cast<float*>(ws + round256((size_t)T * F * 2));
   if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, st);
   if (e == cudaSuccess && plan.y.splits > 1) e = launch_join(a.p[0], y, st);
@@ -938,7 +975,7 @@ int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
   const Operand xm = {x, T, D, true}, dym = {dy, T, D, true}, hm = {h, T, F, true};
   a.problems = 4;
   e = set_problem(&a.p[0], {dgk, duk}, {{wg, F, D, true}, {wu, F, D, true}}, 2, T, D, kTN, F, F, dx);
-  a.p[0].splits = plan.dx.splits;
+  a.p[0].s.splits = plan.dx.splits;
   a.p[0].partial = reinterpret_cast<float*>(ws + 3 * tf);
   if (e == cudaSuccess) e = set_problem(&a.p[1], {dgm, none}, {xm, none}, 1, F, D, kTN, T, 0, dwg);
   if (e == cudaSuccess) e = set_problem(&a.p[2], {dum, none}, {xm, none}, 1, F, D, kTN, T, 0, dwu);
