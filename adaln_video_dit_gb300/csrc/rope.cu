@@ -20,8 +20,11 @@
 // Layout of the work: P lanes share a head, each holding two 16-byte vectors
 // of it that contain whole pairs (interleaved: vectors j and j + half, halves:
 // a vector and its partner), so a rotation never leaves its lane and a norm
-// takes log2(P) shuffles.  A warp keeps one token's cosines and sines in
-// registers and walks that token's heads, 32 / P at a time.
+// takes log2(P) shuffles.  A warp walks tokens, and of each token the heads of
+// its chunk, U groups of 32 / P heads at a time with the next ones on their
+// way.  A token's cosines and sines and the weights are read from shared
+// memory, where the lanes of different heads read the same words: in registers
+// they would cost half of what a thread has, and with it the loads in flight.
 #include <cmath>
 
 #include "common.cuh"
@@ -32,10 +35,11 @@ namespace {
 
 constexpr int kWarps = 8;  // warps of a CTA
 constexpr int kThreads = kWarps * 32;
+constexpr int kCtasPerSm = 2;
 // Elements of a head that the scalar path's 32 lanes hold (8 pairs a lane).
 constexpr int kScalarPairs = 8;
 
-enum { kRotate = 0, kNormFwd = 1, kNormBwd = 2 };
+enum { kRotate = 0, kRotateBack = 1, kNormFwd = 2, kNormBwd = 3 };
 
 struct Tensor {
   const char* p;
@@ -43,7 +47,7 @@ struct Tensor {
 };
 
 struct Side {  // queries or keys
-  Tensor x;    // forward input (kRotate: what is rotated)
+  Tensor x;    // forward input (kRotate, kRotateBack: what is turned)
   Tensor dy;   // kNormBwd only
   char* out;
   int64_t out_ts, out_hs;
@@ -61,8 +65,8 @@ struct RopeArgs {
   int64_t T;
   int rows, axes, P, dh, nvec;
   int axis_end[4];  // pairs [axis_end[a-1], axis_end[a]) belong to axis a
+  int slots;  // (cosine, sine) entries of a token in shared memory (vector path)
   float eps, inv_dh;
-  float sign;  // of the sine: -1 turns back
   unsigned* status;
 };
 
@@ -91,19 +95,18 @@ struct Rows {
   __device__ __forceinline__ float2 at(const RopeArgs& a, int axis, int p) const {
     const int row = axis == 0 ? r[0] : axis == 1 ? r[1] : axis == 2 ? r[2] : axis == 3 ? r[3] : -1;
     if (row < 0) return make_float2(1.0f, 0.0f);
-    float2 c = __ldg(a.table + (int64_t)row * a.P + p);
-    c.y *= a.sign;
-    return c;
+    return __ldg(a.table + (int64_t)row * a.P + p);
   }
 };
 
-// (u, v) turned by (c, s).  A pair with a zero sine takes nothing from its
-// partner, so an unrotated element passes exactly, whatever the other holds.
-__device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
+// (u, v) turned by (c, s), or back.  A pair with a zero sine takes nothing from
+// its partner, so an unrotated element passes exactly, whatever the other holds.
+template <bool BACK>
+__device__ __forceinline__ void turn(float& u, float& v, float c, float s) {
   const float a = u, b = v;
-  const float bs = cs.y == 0.0f ? 0.0f : b * cs.y, as = cs.y == 0.0f ? 0.0f : a * cs.y;
-  u = fmaf(a, cs.x, -bs);
-  v = fmaf(b, cs.x, as);
+  const float bs = s == 0.0f ? 0.0f : b * s, as = s == 0.0f ? 0.0f : a * s;
+  u = fmaf(a, c, BACK ? bs : -bs);
+  v = fmaf(b, c, BACK ? -as : as);
 }
 
 // Sum over the CTA's warps of red[warp][0..dh), in warp order, into slot.
@@ -117,144 +120,200 @@ __device__ __forceinline__ void store_partial(const float* red, float* slot, int
   }
 }
 
+// (volatile: read where it is used, not kept in registers meanwhile)
+__device__ __forceinline__ float4 ld_shared_f4(const float* p) {
+  const uint4 v = ld_shared_v4(smem_addr(p));
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Vector path: head rows of whole, aligned 16-byte vectors, at most 64.
 // P lanes a head, U groups of 32 / P heads in flight.
 template <class E, int P, bool HALF, int MODE, int U>
-__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int N = E::EPV;       // elements of a vector, pairs of a lane
-  constexpr int HPW = 32 / P;     // heads side by side in a warp
-  extern __shared__ float red[];  // kNormBwd: [kWarps][dh]
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int N = E::EPV;    // elements of a vector, pairs of a lane
+  constexpr int HPW = 32 / P;  // heads side by side in a warp
+  constexpr bool kNorm = MODE == kNormFwd || MODE == kNormBwd;
+  constexpr bool kGrad = MODE == kNormBwd;
+  // [kWarps][2][slots] cosines and sines (after the walk, for the norm's
+  // backward, [kWarps][dh] weight sums); before them the weights.
+  extern __shared__ __align__(16) float shared[];
+  float* const weights = shared;
+  float* const red = shared + (kNorm ? (a.dh + 3) / 4 * 4 : 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float2* const angles = reinterpret_cast<float2*>(red) + warp * 2 * a.slots;
   const int j = lane & (P - 1), sub = lane / P;
   const bool is_k = (int)blockIdx.y >= a.side[0].chunks;
   const Side& sd = a.side[is_k];
   const int chunk = is_k ? blockIdx.y - a.side[0].chunks : blockIdx.y;
-  const int h_end = min(sd.heads, (chunk + 1) * sd.per_chunk);
+  const int h_begin = chunk * sd.per_chunk, h_end = min(sd.heads, h_begin + sd.per_chunk);
 
-  // This lane's two vectors (-1: none) and the axes of its pairs.
-  int va, vb, p0, p1;
+  // This lane's two vectors (-1: none) and the first pairs they hold: N pairs
+  // from p0 on (halves), or N / 2 from p0 and N / 2 from p1 (interleaved).
+  int va, vb, p0, p1 = 0;
   const int half = (a.nvec + 1) >> 1;
   if (HALF) {
     const int nr = a.P / N;
     va = j < nr ? j : 2 * nr + 2 * (j - nr);
     vb = j < nr ? j + nr : va + 1;
     p0 = j < nr ? N * j : a.P;
-    p1 = 0;  // one run of N pairs
   } else {
     va = j;
     vb = j + half;
     p0 = N / 2 * va;
     p1 = N / 2 * vb;
   }
-  if (va >= a.nvec || j >= half) va = -1;
-  if (vb >= a.nvec || j >= half) vb = -1;
-  auto pair_of = [&](int i) { return HALF ? p0 + i : (i < N / 2 ? p0 + i : p1 + i - N / 2); };
-  unsigned axes = 0;  // 3 bits a pair
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    axes |= (unsigned)(HALF && p0 >= a.P ? 4 : axis_of(a, pair_of(i))) << (3 * i);
+  if (va >= a.nvec || j >= half) va = -1, p0 = 0;
+  if (vb >= a.nvec || j >= half) vb = -1, p1 = 0;
 
   grid_wait();
   grid_launch_dependents();
 
-  float2 w[N];  // norm weights of vector a, then b
-  if (MODE != kRotate) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = make_float2(1.0f, 1.0f);
-    if (sd.w != nullptr) {
-      float2 f[N / 2];
-      const char* wp = static_cast<const char*>(sd.w);
-      if (va >= 0) {
-        E::unpack2(ld_global_v4(wp + va * 16), f);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) w[i] = f[i];
-      }
-      if (vb >= 0) {
-        E::unpack2(ld_global_v4(wp + vb * 16), f);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) w[N / 2 + i] = f[i];
-      }
+  if (kNorm) {
+    for (int d = threadIdx.x; d < a.dh; d += kThreads) {
+      float w = 1.0f;
+      if (sd.w != nullptr)
+        w = E::SIZE == 2 ? __bfloat162float(static_cast<const __nv_bfloat16*>(sd.w)[d])
+                         : static_cast<const float*>(sd.w)[d];
+      weights[d] = w;
     }
   }
-  float2 dw[MODE == kNormBwd ? N : 1];
-  if (MODE == kNormBwd) {
+  for (int i = a.P + lane; i < a.slots; i += 32)  // entries past the rotated pairs
+    angles[i] = angles[a.slots + i] = make_float2(1.0f, 0.0f);
+  __syncthreads();
+
+  // The angles of a token into slot b, from its rows.
+  auto fetch_angles = [&](const Rows& rows, int b) {
+    for (int p = lane; p < a.P; p += 32) {
+      const int axis = axis_of(a, p);
+      const int row = axis == 0 ? rows.r[0] : axis == 1 ? rows.r[1] : axis == 2 ? rows.r[2] : rows.r[3];
+      if (row >= 0)
+        cp_async8(&angles[b * a.slots + p], a.table + (int64_t)row * a.P + p);
+      else
+        angles[b * a.slots + p] = make_float2(1.0f, 0.0f);
+    }
+  };
+
+  struct Group {
+    uint4 xa[U], xb[U], ya[kGrad ? U : 1], yb[kGrad ? U : 1];
+  };
+  auto load = [&](Group& g, int64_t t, int h0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * HPW + sub;
+      const bool on = h < h_end && t < a.T;
+      const char* x = sd.x.p + t * sd.x.ts + h * sd.x.hs;
+      g.xa[u] = on && va >= 0 ? ld_global_v4(x + va * 16) : make_uint4(0, 0, 0, 0);
+      g.xb[u] = on && vb >= 0 ? ld_global_v4(x + vb * 16) : make_uint4(0, 0, 0, 0);
+      if (kGrad) {
+        const char* y = sd.dy.p + t * sd.dy.ts + h * sd.dy.hs;
+        g.ya[u] = on && va >= 0 ? ld_global_v4(y + va * 16) : make_uint4(0, 0, 0, 0);
+        g.yb[u] = on && vb >= 0 ? ld_global_v4(y + vb * 16) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  auto unpack = [&](float2(&f)[N], const uint4& va4, const uint4& vb4) {
+    float2 v[N / 2];
+    E::unpack2(va4, v);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) f[i] = v[i];
+    E::unpack2(vb4, v);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) f[N / 2 + i] = v[i];
+  };
+  auto rotate = [&](float2(&f)[N], const float* cs) {  // vector a's pairs of floats, then b's
+    constexpr bool back = MODE == kRotateBack || MODE == kNormBwd;
+    if (HALF) {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float4 c = ld_shared_f4(cs + 2 * p0 + 4 * i);
+        turn<back>(f[i].x, f[N / 2 + i].x, c.x, c.y);
+        turn<back>(f[i].y, f[N / 2 + i].y, c.z, c.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float4 c = ld_shared_f4(cs + 2 * (i < N / 4 ? p0 : p1) + 4 * (i < N / 4 ? i : i - N / 4));
+        turn<back>(f[2 * i].x, f[2 * i].y, c.x, c.y);
+        turn<back>(f[2 * i + 1].x, f[2 * i + 1].y, c.z, c.w);
+      }
+    }
+  };
+  auto weights4 = [&](int i) {  // of float pairs 2 i and 2 i + 1
+    const int v = i < N / 4 ? max(va, 0) : max(vb, 0);
+    return ld_shared_f4(weights + v * N + 4 * (i < N / 4 ? i : i - N / 4));
+  };
+
+  float2 dw[kGrad ? N : 1];
+  if (kGrad) {
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[i] = make_float2(0.0f, 0.0f);
   }
 
   const int64_t step = (int64_t)gridDim.x * kWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += step) {
-    Rows rows;
+  int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+  Group cur;
+  load(cur, t, h_begin);
+  Rows rows;  // of the token after the one whose angles are on their way
+  if (t < a.T) {
     rows.load(a, t, lane);
-    float2 cs[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) cs[i] = rows.at(a, (axes >> (3 * i)) & 7, pair_of(i));
+    fetch_angles(rows, 0);
+    if (t + step < a.T) rows.load(a, t + step, lane);
+  }
+  for (int slot = 0; t < a.T; t += step, slot ^= 1) {
+    cp_async_wait();
+    __syncwarp();
+    if (t + step < a.T) {
+      fetch_angles(rows, slot ^ 1);
+      if (t + 2 * step < a.T) rows.load(a, t + 2 * step, lane);
+    }
+    const float* cs = reinterpret_cast<const float*>(angles + slot * a.slots);
 
-    auto rotate = [&](float2(&f)[N]) {  // f: vector a's pairs of floats, then b's
-      if (HALF) {
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          turn(f[i].x, f[N / 2 + i].x, cs[2 * i]);
-          turn(f[i].y, f[N / 2 + i].y, cs[2 * i + 1]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) turn(f[i].x, f[i].y, cs[i]);
-      }
-    };
-
-    for (int h0 = chunk * sd.per_chunk; h0 < h_end; h0 += U * HPW) {
-      uint4 xa[U], xb[U], ya[MODE == kNormBwd ? U : 1], yb[MODE == kNormBwd ? U : 1];
+    for (int h0 = h_begin; h0 < h_end; h0 += U * HPW) {
+      Group next;
+      const bool more = h0 + U * HPW < h_end;
+      load(next, more ? t : t + step, more ? h0 + U * HPW : h_begin);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = h0 + u * HPW + sub;
-        const bool on = h < h_end;
-        const char* x = sd.x.p + t * sd.x.ts + h * sd.x.hs;
-        xa[u] = on && va >= 0 ? ld_global_v4(x + va * 16) : make_uint4(0, 0, 0, 0);
-        xb[u] = on && vb >= 0 ? ld_global_v4(x + vb * 16) : make_uint4(0, 0, 0, 0);
-        if (MODE == kNormBwd) {
-          const char* y = sd.dy.p + t * sd.dy.ts + h * sd.dy.hs;
-          ya[u] = on && va >= 0 ? ld_global_v4(y + va * 16) : make_uint4(0, 0, 0, 0);
-          yb[u] = on && vb >= 0 ? ld_global_v4(y + vb * 16) : make_uint4(0, 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * HPW + sub;
-        float2 f[N], half_v[N / 2];
-        E::unpack2(xa[u], half_v);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) f[i] = half_v[i];
-        E::unpack2(xb[u], half_v);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) f[N / 2 + i] = half_v[i];
-
-        if (MODE == kRotate) {
-          rotate(f);
+        float2 f[N];
+        unpack(f, cur.xa[u], cur.xb[u]);
+        if (!kNorm) {
+          rotate(f, cs);
         } else {
           float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < N; ++i) ss = fma2(f[i], f[i], ss);
           float sx = ss.x + ss.y;
-          if (MODE == kNormFwd) {
+          if (!kGrad) {
 #pragma unroll
             for (int o = P / 2; o > 0; o >>= 1) sx += __shfl_xor_sync(~0u, sx, o);
             const float r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = mul2(mul2(f[i], splat2(r)), w[i]);
-            rotate(f);
+            for (int i = 0; i < N / 2; ++i) {
+              const float4 w = weights4(i);
+              f[2 * i] = mul2(mul2(f[2 * i], splat2(r)), make_float2(w.x, w.y));
+              f[2 * i + 1] = mul2(mul2(f[2 * i + 1], splat2(r)), make_float2(w.z, w.w));
+            }
+            rotate(f, cs);
           } else {
             float2 g[N];
-            E::unpack2(ya[u], half_v);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) g[i] = half_v[i];
-            E::unpack2(yb[u], half_v);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) g[N / 2 + i] = half_v[i];
-            rotate(g);
+            unpack(g, cur.ya[u], cur.yb[u]);
+            rotate(g, cs);
             float2 hs = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) hs = fma2(mul2(g[i], w[i]), f[i], hs);
+            for (int i = 0; i < N / 2; ++i) {
+              const float4 w = weights4(i);
+              hs = fma2(mul2(g[2 * i], make_float2(w.x, w.y)), f[2 * i], hs);
+              hs = fma2(mul2(g[2 * i + 1], make_float2(w.z, w.w)), f[2 * i + 1], hs);
+            }
             float sh = hs.x + hs.y;
 #pragma unroll
             for (int o = P / 2; o > 0; o >>= 1) {
@@ -268,29 +327,34 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
             const float rd = h < h_end ? r : 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
+              const float4 w = weights4(i / 2);
+              const float2 wi = i % 2 ? make_float2(w.z, w.w) : make_float2(w.x, w.y);
               dw[i] = fma2(g[i], mul2(f[i], splat2(rd)), dw[i]);
-              f[i] = fma2(f[i], splat2(k), mul2(mul2(g[i], w[i]), splat2(r)));
+              f[i] = fma2(f[i], splat2(k), mul2(mul2(g[i], wi), splat2(r)));
             }
           }
         }
         if (h < h_end) {
           char* o = sd.out + t * sd.out_ts + h * sd.out_hs;
+          float2 v[N / 2];
           if (va >= 0) {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) half_v[i] = f[i];
-            *reinterpret_cast<uint4*>(o + va * 16) = E::pack2(half_v);
+            for (int i = 0; i < N / 2; ++i) v[i] = f[i];
+            *reinterpret_cast<uint4*>(o + va * 16) = E::pack2(v);
           }
           if (vb >= 0) {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) half_v[i] = f[N / 2 + i];
-            *reinterpret_cast<uint4*>(o + vb * 16) = E::pack2(half_v);
+            for (int i = 0; i < N / 2; ++i) v[i] = f[N / 2 + i];
+            *reinterpret_cast<uint4*>(o + vb * 16) = E::pack2(v);
           }
         }
       }
+      cur = next;
     }
   }
 
-  if (MODE == kNormBwd && sd.partial != nullptr) {
+  if (kGrad && sd.partial != nullptr) {
+    __syncthreads();  // the angles' place is reused
     // Lanes of the same j hold the same columns: sum them in a fixed tree.
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -331,6 +395,7 @@ __device__ __forceinline__ void store1(char* p, float v, F32) { *reinterpret_cas
 template <class E, int MODE>
 __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_constant__ RopeArgs a,
                                                                int interleaved) {
+  constexpr bool kNorm = MODE == kNormFwd || MODE == kNormBwd;
   extern __shared__ float red[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool is_k = (int)blockIdx.y >= a.side[0].chunks;
@@ -355,8 +420,8 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < kScalarPairs; ++i) {
     const char* wp = static_cast<const char*>(sd.w);
-    wa[i] = MODE != kRotate && wp && da[i] >= 0 ? load1<E>(wp + da[i] * E::SIZE) : 1.0f;
-    wb[i] = MODE != kRotate && wp && db[i] >= 0 ? load1<E>(wp + db[i] * E::SIZE) : 1.0f;
+    wa[i] = kNorm && wp && da[i] >= 0 ? load1<E>(wp + da[i] * E::SIZE) : 1.0f;
+    wb[i] = kNorm && wp && db[i] >= 0 ? load1<E>(wp + db[i] * E::SIZE) : 1.0f;
     dwa[i] = dwb[i] = 0.0f;
   }
 
@@ -378,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_cons
         sx = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], sx));
       }
       float r = 1.0f;
-      if (MODE != kRotate) {
+      if (kNorm) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sx += __shfl_xor_sync(~0u, sx, o);
         r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
@@ -390,7 +455,7 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_cons
             fa[i] = fa[i] * r * wa[i];
             fb[i] = fb[i] * r * wb[i];
           }
-          turn(fa[i], fb[i], cs[i]);
+          turn<MODE == kRotateBack>(fa[i], fb[i], cs[i].x, cs[i].y);
         }
       } else {
         const char* y = sd.dy.p + t * sd.dy.ts + h * sd.dy.hs;
@@ -399,7 +464,7 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_cons
         for (int i = 0; i < kScalarPairs; ++i) {
           ga[i] = da[i] >= 0 ? load1<E>(y + da[i] * E::SIZE) : 0.0f;
           gb[i] = db[i] >= 0 ? load1<E>(y + db[i] * E::SIZE) : 0.0f;
-          turn(ga[i], gb[i], cs[i]);
+          turn<true>(ga[i], gb[i], cs[i].x, cs[i].y);
           sh = fmaf(ga[i] * wa[i], fa[i], fmaf(gb[i] * wb[i], fb[i], sh));
         }
 #pragma unroll
@@ -480,36 +545,32 @@ cudaError_t launch(void* kernel, dim3 grid, int threads, size_t smem, void** par
   return cudaLaunchKernelExC(&cfg, kernel, params);
 }
 
-constexpr int kUnroll[3] = {4, 4, 2};  // head groups in flight by mode
-
-template <class E, int P>
-void* vec_kernel(int mode, bool half) {
+// Head groups in flight by mode.
+template <class E, int P, bool HALF>
+void* vec_kernel(int mode) {
   switch (mode) {
-    case kRotate:
-      return half ? (void*)rope_vec_kernel<E, P, true, kRotate, kUnroll[0]>
-                  : (void*)rope_vec_kernel<E, P, false, kRotate, kUnroll[0]>;
-    case kNormFwd:
-      return half ? (void*)rope_vec_kernel<E, P, true, kNormFwd, kUnroll[1]>
-                  : (void*)rope_vec_kernel<E, P, false, kNormFwd, kUnroll[1]>;
-    default:
-      return half ? (void*)rope_vec_kernel<E, P, true, kNormBwd, kUnroll[2]>
-                  : (void*)rope_vec_kernel<E, P, false, kNormBwd, kUnroll[2]>;
+    case kRotate: return (void*)rope_vec_kernel<E, P, HALF, kRotate, 4>;
+    case kRotateBack: return (void*)rope_vec_kernel<E, P, HALF, kRotateBack, 4>;
+    case kNormFwd: return (void*)rope_vec_kernel<E, P, HALF, kNormFwd, 4>;
+    default: return (void*)rope_vec_kernel<E, P, HALF, kNormBwd, 2>;
   }
 }
+int groups_in_flight(int mode) { return mode == kNormBwd ? 2 : 4; }
 
-template <class E>
-void* pick_kernel(int lanes, int mode, bool half) {
-  if (lanes <= 4) return vec_kernel<E, 4>(mode, half);
-  if (lanes <= 8) return vec_kernel<E, 8>(mode, half);
-  if (lanes <= 16) return vec_kernel<E, 16>(mode, half);
-  return vec_kernel<E, 32>(mode, half);
+template <class E, bool HALF>
+void* pick_kernel(int lanes, int mode) {
+  return lanes == 4    ? vec_kernel<E, 4, HALF>(mode)
+         : lanes == 8  ? vec_kernel<E, 8, HALF>(mode)
+         : lanes == 16 ? vec_kernel<E, 16, HALF>(mode)
+                       : vec_kernel<E, 32, HALF>(mode);
 }
 
 template <class E>
 void* scalar_kernel(int mode) {
-  return mode == kRotate    ? (void*)rope_scalar_kernel<E, kRotate>
-         : mode == kNormFwd ? (void*)rope_scalar_kernel<E, kNormFwd>
-                            : (void*)rope_scalar_kernel<E, kNormBwd>;
+  return mode == kRotate       ? (void*)rope_scalar_kernel<E, kRotate>
+         : mode == kRotateBack ? (void*)rope_scalar_kernel<E, kRotateBack>
+         : mode == kNormFwd    ? (void*)rope_scalar_kernel<E, kNormFwd>
+                               : (void*)rope_scalar_kernel<E, kNormBwd>;
 }
 
 struct Plan {
@@ -520,11 +581,11 @@ struct Plan {
   int grid_x;
 };
 
-// Split of a call: token x chunk of heads per warp.  With many tokens a warp
-// takes all of a side's heads, so a token's angles are loaded twice in all;
-// with few, the heads are split until about every SM's warps have work.  The
-// norm's backward keeps its weight sums in registers over a loop of tokens,
-// so its grid is bounded (two CTAs an SM), the others' is not.
+// Split of a call: the warps of a CTA walk tokens of one chunk of heads, with
+// two CTAs an SM in all.  A chunk is at least as many heads as the smaller side
+// has, so that chunks take about as long (grouped keys) and a token's angles
+// are fetched once a chunk; with few tokens the heads are split until about
+// every warp has work.
 cudaError_t make_plan(int64_t T, const int (&heads)[2], int dh, int mode, bool vec, int es,
                       Plan* p) {
   int dev = 0, sms = 0;
@@ -539,22 +600,24 @@ cudaError_t make_plan(int64_t T, const int (&heads)[2], int dh, int mode, bool v
     p->lanes = want <= 4 ? 4 : want <= 8 ? 8 : want <= 16 ? 16 : 32;
     unit = 32 / p->lanes;
   }
-  const int64_t warps = (int64_t)sms * 16;
+  const int64_t warps = (int64_t)sms * kCtasPerSm * kWarps;
+  const int fewer = heads[0] == 0   ? heads[1]
+                    : heads[1] == 0 ? heads[0]
+                                    : (heads[0] < heads[1] ? heads[0] : heads[1]);
+  const int most = unit * (vec ? groups_in_flight(mode) : 4);
+  int64_t per = fewer > most ? fewer : most;
+  const int64_t split = T > 0 ? (warps + T - 1) / T : 1;  // chunks that give every warp a token
+  const int64_t small = (heads[0] + heads[1] + split - 1) / split;
+  if (small < per) per = small;
+  per = (per + unit - 1) / unit * unit;
   for (int s = 0; s < 2; ++s) {
-    const int groups = (heads[s] + unit - 1) / unit;
-    int64_t split = T > 0 ? (warps + 2 * T - 1) / (2 * T) : 1;
-    if (split > groups) split = groups;
-    if (split < 1) split = 1;
-    const int per = groups > 0 ? (int)((groups + split - 1) / split) * unit : unit;
-    p->per_chunk[s] = per;
-    p->chunks[s] = heads[s] > 0 ? (heads[s] + per - 1) / per : 0;
+    p->per_chunk[s] = (int)per;
+    p->chunks[s] = (int)((heads[s] + per - 1) / per);
   }
+  const int chunks = p->chunks[0] + p->chunks[1];
   int64_t gx = (T + kWarps - 1) / kWarps;
-  if (mode == kNormBwd) {
-    const int chunks = p->chunks[0] + p->chunks[1];
-    const int64_t most = (2 * (int64_t)sms + chunks - 1) / chunks;
-    if (gx > most) gx = most;
-  }
+  const int64_t all = ((int64_t)kCtasPerSm * sms + chunks - 1) / chunks;
+  if (gx > all) gx = all;
   p->grid_x = (int)(gx < 1 ? 1 : gx);
   return cudaSuccess;
 }
@@ -611,7 +674,7 @@ bool vec_layout(int dh, int es, int pairs, bool half) {
 int run(int mode, const adaln_heads_t* const (&x)[2], const adaln_heads_t* const (&dy)[2],
         const adaln_heads_t* const (&out)[2], int64_t T, const int (&heads)[2], int32_t dh,
         adaln_dtype_t dtype, const adaln_rope_t* rope, const void* const (&w)[2], float eps,
-        float sign, float* const (&dw)[2], void* workspace, size_t workspace_bytes, bool vec,
+        float* const (&dw)[2], void* workspace, size_t workspace_bytes, bool vec,
         cudaStream_t st) {
   const int es = dtype == ADALN_BF16 ? 2 : 4;
   RopeArgs a = {};
@@ -653,20 +716,28 @@ int run(int mode, const adaln_heads_t* const (&x)[2], const adaln_heads_t* const
   a.nvec = dh * es / 16;
   a.eps = eps;
   a.inv_dh = 1.0f / (float)dh;
-  a.sign = sign;
   a.status = status;
 
   const bool half = !rope->interleaved;
   int interleaved = rope->interleaved != 0;
   void* kernel;
-  if (p.vec)
-    kernel = dtype == ADALN_BF16 ? pick_kernel<BF16>(p.lanes, mode, half)
-                                 : pick_kernel<F32>(p.lanes, mode, half);
-  else
+  size_t smem = mode == kNormBwd ? (size_t)kWarps * dh * sizeof(float) : 0;
+  if (p.vec) {
+    if (dtype == ADALN_BF16)
+      kernel = half ? pick_kernel<BF16, true>(p.lanes, mode) : pick_kernel<BF16, false>(p.lanes, mode);
+    else
+      kernel = half ? pick_kernel<F32, true>(p.lanes, mode) : pick_kernel<F32, false>(p.lanes, mode);
+    // Every pair a lane may hold has an entry: dh / 2, and one vector's worth
+    // past P for the unrotated vectors of the halves layout.
+    const int past = a.P + 16 / es;
+    a.slots = (past > dh / 2 + 1 ? past : dh / 2 + 1) + 1 & ~1;
+    const size_t angles = (size_t)kWarps * 2 * a.slots * sizeof(float2);
+    smem = (angles > smem ? angles : smem) + (size_t)(dh + 3) / 4 * 16;
+  } else {
     kernel = dtype == ADALN_BF16 ? scalar_kernel<BF16>(mode) : scalar_kernel<F32>(mode);
+  }
   void* params[2] = {&a, &interleaved};
   const dim3 grid((unsigned)p.grid_x, (unsigned)(p.chunks[0] + p.chunks[1]));
-  const size_t smem = mode == kNormBwd ? (size_t)kWarps * dh * sizeof(float) : 0;
   if (T > 0) {
     e = traced_launch(ADALN_KERNEL_QK_ROPE, st,
                       [&] { return launch(kernel, grid, kThreads, smem, params, st); });
@@ -717,7 +788,7 @@ int adaln_qk_rope_fwd(const adaln_heads_t* q, const adaln_heads_t* k, int64_t T,
   }
   if (T == 0) return ADALN_OK;
   return run(norm ? kNormFwd : kRotate, {q, k}, {nullptr, nullptr}, {q_out, k_out}, T, {hq, hk},
-             dh, dtype, rope, {wq, wk}, eps, 1.0f, {nullptr, nullptr}, nullptr, 0, vec,
+             dh, dtype, rope, {wq, wk}, eps, {nullptr, nullptr}, nullptr, 0, vec,
              static_cast<cudaStream_t>(stream));
 }
 
@@ -762,8 +833,8 @@ int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t* dk_out,
     // The rotation's transpose is the rotation by the opposite angle.
     if (dwq || dwk) return ADALN_ERR_ARG;
     if (T == 0) return ADALN_OK;
-    return run(kRotate, {dq_out, dk_out}, {nullptr, nullptr}, {dq, dk}, T, {hq, hk}, dh, dtype,
-               rope, {nullptr, nullptr}, 0.0f, -1.0f, {nullptr, nullptr}, nullptr, 0, vec, st);
+    return run(kRotateBack, {dq_out, dk_out}, {nullptr, nullptr}, {dq, dk}, T, {hq, hk}, dh,
+               dtype, rope, {nullptr, nullptr}, 0.0f, {nullptr, nullptr}, nullptr, 0, vec, st);
   }
   if ((rc = check_heads(q, hq, T, es, &vec)) || (rc = check_heads(k, hk, T, es, &vec))) return rc;
   if (!std::isfinite(eps) || eps < 0.0f) return ADALN_ERR_ARG;
@@ -774,7 +845,7 @@ int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t* dk_out,
   if (!aligned_to(workspace, 16)) return ADALN_ERR_ALIGN;
   if (T == 0 && !dwq && !dwk) return ADALN_OK;
   return run(kNormBwd, {q, k}, {dq_out, dk_out}, {dq, dk}, T, {hq, hk}, dh, dtype, rope, {wq, wk},
-             eps, -1.0f, {dwq, dwk}, workspace, workspace_bytes, vec, st);
+             eps, {dwq, dwk}, workspace, workspace_bytes, vec, st);
 }
 
 }  // extern "C"
