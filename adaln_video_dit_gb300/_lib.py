@@ -140,12 +140,19 @@ def dtype_code(t):
 
 
 def _stream_ptr(stream, device):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    """The stream's handle (the device's current stream when None).  A call of
+    a small operator is bound by this host code, so it takes the raw handle:
+    building a torch.cuda.Stream for it costs 2 us."""
+    if stream is not None:
+        return stream.cuda_stream
+    index = device if isinstance(device, int) else device.index
+    if index is None:
+        index = torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _dev(t, name, dtype=None, shape=None):
@@ -155,7 +162,7 @@ def _dev(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -302,7 +309,8 @@ def adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_row
 
 
 def _heads(t, name, like=None):
-    """Check a [T, heads, dh] tensor (any strides, dh contiguous); its Heads."""
+    """Check a [T, heads, dh] tensor (any strides, dh contiguous), with the
+    shape, dtype and device of `like`; its Heads."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 3:
@@ -310,19 +318,47 @@ def _heads(t, name, like=None):
     if like is not None:
         if t.shape != like.shape:
             raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+        _alike(t, name, like)
     ts, hs, ds = t.stride()
     if ds != 1 and t.shape[2] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     return Heads(t.data_ptr(), ts, hs)
 
 
-def _rope(table, pos, axis_pairs, interleaved, T, dh, device):
-    if not (table.is_cuda and pos.is_cuda and table.device == device and pos.device == device):
-        raise ValueError(f"table and pos must be on {device}")
+def _alike(t, name, like):
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+
+
+def _heads_out(t, name, like):
+    """An output like `like`: checked, or allocated contiguous; it and its Heads."""
+    if t is not None:
+        return t, _heads(t, name, like)
+    t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _, h, dh = like.shape
+    return t, Heads(t.data_ptr(), h * dh, dh)
+
+
+def _second(k, name, q, T, dh):
+    """Check the keys against the queries; their head count and Heads."""
+    if k is None:
+        return 0, None
+    kh = _heads(k, name)
+    if k.shape[0] != T or k.shape[2] != dh:
+        raise ValueError("queries and keys must agree in tokens and head width")
+    _alike(k, name, q)
+    return k.shape[1], kh
+
+
+_Pairs = ctypes.c_int32 * MAX_ROPE_AXES
+
+
+def _rope(table, pos, axis_pairs, interleaved, T, like):
+    dev = like.get_device()
+    if table.get_device() != dev or pos.get_device() != dev:
+        raise ValueError(f"table and pos must be on {like.device}")
     if table.dtype != torch.float32 or not table.is_contiguous():
         raise ValueError("table must be contiguous float32")
     if pos.dtype != torch.int32 or not pos.is_contiguous():
@@ -330,20 +366,20 @@ def _rope(table, pos, axis_pairs, interleaved, T, dh, device):
     axes, P = len(axis_pairs), sum(axis_pairs)
     if not 1 <= axes <= MAX_ROPE_AXES or min(axis_pairs) < 0:
         raise ValueError(f"axis_pairs must hold 1 to {MAX_ROPE_AXES} counts >= 0")
-    if table.dim() != 3 or table.shape[1] != P or table.shape[2] != 2:
+    if table.dim() != 3 or table.shape[1:] != (P, 2):
         raise ValueError(f"table must have shape [rows, {P}, 2], got {tuple(table.shape)}")
     if pos.shape != (T, axes):
         raise ValueError(f"pos must have shape {(T, axes)}, got {tuple(pos.shape)}")
-    return Rope(table.data_ptr(), pos.data_ptr(), table.shape[0], axes,
-                (ctypes.c_int32 * MAX_ROPE_AXES)(*axis_pairs), 1 if interleaved else 0)
+    return Rope(table.data_ptr(), pos.data_ptr(), table.shape[0], axes, _Pairs(*axis_pairs),
+                1 if interleaved else 0)
 
 
 def _weight(w, name, like):
-    if w is not None:
-        _dev(w, name, like.dtype, (like.shape[2],))
-        if w.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {w.device}")
-    return _ptr(w)
+    if w is None:
+        return None
+    _dev(w, name, like.dtype, like.shape[2:])
+    _alike(w, name, like)
+    return w.data_ptr()
 
 
 def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False, wq=None,
@@ -354,24 +390,18 @@ def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False
     pos [T, axes] int32 rows of it (-1: unrotated), axis_pairs the pairs of
     each axis (P in all).  q and k may be strided views; q_out, k_out may be q, k.
     Returns (q_out, k_out), allocated contiguous when not given."""
-    T, hq, dh = q.shape
     qh = _heads(q, "q")
-    dev = q.device
-    hk = 0
-    kh = koh = None
-    rope = _rope(table, pos, axis_pairs, interleaved, T, dh, dev)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-    qoh = _heads(q_out, "q_out", q)
-    if k is not None:
-        hk = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != dh or k.dtype != q.dtype or k.device != dev:
-            raise ValueError("q and k must agree in tokens, head width, dtype and device")
-        kh = _heads(k, "k")
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
-        koh = _heads(k_out, "k_out", k)
-    rc = raw.adaln_qk_rope_fwd(qh, kh, T, hq, hk, dh, dtype_code(q.dtype), rope,
-                               1 if norm else 0, _weight(wq, "wq", q), _weight(wk, "wk", q),
-                               float(eps), qoh, koh, _stream_ptr(stream, dev))
+    T, hq, dh = q.shape
+    hk, kh = _second(k, "k", q, T, dh)
+    rope = _rope(table, pos, axis_pairs, interleaved, T, q)
+    wqp, wkp = _weight(wq, "wq", q), _weight(wk, "wk", q)
+    code = dtype_code(q.dtype)
+    q_out, qoh = _heads_out(q_out, "q_out", q)
+    koh = None
+    if kh is not None:
+        k_out, koh = _heads_out(k_out, "k_out", k)
+    rc = raw.adaln_qk_rope_fwd(qh, kh, T, hq, hk, dh, code, rope, 1 if norm else 0, wqp, wkp, eps,
+                               qoh, koh, _stream_ptr(stream, q.get_device()))
     _check(rc, "adaln_qk_rope_fwd")
     return q_out, k_out
 
@@ -393,40 +423,36 @@ def adaln_qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved=True, 
     Returns (dq, dk, dwq, dwk); dwq, dwk are fp32 [dh], None without norm (and
     dk, dwk without k).  `workspace` is a uint8 CUDA tensor of at least
     adaln_qk_rope_bwd_workspace_size bytes (allocated when not given)."""
-    T, hq, dh = dq_out.shape
-    dev, dt = dq_out.device, dq_out.dtype
     doh = _heads(dq_out, "dq_out")
-    rope = _rope(table, pos, axis_pairs, interleaved, T, dh, dev)
-    dq = torch.empty(dq_out.shape, dtype=dt, device=dev) if dq is None else dq
-    dqh = _heads(dq, "dq", dq_out)
-    hk, dkoh, dkh, qh, kh, nbytes = 0, None, None, None, None, 0
-    if dk_out is not None:
-        hk = dk_out.shape[1]
-        if dk_out.shape[0] != T or dk_out.shape[2] != dh or dk_out.dtype != dt or dk_out.device != dev:
-            raise ValueError("dq_out and dk_out must agree in tokens, head width, dtype and device")
-        dkoh = _heads(dk_out, "dk_out")
-        dk = torch.empty(dk_out.shape, dtype=dt, device=dev) if dk is None else dk
-        dkh = _heads(dk, "dk", dk_out)
+    T, hq, dh = dq_out.shape
+    hk, dkoh = _second(dk_out, "dk_out", dq_out, T, dh)
+    rope = _rope(table, pos, axis_pairs, interleaved, T, dq_out)
+    code = dtype_code(dq_out.dtype)
+    wqp, wkp = _weight(wq, "wq", dq_out), _weight(wk, "wk", dq_out)
+    qh = kh = dkh = ws = None
+    nbytes = 0
     if norm:
         if q is None or (k is None) != (dk_out is None):
             raise ValueError("the norm's backward needs the forward's q (and k)")
         qh = _heads(q, "q", dq_out)
         kh = _heads(k, "k", dk_out) if k is not None else None
-        dwq = (torch.empty(dh, device=dev, dtype=torch.float32) if dwq is None
+        dwq = (torch.empty(dh, device=q.device, dtype=torch.float32) if dwq is None
                else _dev(dwq, "dwq", torch.float32, (dh,)))
         if k is not None:
-            dwk = (torch.empty(dh, device=dev, dtype=torch.float32) if dwk is None
+            dwk = (torch.empty(dh, device=q.device, dtype=torch.float32) if dwk is None
                    else _dev(dwk, "dwk", torch.float32, (dh,)))
         if workspace is None:
-            workspace = torch.empty(max(16, adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, dt)),
-                                    device=dev, dtype=torch.uint8)
-        _dev(workspace, "workspace")
-        nbytes = workspace.numel() * workspace.element_size()
-    rc = raw.adaln_qk_rope_bwd(doh, dkoh, qh, kh, T, hq, hk, dh, dtype_code(dt), rope,
-                               1 if norm else 0, _weight(wq, "wq", dq_out),
-                               _weight(wk, "wk", dq_out), float(eps), dqh, dkh, _ptr(dwq),
-                               _ptr(dwk), _ptr(workspace) if norm else None, nbytes,
-                               _stream_ptr(stream, dev))
+            workspace = torch.empty(max(16, adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, code)),
+                                    device=q.device, dtype=torch.uint8)
+        else:
+            _dev(workspace, "workspace", torch.uint8)
+        ws, nbytes = workspace.data_ptr(), workspace.numel()
+    dq, dqh = _heads_out(dq, "dq", dq_out)
+    if dkoh is not None:
+        dk, dkh = _heads_out(dk, "dk", dk_out)
+    rc = raw.adaln_qk_rope_bwd(doh, dkoh, qh, kh, T, hq, hk, dh, code, rope, 1 if norm else 0, wqp,
+                               wkp, eps, dqh, dkh, _ptr(dwq), _ptr(dwk), ws, nbytes,
+                               _stream_ptr(stream, dq_out.get_device()))
     _check(rc, "adaln_qk_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -456,12 +482,13 @@ def _act(act):
 
 
 def _ffn_args(x, wg, wu, wd):
+    _dev(x, "x")
     T, D = x.shape
     F = wg.shape[0]
-    _dev(x, "x")
-    _dev(wg, "wg", x.dtype, (F, D))
-    _dev(wu, "wu", x.dtype, (F, D))
-    _dev(wd, "wd", x.dtype, (D, F))
+    dt = x.dtype
+    _dev(wg, "wg", dt, (F, D))
+    _dev(wu, "wu", dt, (F, D))
+    _dev(wd, "wd", dt, (D, F))
     return T, D, F
 
 
@@ -488,10 +515,11 @@ def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, wor
             raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
     if workspace is None:
         workspace = _bytes(None, adaln_ffn_workspace_size(T, D, F, dt)[0], "workspace", x.device)
-    _dev(workspace, "workspace", torch.uint8)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
     rc = raw.adaln_ffn_fwd(_ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), T, D, F, dt, code, _ptr(y),
                            _ptr(saved), _ptr(workspace), workspace.numel(),
-                           _stream_ptr(stream, x.device))
+                           _stream_ptr(stream, x.get_device()))
     _check(rc, "adaln_ffn_fwd")
     return y, saved
 
@@ -513,10 +541,11 @@ def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=N
     dwd = torch.empty_like(wd) if dwd is None else _dev(dwd, "dwd", x.dtype, (D, F))
     if workspace is None:
         workspace = _bytes(None, adaln_ffn_workspace_size(T, D, F, dt)[1], "workspace", x.device)
-    _dev(workspace, "workspace", torch.uint8)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
     rc = raw.adaln_ffn_bwd(_ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), _ptr(saved), T, D, F,
                            dt, code, _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), _ptr(workspace),
-                           workspace.numel(), _stream_ptr(stream, x.device))
+                           workspace.numel(), _stream_ptr(stream, x.get_device()))
     _check(rc, "adaln_ffn_bwd")
     return dx, dwg, dwu, dwd
 

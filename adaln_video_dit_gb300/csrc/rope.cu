@@ -65,7 +65,6 @@ struct RopeArgs {
   int64_t T;
   int rows, axes, P, dh, nvec;
   int axis_end[4];  // pairs [axis_end[a-1], axis_end[a]) belong to axis a
-  int slots;  // (cosine, sine) entries of a token in shared memory (vector path)
   float eps, inv_dh;
   unsigned* status;
 };
@@ -121,16 +120,72 @@ __device__ __forceinline__ void store_partial(const float* red, float* slot, int
 }
 
 // (volatile: read where it is used, not kept in registers meanwhile)
-__device__ __forceinline__ float4 ld_shared_f4(const float* p) {
+__device__ __forceinline__ float4 ld_shared_f4(const float4* p) {
   const uint4 v = ld_shared_v4(smem_addr(p));
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                      __uint_as_float(v.w));
 }
-__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A lane's two vectors as N pairs, split: the first elements of pairs 2 i and
+// 2 i + 1 in A[i], the second ones in B[i], so that two pairs turn in packed
+// arithmetic.  Interleaved pairs are neighbours in a vector (vector a's, then
+// b's); those of the halves layout are the same element of a and of b.
+template <bool HALF>
+__device__ __forceinline__ void split(const uint4& a, const uint4& b, float2 (&A)[4], float2 (&B)[4],
+                                      BF16) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  auto lo = [&](int i) { return __uint_as_float(w[i] << 16); };
+  auto hi = [&](int i) { return __uint_as_float(w[i] & 0xffff0000u); };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    A[i] = HALF ? make_float2(lo(i), hi(i)) : make_float2(lo(2 * i), lo(2 * i + 1));
+    B[i] = HALF ? make_float2(lo(4 + i), hi(4 + i)) : make_float2(hi(2 * i), hi(2 * i + 1));
+  }
+}
+template <bool HALF>
+__device__ __forceinline__ void split(const uint4& a, const uint4& b, float2 (&A)[2], float2 (&B)[2],
+                                      F32) {
+  const float f[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z),
+                      __uint_as_float(a.w), __uint_as_float(b.x), __uint_as_float(b.y),
+                      __uint_as_float(b.z), __uint_as_float(b.w)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    A[i] = HALF ? make_float2(f[2 * i], f[2 * i + 1]) : make_float2(f[4 * i], f[4 * i + 2]);
+    B[i] = HALF ? make_float2(f[4 + 2 * i], f[5 + 2 * i]) : make_float2(f[4 * i + 1], f[4 * i + 3]);
+  }
+}
+// And back, rounded to the element type.
+template <bool HALF>
+__device__ __forceinline__ void join(const float2 (&A)[4], const float2 (&B)[4], uint4& a, uint4& b,
+                                     BF16) {
+  float2 f[4], g[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = HALF ? A[i] : i % 2 ? make_float2(A[i / 2].y, B[i / 2].y) : make_float2(A[i / 2].x, B[i / 2].x);
+    g[i] = HALF    ? B[i]
+           : i % 2 ? make_float2(A[2 + i / 2].y, B[2 + i / 2].y)
+                   : make_float2(A[2 + i / 2].x, B[2 + i / 2].x);
+  }
+  a = BF16::pack2(f);
+  b = BF16::pack2(g);
+}
+template <bool HALF>
+__device__ __forceinline__ void join(const float2 (&A)[2], const float2 (&B)[2], uint4& a, uint4& b,
+                                     F32) {
+  float2 f[2], g[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[i] = HALF ? A[i] : i ? make_float2(A[0].y, B[0].y) : make_float2(A[0].x, B[0].x);
+    g[i] = HALF ? B[i] : i ? make_float2(A[1].y, B[1].y) : make_float2(A[1].x, B[1].x);
+  }
+  a = F32::pack2(f);
+  b = F32::pack2(g);
 }
 
 // Vector path: head rows of whole, aligned 16-byte vectors, at most 64.
@@ -139,122 +194,135 @@ template <class E, int P, bool HALF, int MODE, int U>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     rope_vec_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int N = E::EPV;    // elements of a vector, pairs of a lane
+  constexpr int M = N / 2;     // packed pairs of pairs of a lane
   constexpr int HPW = 32 / P;  // heads side by side in a warp
   constexpr bool kNorm = MODE == kNormFwd || MODE == kNormBwd;
   constexpr bool kGrad = MODE == kNormBwd;
-  // [kWarps][2][slots] cosines and sines (after the walk, for the norm's
-  // backward, [kWarps][dh] weight sums); before them the weights.
-  extern __shared__ __align__(16) float shared[];
-  float* const weights = shared;
-  float* const red = shared + (kNorm ? (a.dh + 3) / 4 * 4 : 0);
+  constexpr bool kBack = MODE == kRotateBack || MODE == kNormBwd;
+  // Tables of [M][half] float4: lane j's i-th entry holds, for its pairs 2 i
+  // and 2 i + 1, two cosines and two sines, or the two weights of A and of B;
+  // neighbouring lanes' entries are neighbours, so a read has no bank conflict.
+  // The weights' table, then two of angles (this token's, the next's) per warp.
+  // After the walk the norm's backward puts [kWarps][dh] weight sums there.
+  extern __shared__ __align__(16) float4 shared[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float2* const angles = reinterpret_cast<float2*>(red) + warp * 2 * a.slots;
+  const int half = (a.nvec + 1) >> 1, entries = M * half;
+  float4* const weights = shared;
+  float4* const angles = shared + (kNorm ? entries : 0) + warp * 2 * entries;
   const int j = lane & (P - 1), sub = lane / P;
   const bool is_k = (int)blockIdx.y >= a.side[0].chunks;
   const Side& sd = a.side[is_k];
   const int chunk = is_k ? blockIdx.y - a.side[0].chunks : blockIdx.y;
   const int h_begin = chunk * sd.per_chunk, h_end = min(sd.heads, h_begin + sd.per_chunk);
 
-  // This lane's two vectors (-1: none) and the first pairs they hold: N pairs
-  // from p0 on (halves), or N / 2 from p0 and N / 2 from p1 (interleaved).
-  int va, vb, p0, p1 = 0;
-  const int half = (a.nvec + 1) >> 1;
-  if (HALF) {
-    const int nr = a.P / N;
-    va = j < nr ? j : 2 * nr + 2 * (j - nr);
-    vb = j < nr ? j + nr : va + 1;
-    p0 = j < nr ? N * j : a.P;
-  } else {
-    va = j;
-    vb = j + half;
-    p0 = N / 2 * va;
-    p1 = N / 2 * vb;
-  }
-  if (va >= a.nvec || j >= half) va = -1, p0 = 0;
-  if (vb >= a.nvec || j >= half) vb = -1, p1 = 0;
+  // This lane's two vectors (-1: none).
+  const int nr = a.P / N;  // halves: vectors of the first half
+  int va = HALF && j >= nr ? 2 * nr + 2 * (j - nr) : j;
+  int vb = HALF ? (j < nr ? j + nr : va + 1) : j + half;
+  if (va >= a.nvec || j >= half) va = -1;
+  if (vb >= a.nvec || j >= half) vb = -1;
+  const int jj = min(j, half - 1);
+  // Lane and pair of the lane that pair p of the head is, as a float's index
+  // into a table (its partner word two further on).
+  auto entry = [&](int jl, int e) { return ((e >> 1) * half + jl) * 4 + (e & 1); };
+  auto entry_of_pair = [&](int p) {
+    if (HALF) return entry(p / N, p % N);
+    const int v = p / M, q = p % M;
+    return v < half ? entry(v, q) : entry(v - half, q + M);
+  };
 
   grid_wait();
   grid_launch_dependents();
 
   if (kNorm) {
-    for (int d = threadIdx.x; d < a.dh; d += kThreads) {
-      float w = 1.0f;
-      if (sd.w != nullptr)
-        w = E::SIZE == 2 ? __bfloat162float(static_cast<const __nv_bfloat16*>(sd.w)[d])
+    for (int i = threadIdx.x; i < entries; i += kThreads)
+      weights[i] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (sd.w != nullptr) {
+      __syncthreads();
+      for (int d = threadIdx.x; d < a.dh; d += kThreads) {
+        int at;
+        if (!HALF)
+          at = entry_of_pair(d >> 1) + 2 * (d & 1);
+        else if (d < 2 * a.P)
+          at = entry_of_pair(d < a.P ? d : d - a.P) + (d < a.P ? 0 : 2);
+        else
+          at = entry(nr + (d / N - 2 * nr) / 2, d % N) + (d / N - 2 * nr) % 2 * 2;
+        reinterpret_cast<float*>(weights)[at] =
+            E::SIZE == 2 ? __bfloat162float(static_cast<const __nv_bfloat16*>(sd.w)[d])
                          : static_cast<const float*>(sd.w)[d];
-      weights[d] = w;
+      }
     }
   }
-  for (int i = a.P + lane; i < a.slots; i += 32)  // entries past the rotated pairs
-    angles[i] = angles[a.slots + i] = make_float2(1.0f, 0.0f);
+  for (int i = lane; i < 2 * entries; i += 32) angles[i] = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
   __syncthreads();
 
-  // The angles of a token into slot b, from its rows.
+  // The angles of a token into table b, from its rows.
   auto fetch_angles = [&](const Rows& rows, int b) {
+    float* const to = reinterpret_cast<float*>(angles + b * entries);
     for (int p = lane; p < a.P; p += 32) {
       const int axis = axis_of(a, p);
       const int row = axis == 0 ? rows.r[0] : axis == 1 ? rows.r[1] : axis == 2 ? rows.r[2] : rows.r[3];
-      if (row >= 0)
-        cp_async8(&angles[b * a.slots + p], a.table + (int64_t)row * a.P + p);
-      else
-        angles[b * a.slots + p] = make_float2(1.0f, 0.0f);
+      float* const at = to + entry_of_pair(p);
+      if (row >= 0) {
+        const float* from = reinterpret_cast<const float*>(a.table + (int64_t)row * a.P + p);
+        cp_async4(at, from);
+        cp_async4(at + 2, from + 1);
+      } else {
+        at[0] = 1.0f;
+        at[2] = 0.0f;
+      }
     }
+  };
+  // Whether some pair of the token has a zero sine: only then is each looked
+  // at (turn() below), else two pairs turn in four packed operations.
+  const bool partial = 2 * a.P < a.dh;
+  auto any_still = [&](int b) {
+    const float* const from = reinterpret_cast<const float*>(angles + b * entries);
+    bool z = partial;
+    for (int p = lane; p < a.P; p += 32) z |= from[entry_of_pair(p) + 2] == 0.0f;
+    return (bool)__any_sync(~0u, z);
   };
 
   struct Group {
     uint4 xa[U], xb[U], ya[kGrad ? U : 1], yb[kGrad ? U : 1];
   };
   auto load = [&](Group& g, int64_t t, int h0) {
+    const char* x = sd.x.p + t * sd.x.ts + (h0 + sub) * sd.x.hs;
+    const char* y = kGrad ? sd.dy.p + t * sd.dy.ts + (h0 + sub) * sd.dy.hs : nullptr;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * HPW + sub;
-      const bool on = h < h_end && t < a.T;
-      const char* x = sd.x.p + t * sd.x.ts + h * sd.x.hs;
+      const bool on = h0 + u * HPW + sub < h_end && t < a.T;
       g.xa[u] = on && va >= 0 ? ld_global_v4(x + va * 16) : make_uint4(0, 0, 0, 0);
       g.xb[u] = on && vb >= 0 ? ld_global_v4(x + vb * 16) : make_uint4(0, 0, 0, 0);
+      x += HPW * sd.x.hs;
       if (kGrad) {
-        const char* y = sd.dy.p + t * sd.dy.ts + h * sd.dy.hs;
         g.ya[u] = on && va >= 0 ? ld_global_v4(y + va * 16) : make_uint4(0, 0, 0, 0);
         g.yb[u] = on && vb >= 0 ? ld_global_v4(y + vb * 16) : make_uint4(0, 0, 0, 0);
+        y += HPW * sd.dy.hs;
       }
     }
   };
-  auto unpack = [&](float2(&f)[N], const uint4& va4, const uint4& vb4) {
-    float2 v[N / 2];
-    E::unpack2(va4, v);
+  auto rotate = [&](float2(&A)[M], float2(&B)[M], const float4* cs, bool still) {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) f[i] = v[i];
-    E::unpack2(vb4, v);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) f[N / 2 + i] = v[i];
-  };
-  auto rotate = [&](float2(&f)[N], const float* cs) {  // vector a's pairs of floats, then b's
-    constexpr bool back = MODE == kRotateBack || MODE == kNormBwd;
-    if (HALF) {
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float4 c = ld_shared_f4(cs + 2 * p0 + 4 * i);
-        turn<back>(f[i].x, f[N / 2 + i].x, c.x, c.y);
-        turn<back>(f[i].y, f[N / 2 + i].y, c.z, c.w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float4 c = ld_shared_f4(cs + 2 * (i < N / 4 ? p0 : p1) + 4 * (i < N / 4 ? i : i - N / 4));
-        turn<back>(f[2 * i].x, f[2 * i].y, c.x, c.y);
-        turn<back>(f[2 * i + 1].x, f[2 * i + 1].y, c.z, c.w);
+    for (int i = 0; i < M; ++i) {
+      const float4 t = ld_shared_f4(cs + i * half + jj);
+      if (still) {
+        turn<kBack>(A[i].x, B[i].x, t.x, t.z);
+        turn<kBack>(A[i].y, B[i].y, t.y, t.w);
+      } else {
+        const float2 c = make_float2(t.x, t.y);
+        const float2 s = kBack ? make_float2(-t.z, -t.w) : make_float2(t.z, t.w);
+        const float2 bs = mul2(B[i], make_float2(-s.x, -s.y)), as = mul2(A[i], s);
+        A[i] = fma2(A[i], c, bs);
+        B[i] = fma2(B[i], c, as);
       }
     }
-  };
-  auto weights4 = [&](int i) {  // of float pairs 2 i and 2 i + 1
-    const int v = i < N / 4 ? max(va, 0) : max(vb, 0);
-    return ld_shared_f4(weights + v * N + 4 * (i < N / 4 ? i : i - N / 4));
   };
 
-  float2 dw[kGrad ? N : 1];
+  float2 dwa[kGrad ? M : 1], dwb[kGrad ? M : 1];
   if (kGrad) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) dw[i] = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < M; ++i) dwa[i] = dwb[i] = make_float2(0.0f, 0.0f);
   }
 
   const int64_t step = (int64_t)gridDim.x * kWarps;
@@ -270,49 +338,59 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   for (int slot = 0; t < a.T; t += step, slot ^= 1) {
     cp_async_wait();
     __syncwarp();
+    const bool still = any_still(slot);
     if (t + step < a.T) {
       fetch_angles(rows, slot ^ 1);
       if (t + 2 * step < a.T) rows.load(a, t + 2 * step, lane);
     }
-    const float* cs = reinterpret_cast<const float*>(angles + slot * a.slots);
+    const float4* cs = angles + slot * entries;
 
     for (int h0 = h_begin; h0 < h_end; h0 += U * HPW) {
       Group next;
       const bool more = h0 + U * HPW < h_end;
       load(next, more ? t : t + step, more ? h0 + U * HPW : h_begin);
+      char* out = sd.out + t * sd.out_ts + (h0 + sub) * sd.out_hs;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * HPW + sub;
-        float2 f[N];
-        unpack(f, cur.xa[u], cur.xb[u]);
+      for (int u = 0; u < U; ++u, out += HPW * sd.out_hs) {
+        if (h0 + u * HPW >= h_end) break;
+        const bool on = h0 + u * HPW + sub < h_end;
+        float2 A[M], B[M];
+        split<HALF>(cur.xa[u], cur.xb[u], A, B, E());
         if (!kNorm) {
-          rotate(f, cs);
+          rotate(A, B, cs, still);
         } else {
           float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int i = 0; i < N; ++i) ss = fma2(f[i], f[i], ss);
+          for (int i = 0; i < M; ++i) ss = fma2(A[i], A[i], fma2(B[i], B[i], ss));
           float sx = ss.x + ss.y;
           if (!kGrad) {
+            // The rotation is linear: the weights before it, r after it, so
+            // that it does not wait for the sum.
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+              const float4 w = ld_shared_f4(weights + i * half + jj);
+              A[i] = mul2(A[i], make_float2(w.x, w.y));
+              B[i] = mul2(B[i], make_float2(w.z, w.w));
+            }
+            rotate(A, B, cs, still);
 #pragma unroll
             for (int o = P / 2; o > 0; o >>= 1) sx += __shfl_xor_sync(~0u, sx, o);
-            const float r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
+            const float2 r = splat2(rsqrtf(fmaf(sx, a.inv_dh, a.eps)));
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-              const float4 w = weights4(i);
-              f[2 * i] = mul2(mul2(f[2 * i], splat2(r)), make_float2(w.x, w.y));
-              f[2 * i + 1] = mul2(mul2(f[2 * i + 1], splat2(r)), make_float2(w.z, w.w));
+            for (int i = 0; i < M; ++i) {
+              A[i] = mul2(A[i], r);
+              B[i] = mul2(B[i], r);
             }
-            rotate(f, cs);
           } else {
-            float2 g[N];
-            unpack(g, cur.ya[u], cur.yb[u]);
-            rotate(g, cs);
+            float2 GA[M], GB[M];
+            split<HALF>(cur.ya[u], cur.yb[u], GA, GB, E());
+            rotate(GA, GB, cs, still);
             float2 hs = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-              const float4 w = weights4(i);
-              hs = fma2(mul2(g[2 * i], make_float2(w.x, w.y)), f[2 * i], hs);
-              hs = fma2(mul2(g[2 * i + 1], make_float2(w.z, w.w)), f[2 * i + 1], hs);
+            for (int i = 0; i < M; ++i) {
+              const float4 w = ld_shared_f4(weights + i * half + jj);
+              hs = fma2(mul2(GA[i], make_float2(w.x, w.y)), A[i], hs);
+              hs = fma2(mul2(GB[i], make_float2(w.z, w.w)), B[i], hs);
             }
             float sh = hs.x + hs.y;
 #pragma unroll
@@ -320,33 +398,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               sx += __shfl_xor_sync(~0u, sx, o);
               sh += __shfl_xor_sync(~0u, sh, o);
             }
-            const float r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
-            const float k = -r * r * r * (sh * a.inv_dh);
+            const float r = rsqrtf(fmaf(sx, a.inv_dh, a.eps));
+            const float2 k = splat2(-r * r * r * (sh * a.inv_dh)), r2 = splat2(r);
             // Lanes past the last head hold zeros, so they add nothing to dw
             // (g = 0) as long as r is finite; eps = 0 would make it 0 * inf.
-            const float rd = h < h_end ? r : 0.0f;
+            const float2 rd = splat2(on ? r : 0.0f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const float4 w = weights4(i / 2);
-              const float2 wi = i % 2 ? make_float2(w.z, w.w) : make_float2(w.x, w.y);
-              dw[i] = fma2(g[i], mul2(f[i], splat2(rd)), dw[i]);
-              f[i] = fma2(f[i], splat2(k), mul2(mul2(g[i], wi), splat2(r)));
+            for (int i = 0; i < M; ++i) {
+              const float4 w = ld_shared_f4(weights + i * half + jj);
+              dwa[i] = fma2(GA[i], mul2(A[i], rd), dwa[i]);
+              dwb[i] = fma2(GB[i], mul2(B[i], rd), dwb[i]);
+              A[i] = fma2(A[i], k, mul2(mul2(GA[i], make_float2(w.x, w.y)), r2));
+              B[i] = fma2(B[i], k, mul2(mul2(GB[i], make_float2(w.z, w.w)), r2));
             }
           }
         }
-        if (h < h_end) {
-          char* o = sd.out + t * sd.out_ts + h * sd.out_hs;
-          float2 v[N / 2];
-          if (va >= 0) {
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) v[i] = f[i];
-            *reinterpret_cast<uint4*>(o + va * 16) = E::pack2(v);
-          }
-          if (vb >= 0) {
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) v[i] = f[N / 2 + i];
-            *reinterpret_cast<uint4*>(o + vb * 16) = E::pack2(v);
-          }
+        if (on) {
+          uint4 oa, ob;
+          join<HALF>(A, B, oa, ob, E());
+          if (va >= 0) *reinterpret_cast<uint4*>(out + va * 16) = oa;
+          if (vb >= 0) *reinterpret_cast<uint4*>(out + vb * 16) = ob;
         }
       }
       cur = next;
@@ -354,20 +425,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 
   if (kGrad && sd.partial != nullptr) {
-    __syncthreads();  // the angles' place is reused
+    __syncthreads();  // the tables' place is reused
+    float* const red = reinterpret_cast<float*>(shared);
     // Lanes of the same j hold the same columns: sum them in a fixed tree.
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < M; ++i) {
 #pragma unroll
       for (int o = P; o < 32; o <<= 1) {
-        dw[i].x += __shfl_xor_sync(~0u, dw[i].x, o);
-        dw[i].y += __shfl_xor_sync(~0u, dw[i].y, o);
+        dwa[i].x += __shfl_xor_sync(~0u, dwa[i].x, o);
+        dwa[i].y += __shfl_xor_sync(~0u, dwa[i].y, o);
+        dwb[i].x += __shfl_xor_sync(~0u, dwb[i].x, o);
+        dwb[i].y += __shfl_xor_sync(~0u, dwb[i].y, o);
       }
-      const int v = i < N / 2 ? va : vb;
-      if (sub == 0 && v >= 0) {
-        float* to = red + warp * a.dh + v * N + 2 * (i < N / 2 ? i : i - N / 2);
-        to[0] = dw[i].x;
-        to[1] = dw[i].y;
+      if (sub == 0) {
+        float* const to = red + warp * a.dh;
+        if (HALF) {
+          if (va >= 0) to[va * N + 2 * i] = dwa[i].x, to[va * N + 2 * i + 1] = dwa[i].y;
+          if (vb >= 0) to[vb * N + 2 * i] = dwb[i].x, to[vb * N + 2 * i + 1] = dwb[i].y;
+        } else {
+          const int v = i < M / 2 ? va : vb, e = 4 * (i < M / 2 ? i : i - M / 2);
+          if (v >= 0) {
+            to[v * N + e] = dwa[i].x, to[v * N + e + 1] = dwb[i].x;
+            to[v * N + e + 2] = dwa[i].y, to[v * N + e + 3] = dwb[i].y;
+          }
+        }
       }
     }
     store_partial(red, sd.partial + ((int64_t)chunk * gridDim.x + blockIdx.x) * a.dh, a.dh);
@@ -446,7 +527,7 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_cons
       if (kNorm) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sx += __shfl_xor_sync(~0u, sx, o);
-        r = 1.0f / sqrtf(fmaf(sx, a.inv_dh, a.eps));
+        r = rsqrtf(fmaf(sx, a.inv_dh, a.eps));
       }
       if (MODE != kNormBwd) {
 #pragma unroll
@@ -545,17 +626,20 @@ cudaError_t launch(void* kernel, dim3 grid, int threads, size_t smem, void** par
   return cudaLaunchKernelExC(&cfg, kernel, params);
 }
 
-// Head groups in flight by mode.
+// Head groups in flight: what fits 128 registers a thread (the norm's backward
+// holds twice the tensors and its weight sums; with two groups of bf16 heads
+// it spilled, and 8192 tokens x 24 heads x 128 took 41.0 instead of 30.6 us).
+constexpr int groups_in_flight(int mode, int es) { return mode != kNormBwd ? 4 : es == 2 ? 1 : 2; }
+
 template <class E, int P, bool HALF>
 void* vec_kernel(int mode) {
   switch (mode) {
-    case kRotate: return (void*)rope_vec_kernel<E, P, HALF, kRotate, 4>;
-    case kRotateBack: return (void*)rope_vec_kernel<E, P, HALF, kRotateBack, 4>;
-    case kNormFwd: return (void*)rope_vec_kernel<E, P, HALF, kNormFwd, 4>;
-    default: return (void*)rope_vec_kernel<E, P, HALF, kNormBwd, 2>;
+    case kRotate: return (void*)rope_vec_kernel<E, P, HALF, kRotate, groups_in_flight(kRotate, E::SIZE)>;
+    case kRotateBack: return (void*)rope_vec_kernel<E, P, HALF, kRotateBack, groups_in_flight(kRotateBack, E::SIZE)>;
+    case kNormFwd: return (void*)rope_vec_kernel<E, P, HALF, kNormFwd, groups_in_flight(kNormFwd, E::SIZE)>;
+    default: return (void*)rope_vec_kernel<E, P, HALF, kNormBwd, groups_in_flight(kNormBwd, E::SIZE)>;
   }
 }
-int groups_in_flight(int mode) { return mode == kNormBwd ? 2 : 4; }
 
 template <class E, bool HALF>
 void* pick_kernel(int lanes, int mode) {
@@ -604,7 +688,7 @@ cudaError_t make_plan(int64_t T, const int (&heads)[2], int dh, int mode, bool v
   const int fewer = heads[0] == 0   ? heads[1]
                     : heads[1] == 0 ? heads[0]
                                     : (heads[0] < heads[1] ? heads[0] : heads[1]);
-  const int most = unit * (vec ? groups_in_flight(mode) : 4);
+  const int most = unit * (vec ? groups_in_flight(mode, es) : 4);
   int64_t per = fewer > most ? fewer : most;
   const int64_t split = T > 0 ? (warps + T - 1) / T : 1;  // chunks that give every warp a token
   const int64_t small = (heads[0] + heads[1] + split - 1) / split;
@@ -616,7 +700,7 @@ cudaError_t make_plan(int64_t T, const int (&heads)[2], int dh, int mode, bool v
   }
   const int chunks = p->chunks[0] + p->chunks[1];
   int64_t gx = (T + kWarps - 1) / kWarps;
-  const int64_t all = ((int64_t)kCtasPerSm * sms + chunks - 1) / chunks;
+  const int64_t all = (int64_t)kCtasPerSm * sms / chunks;  // one wave, not a CTA more
   if (gx > all) gx = all;
   p->grid_x = (int)(gx < 1 ? 1 : gx);
   return cudaSuccess;
@@ -727,12 +811,9 @@ int run(int mode, const adaln_heads_t* const (&x)[2], const adaln_heads_t* const
       kernel = half ? pick_kernel<BF16, true>(p.lanes, mode) : pick_kernel<BF16, false>(p.lanes, mode);
     else
       kernel = half ? pick_kernel<F32, true>(p.lanes, mode) : pick_kernel<F32, false>(p.lanes, mode);
-    // Every pair a lane may hold has an entry: dh / 2, and one vector's worth
-    // past P for the unrotated vectors of the halves layout.
-    const int past = a.P + 16 / es;
-    a.slots = (past > dh / 2 + 1 ? past : dh / 2 + 1) + 1 & ~1;
-    const size_t angles = (size_t)kWarps * 2 * a.slots * sizeof(float2);
-    smem = (angles > smem ? angles : smem) + (size_t)(dh + 3) / 4 * 16;
+    const size_t table = (size_t)(16 / es / 2) * ((a.nvec + 1) / 2) * sizeof(float4);
+    const size_t tables = table * (2 * kWarps + (mode == kNormFwd || mode == kNormBwd ? 1 : 0));
+    smem = tables > smem ? tables : smem;
   } else {
     kernel = dtype == ADALN_BF16 ? scalar_kernel<BF16>(mode) : scalar_kernel<F32>(mode);
   }
