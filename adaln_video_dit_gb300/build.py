@@ -15,9 +15,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libadaln.so")
 LIB_TUNING = os.path.join(HERE, "libadaln_tuning.so")
-SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "ffn.cu", "host.cu", "noalloc.cu", "rope.cu",
+SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "ffn.cu", "ffn_skinny.cu", "host.cu", "noalloc.cu", "rope.cu",
            "selftest.cu"]
-HEADERS = ["common.cuh", "ring.cuh", "tc.cuh", "internal.h"]
+HEADERS = ["common.cuh", "ring.cuh", "tc.cuh", "ffn.cuh", "internal.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -29,8 +29,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "internal.h"
-#include "tc.cuh"
+#include "ffn.cuh"
 
 namespace adaln {
 namespace {
@@ -54,11 +53,6 @@ constexpr int kBlock = 32 * 32 * 2;
 // others; and the ring stages that fit beside it.
 ADALN_HD constexpr int staging_bytes(int kind) { return (kind == kGateBwd ? 3 : 2) * kBlock; }
 ADALN_HD constexpr int stages_of(int kind) { return kind == kGateBwd ? 5 : 6; }
-// The saved g and u are only ever read by the backward's epilogue, so they lie
-// in its order: for each 32 x 32 block twelve rows of 32 lanes x 16 bytes (g:
-// four of upper halves, two of the next bytes; then u), each one coalesced
-// access of a warp.
-constexpr int kSavedVecs = 12, kSavedBlock = kSavedVecs * 512;
 constexpr int smem_of(int kind) {
   return 1024 + stages_of(kind) * kStageBytes + kEpiWarps * staging_bytes(kind) + 256;
 }
@@ -120,35 +114,6 @@ __device__ __forceinline__ Unit unit_of(const Dims* shapes, int problems, int u)
   r.n = in / rows;
   r.m = group * kGroupM + in - r.n * rows;
   return r;
-}
-
-// ----- activations --------------------------------------------------------------
-// p such that act(g) = g p, and act'(g).  The sigmoid form of the tanh
-// approximation (0.5 (1 + tanh z) = 1 / (1 + exp(-2 z))) keeps its relative
-// accuracy for negative g.  The fast exponential and division are good to a
-// few fp32 units, far below the bf16 rounding that follows.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
-
-template <int ACT>
-__device__ __forceinline__ void gate(float g, float& p, float& d) {
-  if (ACT == ADALN_ACT_SILU) {
-    p = sigmoid(g);
-    d = p * (1.0f + g * (1.0f - p));
-  } else if (ACT == ADALN_ACT_GELU_TANH) {
-    const float k = 0.7978845608028654f, c = 0.044715f;
-    const float g2 = g * g;
-    p = sigmoid(2.0f * k * g * (1.0f + c * g2));
-    const float q = p * (1.0f - p);
-    d = q > 0.0f ? p + 2.0f * k * g * q * (1.0f + 3.0f * c * g2) : p;
-  } else {
-    p = 0.5f * erfcf(-0.7071067811865476f * g);
-    d = p + g * 0.3989422804014327f * __expf(-0.5f * g * g);
-  }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
 }
 
 // This lane's row of 32 values, as 16 words of bf16 pairs, into a block (rows
@@ -621,9 +586,8 @@ cudaError_t encode_fn(EncodeFn* out) {
   return cudaSuccess;
 }
 
-// Tensor map of a row-major bf16 matrix [rows, cols] in boxes of box_cols (64
-// or 32: rows of 128 or 64 bytes, swizzled at that width) x box_rows.  What
-// lies outside reads as zero and is not written.
+}  // namespace
+
 cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_cols,
                      int box_rows) {
   EncodeFn fn;
@@ -639,6 +603,26 @@ cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, 
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+cudaError_t launch_cluster(void* kernel, int grid, int threads, int smem, int cluster, void** params,
+                           cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, kernel, params);
+}
+
+namespace {
 
 // Operand of a product: a row-major matrix whose rows run along k (K-major)
 // or along m or n (MN-major).
@@ -669,24 +653,6 @@ void* kernel_of(int kind, int act) {
          : kind == kGate     ? gemm_kernel<kGate>(act)
          : kind == kGateSave ? gemm_kernel<kGateSave>(act)
                              : gemm_kernel<kGateBwd>(act);
-}
-
-cudaError_t launch_cluster(void* kernel, int grid, int threads, int smem, int cluster, void** params,
-                           cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelExC(&cfg, kernel, params);
 }
 
 // CTA pairs that the device holds at once (one CTA an SM), after allowing the
@@ -726,24 +692,25 @@ cudaError_t pairs_of_device(int* pairs) {
   return cudaSuccess;
 }
 
-int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-// k splits of a product of `tiles` tiles and kb k blocks on `pairs` CTA pairs,
-// with `other` k blocks of work per pair beside it: the fewest rounds of k
-// blocks, a unit costing about 6 blocks of start and end.  A split costs its
-// fp32 partials written and read again, about 0.3 k blocks a unit.
-int choose_splits(int tiles, int kb, int pairs, int64_t other) {
+// k splits of a product [M, N] of `tiles` tiles and kb k blocks on `pairs` CTA
+// pairs, with `other` k blocks of work per pair beside it: the fewest rounds of
+// k blocks (0.28 us each), a unit costing about 6 of them at its start and end.
+// A split costs the joining launch, about 14, and its fp32 partials written and
+// read again, mostly in L2 (256 tokens, D = 5120, F = 13824: the 7 splits that
+// fill the pairs best took 44.7 + 9.6 us, 3 splits 38 + 6).
+int choose_splits(int64_t M, int N, int kb, int pairs, int64_t other) {
+  const int64_t tiles = (int64_t)div_up(M, kTM) * div_up(N, kTN);
   int best = 1;
   double least = 0;
   for (int s = 1; s <= 32 && (s == 1 || kb / s >= 8); ++s) {
-    const double rounds = (double)div_up((int64_t)tiles * s, pairs);
+    const double rounds = (double)div_up(tiles * s, pairs);
     double cost = rounds * (div_up(kb, s) + 6);
     // Beside other work only the longest unit and the total matter.
     if (other > 0) {
       const double mean = (double)tiles * (kb + 6.0 * s) / pairs + (double)other;
       cost = mean > 2.0 * (div_up(kb, s) + 6) ? mean : 2.0 * (div_up(kb, s) + 6);
     }
-    if (s > 1) cost += 4 + 0.3 * s * tiles / pairs;
+    if (s > 1) cost += 14 + 8.0 * s * (double)M * N / 1.4e6;
     if (s == 1 || cost < least) {
       least = cost;
       best = s;
@@ -757,9 +724,8 @@ struct Split {
   size_t bytes;  // of the fp32 partials
 };
 Split split_of(int64_t M, int N, int kb, int pairs, int64_t other) {
-  const int tiles = div_up(M, kTM) * div_up(N, kTN);
   Split s;
-  s.splits = choose_splits(tiles, kb, pairs, other);
+  s.splits = choose_splits(M, N, kb, pairs, other);
   s.bytes = s.splits > 1 ? (size_t)s.splits * M * N * 4 : 0;
   return s;
 }
@@ -816,8 +782,6 @@ cudaError_t launch_join(const Problem& p, void* to, cudaStream_t st) {
   });
 }
 
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int check(int64_t T, int32_t D, int32_t F, adaln_dtype_t dt, int act) {
@@ -830,16 +794,16 @@ int check(int64_t T, int32_t D, int32_t F, adaln_dtype_t dt, int act) {
   return ADALN_OK;
 }
 
-size_t saved_bytes(int64_t T, int32_t F) {
-  return (size_t)div_up(T, 32) * div_up(F, 32) * kSavedBlock;
-}
-
 struct FwdPlan {
   Split y;
   size_t bytes;
 };
 FwdPlan fwd_plan(int64_t T, int32_t D, int32_t F, int pairs) {
-  FwdPlan p;
+  FwdPlan p = {};
+  if (skinny_serves(T)) {
+    p.bytes = skinny_workspace(T, F);
+    return p;
+  }
   p.y = split_of(T, D, div_up(F, kBK), pairs, 0);
   p.bytes = round256((size_t)T * F * 2) + round256(p.y.bytes);
   return p;
@@ -905,6 +869,10 @@ int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd,
   if (workspace_bytes < plan.bytes) return ADALN_ERR_WORKSPACE;
   GemmArgs a = {};
   if ((e = status_word(&a.status)) != cudaSuccess) return launch_failed(e);
+  if (skinny_serves(T)) {
+    e = skinny_fwd(x, wg, wu, wd, (int)T, D, F, act, y, saved, workspace, a.status, st);
+    return e == cudaSuccess ? ADALN_OK : launch_failed(e);
+  }
 
   char* ws = static_cast<char*>(workspace);
   a.saved = static_cast<uint4*>(saved);

@@ -112,7 +112,7 @@ def call(L, x, wg, wu, wd, dy, act):
 
 SHAPES = [
     (1, 8, 8), (1, 64, 128), (1, 1536, 4096), (2, 512, 1376), (3, 72, 40), (16, 1536, 512),
-    (17, 256, 8192), (40, 264, 6000), (64, 520, 2000), (65, 128, 128), (127, 1000, 344),
+    (17, 256, 8192), (32, 392, 904), (33, 392, 904), (40, 264, 6000), (64, 520, 2000), (65, 128, 128), (127, 1000, 344),
     (128, 128, 128), (129, 136, 264), (200, 5120, 648), (255, 256, 512), (256, 256, 256),
     (257, 520, 312), (300, 64, 1000), (513, 264, 2056), (1111, 1000, 2728), (2500, 512, 768),
     (4100, 8, 16),
