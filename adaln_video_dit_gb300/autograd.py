@@ -1,4 +1,5 @@
-"""The fused AdaLN operator as one autograd node.
+"""The operators as autograd nodes: the fused AdaLN, the rotary positions and
+norm of queries and keys, and the gated feed-forward block.
 
 AdaptiveLoad (Technical summary, section 2.B, "graph simplification"): the
 LayerNorm -> multiply -> add chain of an adaLN modulation site collapses into
@@ -70,3 +71,108 @@ class AdaLNModulate(torch.nn.Module):
 
     def extra_repr(self):
         return f"eps={self.eps}"
+
+
+class QKNormRopeFunction(torch.autograd.Function):
+    """Rotary positions of queries and keys, with an optional RMS norm of every
+    head first.  Saves q and k themselves (they may be views of a packed
+    projection), the weights, the table and the positions; nothing else."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, table, pos, axis_pairs, interleaved, norm, eps):
+        wq = wq.contiguous() if wq is not None else None
+        wk = wk.contiguous() if wk is not None else None
+        ctx.how = (tuple(axis_pairs), interleaved, norm)
+        ctx.eps = eps
+        ctx.save_for_backward(*((q, k) if norm else (None, None)), wq, wk, table, pos)
+        return _lib.adaln_qk_rope_fwd(q, k, table, pos, *ctx.how, wq=wq, wk=wk, eps=eps)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, wq, wk, table, pos = ctx.saved_tensors
+        dq_out, dk_out = (d if d is None or d.stride(-1) == 1 else d.contiguous()
+                          for d in (dq_out, dk_out))
+        dq, dk, dwq, dwk = _lib.adaln_qk_rope_bwd(dq_out, dk_out, table, pos, *ctx.how, q=q, k=k,
+                                                  wq=wq, wk=wk, eps=ctx.eps)
+        return (dq, dk, dwq.to(wq.dtype) if wq is not None else None,
+                dwk.to(wk.dtype) if wk is not None else None) + (None,) * 6
+
+
+def qk_rope(q, k, table, pos, axis_pairs, interleaved=True):
+    """Rotary positions of q [T, hq, dh] and k [T, hk, dh] (differentiable)."""
+    return QKNormRopeFunction.apply(q, k, None, None, table, pos, axis_pairs, interleaved, False,
+                                    0.0)
+
+
+def qk_norm_rope(q, k, wq, wk, table, pos, axis_pairs, interleaved=True, eps=1e-6):
+    """RMS norm of every head (weights wq, wk [dh], or None for ones), then the
+    rotary positions, in one pass (differentiable in q, k, wq, wk)."""
+    return QKNormRopeFunction.apply(q, k, wq, wk, table, pos, axis_pairs, interleaved, True,
+                                    float(eps))
+
+
+class QKNormRope(torch.nn.Module):
+    """Module form: holds the two weights; forward(q, k, table, pos) -> (q, k)."""
+
+    def __init__(self, head_dim, axis_pairs, interleaved=True, eps=1e-6, device=None, dtype=None):
+        super().__init__()
+        self.wq = torch.nn.Parameter(torch.ones(head_dim, device=device, dtype=dtype))
+        self.wk = torch.nn.Parameter(torch.ones(head_dim, device=device, dtype=dtype))
+        self.axis_pairs, self.interleaved, self.eps = tuple(axis_pairs), interleaved, float(eps)
+
+    def forward(self, q, k, table, pos):
+        return qk_norm_rope(q, k, self.wq, self.wk, table, pos, self.axis_pairs, self.interleaved,
+                            self.eps)
+
+    def extra_repr(self):
+        return f"axis_pairs={self.axis_pairs}, interleaved={self.interleaved}, eps={self.eps}"
+
+
+class GatedFFNFunction(torch.autograd.Function):
+    """y = (act(x wg') * (x wu')) wd', saving x and the two projections (24 bits
+    a value); without a gradient to come, nothing."""
+
+    @staticmethod
+    def forward(ctx, x, wg, wu, wd, act):
+        shape = x.shape
+        x2 = x.reshape(-1, shape[-1]).contiguous()
+        wg, wu, wd = wg.contiguous(), wu.contiguous(), wd.contiguous()
+        y, saved = _lib.adaln_ffn_fwd(x2, wg, wu, wd, act=act, save=any(ctx.needs_input_grad))
+        ctx.save_for_backward(x2, wg, wu, wd, saved)
+        ctx.act, ctx.shape = act, shape
+        return y.reshape(shape)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, wg, wu, wd, saved = ctx.saved_tensors
+        dy2 = dy.reshape(x2.shape).to(x2.dtype).contiguous()
+        dx, dwg, dwu, dwd = _lib.adaln_ffn_bwd(dy2, x2, wg, wu, wd, saved, act=ctx.act)
+        return dx.reshape(ctx.shape), dwg, dwu, dwd, None
+
+
+def gated_ffn(x, wg, wu, wd, act="silu"):
+    """The gated feed-forward block of bf16 x [..., D] with wg, wu [F, D], wd
+    [D, F]; act "silu", "gelu_tanh" or "gelu" (differentiable)."""
+    return GatedFFNFunction.apply(x, wg, wu, wd, act)
+
+
+class GatedFFN(torch.nn.Module):
+    """Module form of the gated feed-forward block (bf16, no biases)."""
+
+    def __init__(self, dim, hidden, act="silu", device=None):
+        super().__init__()
+        if act not in _lib.ACTS:
+            raise ValueError(f"act must be one of {sorted(_lib.ACTS)}, got {act!r}")
+
+        def weight(rows, cols):
+            w = torch.empty(rows, cols, device=device, dtype=torch.bfloat16)
+            return torch.nn.Parameter(torch.nn.init.normal_(w, std=cols ** -0.5))
+
+        self.wg, self.wu, self.wd = weight(hidden, dim), weight(hidden, dim), weight(dim, hidden)
+        self.act = act
+
+    def forward(self, x):
+        return gated_ffn(x, self.wg, self.wu, self.wd, self.act)
+
+    def extra_repr(self):
+        return f"dim={self.wg.shape[1]}, hidden={self.wg.shape[0]}, act={self.act!r}"

@@ -1,0 +1,80 @@
+"""The operators as autograd nodes, and together in the example block."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+from gpu_helpers import status_ok
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def example():
+    spec = importlib.util.spec_from_file_location("dit_block",
+                                                  os.path.join(ROOT, "examples", "dit_block.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_qk_norm_rope_node_is_the_calls(adaln):
+    from adaln_video_dit_gb300 import autograd as A
+    from adaln_video_dit_gb300 import rotary
+    T, h, dh = 50, 4, 64
+    qkv = torch.randn(T, 3, h, dh, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    wq = torch.randn(dh, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    wk = torch.randn(dh, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    pairs = rotary.split_pairs(dh // 2)
+    table = rotary.rope_table(10, pairs, device="cuda")
+    pos = rotary.grid_positions([(2, 2, 4, 6)], device="cuda")
+    q, k, _ = qkv.unbind(1)
+    qo, ko = A.qk_norm_rope(q, k, wq, wk, table, pos, pairs)
+    dqo, dko = torch.randn_like(qo), torch.randn_like(ko)
+    (qo * dqo + ko * dko).float().sum().backward()
+    with torch.no_grad():
+        q, k, _ = qkv.unbind(1)
+        want = adaln.adaln_qk_rope_fwd(q, k, table, pos, pairs, norm=True, wq=wq, wk=wk)
+        dq, dk, dwq, dwk = adaln.adaln_qk_rope_bwd(dqo, dko, table, pos, pairs, norm=True, q=q, k=k,
+                                                   wq=wq, wk=wk)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+    assert torch.equal(qkv.grad[:, 0], dq) and torch.equal(qkv.grad[:, 1], dk)
+    assert not qkv.grad[:, 2].any()
+    assert torch.equal(wq.grad, dwq.bfloat16()) and torch.equal(wk.grad, dwk.bfloat16())
+    # plain rotation: its gradient turns back, so q comes back to a bf16 rounding
+    x = torch.randn(T, h, dh, device="cuda", requires_grad=True)
+    y, _ = A.qk_rope(x, x, table, pos, pairs, interleaved=False)
+    (y * y.detach()).sum().backward()
+    assert float((x.grad - x.detach()).abs().max()) < 1e-5
+    z, none = A.qk_rope(x, None, table, pos, pairs, interleaved=False)  # queries alone
+    z.sum().backward()
+    assert none is None and torch.equal(z, y)
+    status_ok()
+
+
+def test_gated_ffn_node_is_the_calls(adaln):
+    from adaln_video_dit_gb300 import autograd as A
+    m = A.GatedFFN(96, 160, act="gelu", device="cuda")
+    x = torch.randn(3, 21, 96, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = m(x)
+    dy = torch.randn_like(y)
+    y.backward(dy)
+    x2 = x.detach().reshape(-1, 96)
+    want, saved = adaln.adaln_ffn_fwd(x2, m.wg, m.wu, m.wd, act="gelu", save=True)
+    grads = adaln.adaln_ffn_bwd(dy.reshape(-1, 96), x2, m.wg, m.wu, m.wd, saved, act="gelu")
+    assert torch.equal(y.reshape(-1, 96), want)
+    for got, ref in zip((x.grad.reshape(-1, 96), m.wg.grad, m.wu.grad, m.wd.grad), grads):
+        assert torch.equal(got, ref)
+    with torch.no_grad():
+        assert torch.equal(m(x), y)
+    with pytest.raises(ValueError):
+        A.GatedFFN(8, 8, act="relu", device="cuda")
+    status_ok()
+
+
+def test_example_block_trains(adaln):
+    losses = example().main(["--dim", "256", "--heads", "4", "--hidden", "512", "--steps", "8"])
+    assert all(map(lambda v: v == v, losses))
+    assert losses[-1] < losses[0]
+    status_ok()

@@ -1,4 +1,4 @@
-"""Host-side argument checks of the rotary entry points: refused before any
+"""Host-side argument checks of the rotary and feed-forward entry points: refused before any
 CUDA call (no GPU is touched; addresses are never dereferenced)."""
 import ctypes
 
@@ -84,3 +84,43 @@ def test_rope_binding_rejects_host_tensors(lib):
         lib.adaln_qk_rope_fwd(x, None, torch.zeros(3, 4, 2), torch.zeros(4, 1, dtype=torch.int32),
                               (4,))
     assert lib.strerror(lib.ADALN_ERR_POS) != lib.strerror(12345)
+
+
+def ffn_fwd(lib, **kw):
+    a = dict(x=A, wg=A, wu=A, wd=A, T=10, D=64, F=128, dt=lib.ADALN_BF16, act=0, y=B, saved=B, ws=B,
+             wsb=1 << 30)
+    a.update(kw)
+    return lib.raw.adaln_ffn_fwd(*a.values(), None)
+
+
+def ffn_bwd(lib, **kw):
+    a = dict(dy=A, x=A, wg=A, wu=A, wd=A, saved=A, T=10, D=64, F=128, dt=lib.ADALN_BF16, act=0,
+             dx=B, dwg=B, dwu=B, dwd=B, ws=B, wsb=1 << 30)
+    a.update(kw)
+    return lib.raw.adaln_ffn_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [ffn_fwd, ffn_bwd])
+def test_ffn_refusals(lib, call):
+    assert call(lib, dt=lib.ADALN_F32) == lib.ADALN_ERR_DTYPE
+    for bad in (dict(T=-1), dict(T=2 ** 24 + 1), dict(D=0), dict(D=12), dict(F=4), dict(F=100),
+                dict(D=2 ** 18 + 8), dict(F=-8)):
+        assert call(lib, **bad) == lib.ADALN_ERR_DIM, bad
+    assert call(lib, act=3) == lib.ADALN_ERR_ARG
+    for k in ("x", "wg", "wu", "wd", "ws"):
+        assert call(lib, **{k: None}) == lib.ADALN_ERR_NULL, k
+        assert call(lib, **{k: A + 8}) == lib.ADALN_ERR_ALIGN, k
+
+
+def test_ffn_only_what_is_missing_is_refused(lib):
+    assert ffn_fwd(lib, y=None) == lib.ADALN_ERR_NULL
+    assert ffn_fwd(lib, saved=B + 8) == lib.ADALN_ERR_ALIGN
+    assert ffn_bwd(lib, saved=None) == lib.ADALN_ERR_NULL
+    assert ffn_bwd(lib, T=0, dwd=None) == lib.ADALN_ERR_NULL
+    assert ffn_fwd(lib, T=0, x=None, y=None, ws=None, saved=None) == lib.ADALN_OK
+    n = ctypes.c_size_t(0)
+    assert lib.raw.adaln_ffn_saved_size(40, 64, 40, lib.ADALN_BF16, ctypes.byref(n)) == lib.ADALN_OK
+    assert n.value == 2 * 2 * 6144  # blocks of 32 x 32 values, two of 24 bits each
+    assert lib.raw.adaln_ffn_saved_size(40, 64, 40, lib.ADALN_BF16, None) == lib.ADALN_ERR_NULL
+    assert lib.raw.adaln_ffn_workspace_size(40, 64, 40, lib.ADALN_BF16, None, None) == lib.ADALN_ERR_NULL
+    assert lib.raw.adaln_ffn_workspace_size(40, 64, 41, lib.ADALN_BF16, None, None) == lib.ADALN_ERR_DIM
