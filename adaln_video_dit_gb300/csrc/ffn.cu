@@ -22,8 +22,8 @@
 // another: 2^-15 relative), not as bf16: with 8 bits of mantissa their rounding
 // would enter dg, du and h beside those arrays' own.
 //
-// A kernel is persistent, one CTA pair per two SMs: a 256 x 256 tile a pair, k
-// steps of 64 through a ring of TMA-filled stages; per CTA one producer warp,
+// A kernel is persistent, one CTA pair per two SMs: a 256 x 256 tile a pair
+// (narrower ones where that fills the pairs better), k steps of 64 through a ring of TMA-filled stages; per CTA one producer warp,
 // one issuing warp (even CTA) and eight epilogue warps, two accumulators in
 // tensor memory so that a tile's epilogue runs under the next tile's products.
 #include <cmath>
@@ -41,7 +41,9 @@ enum { kPlain = 0, kGate = 1, kGateSave = 2, kGateBwd = 3, kKinds = 4 };
 constexpr int kBK = 64;                    // k values of a stage
 constexpr int kTileBytes = 128 * kBK * 2;  // one CTA's share of an operand stage
 constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kTM = 256, kTN = 256;        // tile of a CTA pair
+// Tile of a CTA pair: 256 rows x 2 w columns, w the rows of B that each CTA
+// stages (128, 96 or 64: choose_tiling); kGate: w columns of g and w of u.
+constexpr int kTM = 256, kAccCols = 256;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 // Outputs leave through blocks of 32 rows x 32 columns in shared memory, copied
@@ -63,6 +65,7 @@ constexpr int kMaxProblems = 4;
 struct Dims {        // what the roles of a CTA read of a problem
   int M, N;
   int kb0, kb;         // k blocks of segment 0, of both
+  int w;               // rows of B a CTA stages
   int tiles_m, tiles_n, splits;
   int first;           // first unit of the problem
   int a_mn, b_mn;      // operand layouts
@@ -77,6 +80,9 @@ struct Problem {
 struct GemmArgs {
   Problem p[kMaxProblems];
   int problems, units;
+  // Order of the units (unit_index): the first `lead` are long ones, each worth
+  // `worth` of the others.
+  int lead, worth;
   // Gate epilogues ([T, F] each).
   CUtensorMap h, dg, du;
   uint4* saved;
@@ -89,6 +95,19 @@ struct Unit {
   int k0, k1;      // k blocks
   int split;
 };
+
+// Unit i of CTA pair c out of n, or one past the last unit.  All pairs walk the
+// long units round-robin; those that a last, partial round of them leaves free
+// take `worth` shorter ones each meanwhile; then all walk the rest.  (Unit costs
+// are known, so this is the order in which a queue would hand them out.)
+__device__ __forceinline__ int unit_index(int c, int i, int n, int lead, int worth) {
+  const int extra = lead % n, first = lead / n + (c < extra);
+  if (i < first) return i * n + c;
+  i -= first;
+  const int free = n - extra, rest = lead + worth * free;
+  if (c < extra) return rest + i * n + free + c;
+  return i < worth ? lead + i * free + c - extra : rest + (i - worth) * n + c - extra;
+}
 
 // `shapes` is the problems' copy in shared memory (reads of the kernel's
 // parameters with an index cost several hundred cycles each).
@@ -155,21 +174,21 @@ __device__ __forceinline__ float saved_value(const uint4& w, uint32_t b0, uint32
   return __uint_as_float((e % 2 ? x & 0xffff0000u : x << 16) | (b >> (8 * (e % 4)) & 0xff) << 8);
 }
 
-// ----- epilogues: one warp's 32 rows x half of the tile's columns -----------------
-// `row0` is the warp's first row of the output, `half` its column half, `acc`
+// ----- epilogues: one warp's 32 rows x every other 32 of the tile's columns -----------------
+// `row0` is the warp's first row of the output, `half` which ones, `acc`
 // its lanes of the accumulator, `buf` its staging memory.
 
 __device__ __forceinline__ void epilogue_plain(const Problem& p, const Dims& s, const Unit& u,
                                                uint32_t acc, int row0, int half, uint32_t buf,
                                                int lane, int& turn) {
-  const int M = s.M, N = s.N, splits = s.splits;
+  const int M = s.M, N = s.N, splits = s.splits, chunks = s.w / 16;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const int col = u.n * kTN + half * 128 + c * 32;
+  for (int c = half; c < chunks; c += 2) {
+    const int col = u.n * 2 * s.w + c * 32;
     if (col >= N) break;
     __syncwarp();
     uint32_t r[32];
-    tmem_ld32(acc + half * 128 + c * 32, r);
+    tmem_ld32(acc + c * 32, r);
     tc_wait_ld();
     if (splits > 1) {
       const int left = row0 + lane < M ? N - col : 0;  // columns of this row to write
@@ -204,15 +223,15 @@ template <int ACT, bool SAVE>
 __device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Dims& s, const Unit& u,
                                               uint32_t acc, int row0, int half, uint32_t buf,
                                               int lane, int& turn) {
-  const int M = s.M, N = s.N;
+  const int M = s.M, N = s.N, w_cols = s.w;
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    const int col = u.n * 128 + half * 64 + c * 32;
+  for (int c = half; c < w_cols / 32; c += 2) {
+    const int col = u.n * w_cols + c * 32;
     if (col >= N) break;
     __syncwarp();
     uint32_t g[32], v[32];
-    tmem_ld32(acc + half * 64 + c * 32, g);
-    tmem_ld32(acc + 128 + half * 64 + c * 32, v);
+    tmem_ld32(acc + c * 32, g);
+    tmem_ld32(acc + w_cols + c * 32, v);
     tc_wait_ld();
     uint32_t w[16];
 #pragma unroll
@@ -348,6 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  // (Constant while the previous kernel runs: fetched before the wait for it.)
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + a.problems) {
+    const Problem& p = a.p[threadIdx.x - 64];
+    prefetch_map(&p.a[0]);
+    prefetch_map(&p.b[kIsGate ? (int)rank : 0]);
+  }
   if (threadIdx.x >= 32 && threadIdx.x < 32 + kMaxProblems)
     shapes[threadIdx.x - 32] = a.p[threadIdx.x - 32].s;
   if (warp == 2) tmem_alloc<2>(tmem_ptr, 512);
@@ -362,6 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
 
   const int units = a.units, problems = a.problems;
+  const int lead = a.lead, worth = a.worth;
+  auto index = [&](int i) { return unit_index(cluster, i, clusters, lead, worth); };
   auto unit = [&](int ui) { return unit_of(shapes, problems, min(ui, units - 1)); };
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (mbar_wait_spin(bar, parity, abort_flag)) return true;
@@ -375,15 +402,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t parity = 0;
     bool ok = true;
-    Unit next = unit(cluster);
-    for (int ui = cluster; ok && ui < units; ui += clusters) {
+    int ui = index(0);
+    Unit next = unit(ui);
+    for (int i = 1; ok && ui < units; ++i) {
       const Unit u = next;
       // In registers before the loop: after each asm with a memory clobber
       // they would be read again.
       const Problem& p = a.p[u.i];
       const Dims& sh = shapes[u.i];
       const int m = u.m * kTM + (int)rank * 128;
-      const int n = kIsGate ? u.n * 128 : u.n * kTN + (int)rank * 128;
+      const int w = sh.w;
+      const int n = kIsGate ? u.n * w : u.n * 2 * w + (int)rank * w;
       const int kb0 = sh.kb0;
       const bool a_mn = sh.a_mn, b_mn = sh.b_mn;
       const CUtensorMap* const maps_a = p.a;
@@ -399,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* mb = maps_b + seg;
         const uint32_t da = ring + s * kStageBytes, db = da + kTileBytes;
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * (kTileBytes + w * kBK * 2));
           if (a_mn) {
             tma_load_pair(da, ma, m, k, full(s));
             tma_load_pair(da + kTileBytes / 2, ma, m + 64, k, full(s));
@@ -408,12 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (b_mn) {
             tma_load_pair(db, mb, n, k, full(s));
-            tma_load_pair(db + kTileBytes / 2, mb, n + 64, k, full(s));
+            if (w > 64) tma_load_pair(db + kTileBytes / 2, mb, n + 64, k, full(s));
           } else {
             tma_load_pair(db, mb, k, n, full(s));
           }
         }
-        if (kb == u.k0) next = unit(ui + clusters);  // decoded under the copies
+        if (kb == u.k0) {  // decoded under the copies
+          ui = index(i);
+          next = unit(ui);
+        }
         if (++s == kStages) {
           s = 0;
           parity ^= 1;
@@ -431,15 +463,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0, acc = 0;
     uint32_t parity = 0, acc_parity = 0;
     bool ok = true;
-    Unit next = unit(cluster);
-    for (int ui = cluster; ok && ui < units; ui += clusters) {
+    int ui = index(0);
+    Unit next = unit(ui);
+    for (int i = 1; ok && ui < units; ++i) {
       const Unit u = next;
       const bool a_mn = shapes[u.i].a_mn, b_mn = shapes[u.i].b_mn;
-      const uint32_t idesc = instr_desc(kTM, kTN, a_mn, b_mn);
+      const uint32_t idesc = instr_desc(kTM, 2 * shapes[u.i].w, a_mn, b_mn);
       const uint32_t step_a = k_step_bytes(a_mn) >> 4, step_b = k_step_bytes(b_mn) >> 4;
       if (!(ok = __all_sync(~0u, wait(acc_empty(acc), acc_parity ^ 1)))) break;
       tc_fence_after();
-      const uint32_t d = tmem + acc * kTN;
+      const uint32_t d = tmem + acc * kAccCols;
       for (int kb = u.k0; kb < u.k1; ++kb) {
         if (!(ok = __all_sync(~0u, wait(full(s), parity)))) break;
         tc_fence_after();
@@ -452,7 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit<2>(empty(s));
           if (kb + 1 == u.k1) tc_commit<2>(acc_full(acc));
         }
-        if (kb == u.k0) next = unit(ui + clusters);  // decoded under the products
+        if (kb == u.k0) {  // decoded under the products
+          ui = index(i);
+          next = unit(ui);
+        }
         if (++s == kStages) {
           s = 0;
           parity ^= 1;
@@ -473,56 +509,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0, turn = 0;
     uint32_t acc_parity = 0;
     bool ok = true;
-    // kGateBwd: this warp's chunks of 32 columns of a unit: chunk c exists if it
-    // starts before the last column.  The saved values are read one chunk
-    // ahead, into the next unit that has one.
-    auto col_of = [&](const Unit& u, int c) { return u.n * kTN + half * 128 + c * 32; };
+    // kGateBwd: this warp's chunks are every other 32 columns of a unit; its
+    // chunk c exists if it starts before the last column.  The saved values are
+    // read one chunk ahead, into the next unit that has one.
+    auto col_of = [&](const Unit& u, int c) { return u.n * 2 * shapes[u.i].w + (2 * c + half) * 32; };
     auto saved_of = [&](const Unit& u) -> const uint4* {  // of the unit's first chunk
       const Dims& s = shapes[u.i];
       const int row0 = u.m * kTM + row_in;
       return row0 < s.M ? saved_at(a.saved, row0, col_of(u, 0), s.N, lane) : nullptr;
     };
-    // First unit from `ui` on with a chunk for this warp (>= units: none).
-    auto seek = [&](int ui, Unit& u) {
-      for (; ui < units; ui += clusters) {
-        u = unit(ui);
-        if (col_of(u, 0) < shapes[u.i].N) break;
+    // The first unit from the pair's i-th on with a chunk for this warp.
+    auto seek = [&](int i) -> const uint4* {
+      for (int ui; (ui = index(i)) < units; ++i) {
+        const Unit u = unit(ui);
+        if (col_of(u, 0) < shapes[u.i].N) return saved_of(u);
       }
-      return ui;
+      return nullptr;
     };
     SavedRow in = {};
     const uint4* at_saved = nullptr;  // of the next unit's first chunk
     if (KIND == kGateBwd) {
-      Unit u;
-      if (seek(cluster, u) < units) at_saved = saved_of(u);
+      at_saved = seek(0);
 #pragma unroll
       for (int i = 0; i < kSavedVecs; ++i) in.load(at_saved, i);
     }
-    Unit next = unit(cluster);
-    for (int ui = cluster; ok && ui < units; ui += clusters) {
+    int ui = index(0);
+    Unit next = unit(ui);
+    for (int i = 1; ok && ui < units; ++i) {
       const Unit u = next;
-      next = unit(ui + clusters);
+      ui = index(i);
+      next = unit(ui);
       const Dims& sh = shapes[u.i];
       const uint4* here = at_saved;
-      if (KIND == kGateBwd && col_of(u, 0) < sh.N) {
-        Unit v;
-        at_saved = seek(ui + clusters, v) < units ? saved_of(v) : nullptr;
-      }
+      if (KIND == kGateBwd && col_of(u, 0) < sh.N) at_saved = seek(i);
       if (!(ok = __all_sync(~0u, wait(acc_full(acc), acc_parity)))) break;
       tc_fence_after();
       const int row0 = u.m * kTM + row_in;
-      const uint32_t at = tmem + acc * kTN + ((uint32_t)lanes << 16);
+      const uint32_t at = tmem + acc * kAccCols + ((uint32_t)lanes << 16);
       if constexpr (KIND == kPlain) {
         epilogue_plain(a.p[u.i], sh, u, at, row0, half, buf, lane, turn);
       } else if constexpr (kIsGate) {
         epilogue_gate<ACT, KIND == kGateSave>(a, sh, u, at, row0, half, buf, lane, turn);
       } else {
-        const int M = sh.M, N = sh.N;
+        const int M = sh.M, N = sh.N, chunks = sh.w / 32;
 #pragma unroll 1
-        for (int c = 0; c < 4 && col_of(u, c) < N; ++c) {
-          const bool last = c == 3 || col_of(u, c + 1) >= N;
-          if (here != nullptr) here += kSavedBlock / 16;
-          chunk_gate_bwd<ACT>(a, at + half * 128 + c * 32, col_of(u, c), row0, M, buf, lane, in,
+        for (int c = 0; c < chunks && col_of(u, c) < N; ++c) {
+          const bool last = c + 1 == chunks || col_of(u, c + 1) >= N;
+          if (here != nullptr) here += 2 * kSavedBlock / 16;
+          chunk_gate_bwd<ACT>(a, at + (2 * c + half) * 32, col_of(u, c), row0, M, buf, lane, in,
                               last ? at_saved : here);
         }
       }
@@ -631,8 +665,8 @@ struct Operand {
   int64_t rows, cols;
   bool mn;
 };
-cudaError_t operand_map(CUtensorMap* m, const Operand& o) {
-  return make_map(m, o.p, o.rows, o.cols, 64, o.mn ? kBK : 128);
+cudaError_t operand_map(CUtensorMap* m, const Operand& o, int rows) {
+  return make_map(m, o.p, o.rows, o.cols, 64, o.mn ? kBK : rows);
 }
 // Blocks of 32 x 32 of an epilogue.
 cudaError_t block_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
@@ -692,51 +726,59 @@ cudaError_t pairs_of_device(int* pairs) {
   return cudaSuccess;
 }
 
-// k splits of a product [M, N] of `tiles` tiles and kb k blocks on `pairs` CTA
-// pairs, with `other` k blocks of work per pair beside it: the fewest rounds of
-// k blocks (0.28 us each), a unit costing about 6 of them at its start and end.
-// A split costs the joining launch, about 14, and its fp32 partials written and
-// read again, mostly in L2 (256 tokens, D = 5120, F = 13824: the 7 splits that
-// fill the pairs best took 44.7 + 9.6 us, 3 splits 38 + 6).
-int choose_splits(int64_t M, int N, int kb, int pairs, int64_t other) {
-  const int64_t tiles = (int64_t)div_up(M, kTM) * div_up(N, kTN);
-  int best = 1;
+// How a product [M, N] over kb k blocks is cut into units for the CTA pairs: the
+// width w of a tile and the splits of k.
+struct Tiling {
+  int w, splits;
+  size_t bytes;  // of the fp32 partials
+};
+// Clocks of a unit: a k block takes its products' time (4 w) or that of the
+// copies that feed them (about 62 bytes a clock and SM, from L2), and a unit's
+// start and end cost about 3000.
+double unit_clocks(int kb, int w) {
+  const double copies = (128 + w) * 128 / 62.0;
+  return kb * (copies > 4.0 * w ? copies : 4.0 * w) + 3000;
+}
+int cover(bool gate, int w) { return gate ? w : 2 * w; }
+int tiles_of(int64_t M, int N, bool gate, int w) { return div_up(M, kTM) * div_up(N, cover(gate, w)); }
+
+// The cheapest tiling.  256-column tiles (w = 128) feed the products best; w =
+// 96 and 64 (an MN-major B: 64 only) fill the pairs better where there are few
+// tiles: with 256 tokens, D = 5120, F = 13824 the 108 tiles of the projections
+// take two rounds of 76 pairs, the 144 of w = 96 two shorter ones.  A split of k
+// costs the joining launch and its partials, written and read again.  `other`:
+// clocks of shorter units beside it in the launch, of `other_unit` each.
+Tiling choose_tiling(int64_t M, int N, int kb, bool gate, bool b_mn, bool may_split, int pairs,
+                     double other = 0, double other_unit = 0) {
+  Tiling best = {};
   double least = 0;
-  for (int s = 1; s <= 32 && (s == 1 || kb / s >= 8); ++s) {
-    const double rounds = (double)div_up(tiles * s, pairs);
-    double cost = rounds * (div_up(kb, s) + 6);
-    // Beside other work only the longest unit and the total matter.
-    if (other > 0) {
-      const double mean = (double)tiles * (kb + 6.0 * s) / pairs + (double)other;
-      cost = mean > 2.0 * (div_up(kb, s) + 6) ? mean : 2.0 * (div_up(kb, s) + 6);
-    }
-    if (s > 1) cost += 14 + 8.0 * s * (double)M * N / 1.4e6;
-    if (s == 1 || cost < least) {
-      least = cost;
-      best = s;
+  for (int w = 128; w >= 64; w -= b_mn ? 64 : 32) {
+    const int64_t tiles = tiles_of(M, N, gate, w);
+    for (int s = 1; s == 1 || (may_split && s <= 32 && kb / s >= 8); ++s) {
+      const double unit = unit_clocks(div_up(kb, s), w);
+      const double rounds = (double)div_up(tiles * s, pairs);
+      double cost = rounds * unit;
+      if (other > 0) {
+        const double even = (tiles * s * unit + other) / pairs + other_unit / 2;
+        if (even > cost) cost = even;
+      }
+      if (s > 1) cost += 7000 + 3e-3 * s * (double)M * N;
+      if (best.w == 0 || cost < least) {
+        least = cost;
+        best = {w, s, s > 1 ? (size_t)s * M * N * 4 : 0};
+      }
     }
   }
   return best;
 }
 
-struct Split {
-  int splits;
-  size_t bytes;  // of the fp32 partials
-};
-Split split_of(int64_t M, int N, int kb, int pairs, int64_t other) {
-  Split s;
-  s.splits = choose_splits(M, N, kb, pairs, other);
-  s.bytes = s.splits > 1 ? (size_t)s.splits * M * N * 4 : 0;
-  return s;
-}
-
 cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2], int segs, int64_t M,
-                        int N, int tn, int64_t k0, int64_t k1, void* out) {
+                        int N, bool gate, const Tiling& t, int64_t k0, int64_t k1, void* out) {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
     const bool have_a = i < segs, have_b = b[i].p != nullptr;
-    e = operand_map(&p->a[i], have_a ? a[i] : a[0]);
-    if (e == cudaSuccess) e = operand_map(&p->b[i], have_b ? b[i] : b[0]);
+    e = operand_map(&p->a[i], have_a ? a[i] : a[0], 128);
+    if (e == cudaSuccess) e = operand_map(&p->b[i], have_b ? b[i] : b[0], t.w);
   }
   if (e == cudaSuccess && out) e = block_map(&p->out, out, M, N);
   p->partial = nullptr;
@@ -746,15 +788,18 @@ cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2]
   s.kb0 = div_up(k0, kBK);
   s.kb = s.kb0 + (segs > 1 ? div_up(k1, kBK) : 0);
   s.tiles_m = div_up(M, kTM);
-  s.tiles_n = div_up(N, tn);
-  s.splits = 1;
+  s.w = t.w;
+  s.tiles_n = div_up(N, cover(gate, t.w));
+  s.splits = t.splits;
   s.first = 0;
   s.a_mn = a[0].mn;
   s.b_mn = b[0].mn;
   return e;
 }
 
-cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, cudaStream_t st) {
+// `worth`: with several problems, how many units of the others one of the first
+// takes the time of.
+cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, int worth, cudaStream_t st) {
   int at = 0;
   for (int i = 0; i < a.problems; ++i) {
     Dims& s = a.p[i].s;
@@ -762,6 +807,8 @@ cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, cudaStream_t 
     at += s.tiles_m * s.tiles_n * s.splits;
   }
   a.units = at;
+  a.lead = a.problems > 1 ? a.p[1].s.first : 0;
+  a.worth = worth;
   const int grid = 2 * (at < pairs ? at : pairs);
   void* params[1] = {&a};
   return traced_launch(ADALN_KERNEL_FFN, st, [&] {
@@ -795,7 +842,7 @@ int check(int64_t T, int32_t D, int32_t F, adaln_dtype_t dt, int act) {
 }
 
 struct FwdPlan {
-  Split y;
+  Tiling gate, y;
   size_t bytes;
 };
 FwdPlan fwd_plan(int64_t T, int32_t D, int32_t F, int pairs) {
@@ -804,21 +851,26 @@ FwdPlan fwd_plan(int64_t T, int32_t D, int32_t F, int pairs) {
     p.bytes = skinny_workspace(T, F);
     return p;
   }
-  p.y = split_of(T, D, div_up(F, kBK), pairs, 0);
+  p.gate = choose_tiling(T, F, div_up(D, kBK), true, false, false, pairs);
+  p.y = choose_tiling(T, D, div_up(F, kBK), false, false, true, pairs);
   p.bytes = round256((size_t)T * F * 2) + round256(p.y.bytes);
   return p;
 }
 
 struct BwdPlan {
-  Split dx;
+  Tiling gate, dx, dw;
+  int worth;
   size_t bytes;
 };
 BwdPlan bwd_plan(int64_t T, int32_t D, int32_t F, int pairs) {
-  BwdPlan p;
-  const int64_t weight_tiles = 2 * (int64_t)div_up(F, kTM) * div_up(D, kTN) +
-                               (int64_t)div_up(D, kTM) * div_up(F, kTN);
-  const int64_t other = weight_tiles * (div_up(T, kBK) + 6) / pairs;
-  p.dx = split_of(T, D, 2 * div_up(F, kBK), pairs, other > 0 ? other : 1);
+  BwdPlan p = {};
+  p.gate = choose_tiling(T, F, div_up(D, kBK), false, true, false, pairs);
+  p.dw = {128, 1, 0};
+  const double unit = unit_clocks(div_up(T, kBK), 128);
+  const int64_t tiles = 2 * (int64_t)tiles_of(F, D, false, 128) + tiles_of(D, F, false, 128);
+  const int kb = 2 * div_up(F, kBK);
+  p.dx = choose_tiling(T, D, kb, false, true, true, pairs, tiles * unit, unit);
+  p.worth = (int)(unit_clocks(div_up(kb, p.dx.splits), p.dx.w) / unit);
   p.bytes = 3 * round256((size_t)T * F * 2) + round256(p.dx.bytes);
   return p;
 }
@@ -881,14 +933,14 @@ int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd,
   const Operand none = {};
   a.problems = 1;
   e = set_problem(&a.p[0], {{x, T, D, false}, none}, {{wg, F, D, false}, {wu, F, D, false}}, 1, T, F,
-                  128, D, 0, nullptr);
-  if (e == cudaSuccess) e = launch_gemm(a, saved ? kGateSave : kGate, act, pairs, st);
+                  true, plan.gate, D, 0, nullptr);
+  if (e == cudaSuccess) e = launch_gemm(a, saved ? kGateSave : kGate, act, pairs, 0, st);
   if (e != cudaSuccess) return launch_failed(e);
 
-  e = set_problem(&a.p[0], {{ws, T, F, false}, none}, {{wd, D, F, false}, none}, 1, T, D, kTN, F, 0, y);
-  a.p[0].s.splits = plan.y.splits;
+  e = set_problem(&a.p[0], {{ws, T, F, false}, none}, {{wd, D, F, false}, none}, 1, T, D, false, plan.y,
+                  F, 0, y);
   a.p[0].partial = reinterpret_cast<float*>(ws + round256((size_t)T * F * 2));
-  if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, st);
+  if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, 0, st);
   if (e == cudaSuccess && plan.y.splits > 1) e = launch_join(a.p[0], y, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
@@ -932,23 +984,26 @@ int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
 
   const Operand none = {};
   a.problems = 1;
-  e = set_problem(&a.p[0], {{dy, T, D, false}, none}, {{wd, D, F, true}, none}, 1, T, F, kTN, D, 0,
-                  nullptr);
-  if (e == cudaSuccess) e = launch_gemm(a, kGateBwd, act, pairs, st);
+  e = set_problem(&a.p[0], {{dy, T, D, false}, none}, {{wd, D, F, true}, none}, 1, T, F, false,
+                  plan.gate, D, 0, nullptr);
+  if (e == cudaSuccess) e = launch_gemm(a, kGateBwd, act, pairs, 0, st);
   if (e != cudaSuccess) return launch_failed(e);
 
-  // dx first: its units are the longest.
+  // dx first: its units are the longer ones.
   const Operand dgk = {dg, T, F, false}, duk = {du, T, F, false};
   const Operand dgm = {dg, T, F, true}, dum = {du, T, F, true};
   const Operand xm = {x, T, D, true}, dym = {dy, T, D, true}, hm = {h, T, F, true};
   a.problems = 4;
-  e = set_problem(&a.p[0], {dgk, duk}, {{wg, F, D, true}, {wu, F, D, true}}, 2, T, D, kTN, F, F, dx);
-  a.p[0].s.splits = plan.dx.splits;
+  e = set_problem(&a.p[0], {dgk, duk}, {{wg, F, D, true}, {wu, F, D, true}}, 2, T, D, false,
+                  plan.dx, F, F, dx);
   a.p[0].partial = reinterpret_cast<float*>(ws + 3 * tf);
-  if (e == cudaSuccess) e = set_problem(&a.p[1], {dgm, none}, {xm, none}, 1, F, D, kTN, T, 0, dwg);
-  if (e == cudaSuccess) e = set_problem(&a.p[2], {dum, none}, {xm, none}, 1, F, D, kTN, T, 0, dwu);
-  if (e == cudaSuccess) e = set_problem(&a.p[3], {dym, none}, {hm, none}, 1, D, F, kTN, T, 0, dwd);
-  if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, st);
+  if (e == cudaSuccess)
+    e = set_problem(&a.p[1], {dgm, none}, {xm, none}, 1, F, D, false, plan.dw, T, 0, dwg);
+  if (e == cudaSuccess)
+    e = set_problem(&a.p[2], {dum, none}, {xm, none}, 1, F, D, false, plan.dw, T, 0, dwu);
+  if (e == cudaSuccess)
+    e = set_problem(&a.p[3], {dym, none}, {hm, none}, 1, D, F, false, plan.dw, T, 0, dwd);
+  if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, plan.worth, st);
   if (e == cudaSuccess && plan.dx.splits > 1) e = launch_join(a.p[0], dx, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
