@@ -110,13 +110,17 @@ def _strip_comments(text):
     return " ".join("".join(out).split())
 
 
+# Sources that no AdaLN kernel is made of.
+OTHER_OPERATORS = {"ffn.cu", "ffn.cuh", "ffn_skinny.cu", "rope.cu", "tc.cuh"}
+
+
 def source_hash():
-    """sha256 over the CUDA sources and headers with comments removed
+    """sha256 over the AdaLN's CUDA sources and headers with comments removed
     (identifies a kernel build's code)."""
     import hashlib
     h = hashlib.sha256()
     for f in sorted(_deps()):
-        if f.endswith(".py"):
+        if f.endswith(".py") or os.path.basename(f) in OTHER_OPERATORS:
             continue
         with open(f, encoding="utf-8") as fh:
             h.update(os.path.basename(f).encode())

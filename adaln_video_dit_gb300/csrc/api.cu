@@ -270,9 +270,8 @@ cudaError_t sm_count(int dev, int* sms) {
   return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
-cudaError_t traced_launch(int kernel, cudaStream_t st,
-                          const std::function<cudaError_t()>& launch) {
-  return traced(kernel, st, launch);
+cudaError_t traced_call(int kernel, cudaStream_t st, cudaError_t (*launch)(void*), void* with) {
+  return traced(kernel, st, [&] { return launch(with); });
 }
 
 int launch_failed(cudaError_t e) { return cuda_fail(e); }

@@ -5,8 +5,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <functional>
-
 #include "../../include/adaln.h"
 
 #ifdef __CUDACC__
@@ -238,7 +236,12 @@ cudaError_t launch_slot_release(int pool, int slot, cudaStream_t st, bool launch
 // trace, and the status code of a failed CUDA call (its error is cleared).
 cudaError_t status_word(unsigned** out);
 cudaError_t sm_count(int dev, int* sms);
-cudaError_t traced_launch(int kernel, cudaStream_t st, const std::function<cudaError_t()>& launch);
+cudaError_t traced_call(int kernel, cudaStream_t st, cudaError_t (*launch)(void*), void* with);
+template <class F>
+inline cudaError_t traced_launch(int kernel, cudaStream_t st, F launch) {
+  return traced_call(
+      kernel, st, [](void* f) { return (*static_cast<F*>(f))(); }, &launch);
+}
 int launch_failed(cudaError_t e);
 
 // Bounded-wait self-test (selftest.cu).

@@ -626,10 +626,13 @@ cudaError_t launch(void* kernel, dim3 grid, int threads, size_t smem, void** par
   return cudaLaunchKernelExC(&cfg, kernel, params);
 }
 
-// Head groups in flight: what fits 128 registers a thread (the norm's backward
-// holds twice the tensors and its weight sums; with two groups of bf16 heads
-// it spilled, and 8192 tokens x 24 heads x 128 took 41.0 instead of 30.6 us).
-constexpr int groups_in_flight(int mode, int es) { return mode != kNormBwd ? 4 : es == 2 ? 1 : 2; }
+// Head groups in flight: what fits 128 registers a thread.  Forward and plain
+// rotation, T = 32760 x 80 heads x 128: three groups 205.9 us, four (spilling
+// with the norm) 226.5, two 206.9 (T = 36864 x 48 heads, rotation alone: 134.9,
+// 135.2 and 144.4).  The norm's backward holds twice the tensors and its weight
+// sums: with two groups of bf16 heads it spilled, and 8192 tokens x 24 heads x
+// 128 took 41.0 instead of 30.6 us.
+constexpr int groups_in_flight(int mode, int es) { return mode != kNormBwd ? 3 : es == 2 ? 1 : 2; }
 
 template <class E, int P, bool HALF>
 void* vec_kernel(int mode) {
