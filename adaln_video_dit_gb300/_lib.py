@@ -378,7 +378,8 @@ def _weight(w, name, like):
     if w is None:
         return None
     _dev(w, name, like.dtype, like.shape[2:])
-    _alike(w, name, like)
+    if w.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}, got {w.device}")
     return w.data_ptr()
 
 
@@ -475,6 +476,16 @@ def adaln_ffn_workspace_size(T, D, F, dtype=torch.bfloat16):
     return f.value, b.value
 
 
+def _ffn_workspace(t, T, D, F, dt, backward, device):
+    """A call's workspace: the given one, checked, or a new one of the size needed."""
+    if t is not None:
+        return _dev(t, "workspace", torch.uint8)
+    n = ctypes.c_size_t(0)
+    f, b = (None, ctypes.byref(n)) if backward else (ctypes.byref(n), None)
+    _check(raw.adaln_ffn_workspace_size(T, D, F, dt, f, b), "adaln_ffn_workspace_size")
+    return torch.empty(max(16, n.value), device=device, dtype=torch.uint8)
+
+
 def _act(act):
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
@@ -492,13 +503,6 @@ def _ffn_args(x, wg, wu, wd):
     return T, D, F
 
 
-def _bytes(t, n, name, device):
-    """A uint8 CUDA buffer of at least n bytes (allocated when not given)."""
-    if t is None:
-        return torch.empty(max(16, n), device=device, dtype=torch.uint8)
-    return _dev(t, name, torch.uint8)
-
-
 def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, workspace=None,
                   stream=None):
     """y = (act(x wg') * (x wu')) wd' for bf16 x [T, D], wg, wu [F, D], wd [D, F];
@@ -510,13 +514,11 @@ def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, wor
     y = torch.empty_like(x) if y is None else _dev(y, "y", x.dtype, (T, D))
     if save or saved is not None:
         need = adaln_ffn_saved_size(T, D, F, dt)
-        saved = _bytes(saved, need, "saved", x.device)
-        if saved.numel() < need:
+        if saved is None:
+            saved = torch.empty(max(16, need), device=x.device, dtype=torch.uint8)
+        elif _dev(saved, "saved", torch.uint8).numel() < need:
             raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
-    if workspace is None:
-        workspace = _bytes(None, adaln_ffn_workspace_size(T, D, F, dt)[0], "workspace", x.device)
-    else:
-        _dev(workspace, "workspace", torch.uint8)
+    workspace = _ffn_workspace(workspace, T, D, F, dt, False, x.device)
     rc = raw.adaln_ffn_fwd(_ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), T, D, F, dt, code, _ptr(y),
                            _ptr(saved), _ptr(workspace), workspace.numel(),
                            _stream_ptr(stream, x.get_device()))
@@ -532,17 +534,13 @@ def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=N
     code, dt = _act(act), dtype_code(x.dtype)
     _dev(dy, "dy", x.dtype, (T, D))
     need = adaln_ffn_saved_size(T, D, F, dt)
-    _dev(saved, "saved", torch.uint8)
-    if saved.numel() < need:
+    if _dev(saved, "saved", torch.uint8).numel() < need:
         raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
     dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", x.dtype, (T, D))
     dwg = torch.empty_like(wg) if dwg is None else _dev(dwg, "dwg", x.dtype, (F, D))
     dwu = torch.empty_like(wu) if dwu is None else _dev(dwu, "dwu", x.dtype, (F, D))
     dwd = torch.empty_like(wd) if dwd is None else _dev(dwd, "dwd", x.dtype, (D, F))
-    if workspace is None:
-        workspace = _bytes(None, adaln_ffn_workspace_size(T, D, F, dt)[1], "workspace", x.device)
-    else:
-        _dev(workspace, "workspace", torch.uint8)
+    workspace = _ffn_workspace(workspace, T, D, F, dt, True, x.device)
     rc = raw.adaln_ffn_bwd(_ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), _ptr(saved), T, D, F,
                            dt, code, _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), _ptr(workspace),
                            workspace.numel(), _stream_ptr(stream, x.get_device()))

@@ -168,10 +168,15 @@ __device__ __forceinline__ void save_row(uint4* to, const uint32_t (&v)[32]) {
     st_global_cs_v4(to + 32 * (4 + i), make_uint4(b[0], b[1], b[2], b[3]));
   }
 }
-// And back: value e (0..7) of upper halves w, their next bytes in b0 (0..3), b1.
-__device__ __forceinline__ float saved_value(const uint4& w, uint32_t b0, uint32_t b1, int e) {
-  const uint32_t x = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w, b = e < 4 ? b0 : b1;
-  return __uint_as_float((e % 2 ? x & 0xffff0000u : x << 16) | (b >> (8 * (e % 4)) & 0xff) << 8);
+// And back: values 2 i and 2 i + 1 (i = 0..3) from their word of upper halves and
+// from the four next bytes that they are the lower (i even) or upper two of.
+// (The lowest byte, which was not kept, repeats the one before it: one
+// instruction a value.)
+__device__ __forceinline__ float2 saved_pair(uint32_t w, uint32_t b, int i) {
+  return i % 2 ? make_float2(__uint_as_float(__byte_perm(w, b, 0x1066)),
+                             __uint_as_float(__byte_perm(w, b, 0x3277)))
+               : make_float2(__uint_as_float(__byte_perm(w, b, 0x1044)),
+                             __uint_as_float(__byte_perm(w, b, 0x3255)));
 }
 
 // ----- epilogues: one warp's 32 rows x every other 32 of the tile's columns -----------------
@@ -236,15 +241,12 @@ __device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Dims& s, 
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float h[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float x = __uint_as_float(g[2 * i + j]);
-        float p, d;
-        gate<ACT>(x, p, d);
-        h[j] = x * p * __uint_as_float(v[2 * i + j]);
-      }
-      w[i] = pack_bf16(h[0], h[1]);
+      const float2 x = make_float2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+      float2 p, d;
+      gate<ACT>(x, p, d);
+      const float2 h = mul2(mul2(x, p), make_float2(__uint_as_float(v[2 * i]),
+                                                    __uint_as_float(v[2 * i + 1])));
+      w[i] = pack_bf16(h.x, h.y);
     }
     const uint32_t block = buf + turn * kBlock;
     turn ^= 1;
@@ -291,21 +293,18 @@ __device__ __forceinline__ void chunk_gate_bwd(const GemmArgs& a, uint32_t acc, 
     const uint32_t u0 = j % 2 ? ub.z : ub.x, u1 = j % 2 ? ub.w : ub.y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float dg[2], du[2], h[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = saved_value(in.v[j], g0, g1, 2 * i + e);
-        const float w = saved_value(in.v[6 + j], u0, u1, 2 * i + e);
-        const float dh = __uint_as_float(r[8 * j + 2 * i + e]);
-        float s, d;
-        gate<ACT>(x, s, d);
-        dg[e] = dh * w * d;
-        du[e] = dh * (x * s);
-        h[e] = x * s * w;
-      }
-      wg[4 * j + i] = pack_bf16(dg[0], dg[1]);
-      wu[4 * j + i] = pack_bf16(du[0], du[1]);
-      wh[4 * j + i] = pack_bf16(h[0], h[1]);
+      const uint4 &gw = in.v[j], &uw = in.v[6 + j];
+      const float2 x = saved_pair(i == 0 ? gw.x : i == 1 ? gw.y : i == 2 ? gw.z : gw.w, i < 2 ? g0 : g1, i);
+      const float2 w = saved_pair(i == 0 ? uw.x : i == 1 ? uw.y : i == 2 ? uw.z : uw.w, i < 2 ? u0 : u1, i);
+      const float2 dh = make_float2(__uint_as_float(r[8 * j + 2 * i]),
+                                    __uint_as_float(r[8 * j + 2 * i + 1]));
+      float2 p, d;
+      gate<ACT>(x, p, d);
+      const float2 act = mul2(x, p);
+      const float2 dg = mul2(mul2(dh, w), d), du = mul2(dh, act), h = mul2(act, w);
+      wg[4 * j + i] = pack_bf16(dg.x, dg.y);
+      wu[4 * j + i] = pack_bf16(du.x, du.y);
+      wh[4 * j + i] = pack_bf16(h.x, h.y);
     }
     in.load(next, j);
     in.load(next, 6 + j);
@@ -754,7 +753,8 @@ Tiling choose_tiling(int64_t M, int N, int kb, bool gate, bool b_mn, bool may_sp
   double least = 0;
   for (int w = 128; w >= 64; w -= b_mn ? 64 : 32) {
     const int64_t tiles = tiles_of(M, N, gate, w);
-    for (int s = 1; s == 1 || (may_split && s <= 32 && kb / s >= 8); ++s) {
+    // (Twice as many units as pairs are as many as a split can be good for.)
+    for (int s = 1; s == 1 || (may_split && tiles * (s - 1) < 2 * pairs && kb / s >= 8); ++s) {
       const double unit = unit_clocks(div_up(kb, s), w);
       const double rounds = (double)div_up(tiles * s, pairs);
       double cost = rounds * unit;

@@ -12,27 +12,49 @@ namespace adaln {
 // four of upper halves, two of the next bytes; then u), each one coalesced
 // access of a warp.
 constexpr int kSavedVecs = 12, kSavedBlock = kSavedVecs * 512;
+
 // ----- activations --------------------------------------------------------------
-// p such that act(g) = g p, and act'(g).  The sigmoid form of the tanh
-// approximation (0.5 (1 + tanh z) = 1 / (1 + exp(-2 z))) keeps its relative
-// accuracy for negative g.  The fast exponential and division are good to a
-// few fp32 units, far below the bf16 rounding that follows.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// p such that act(g) = g p, and d = act'(g), for two values at a time.  The
+// sigmoid form of the tanh approximation (0.5 (1 + tanh z) = 1 / (1 + exp(-2 z)))
+// keeps its relative accuracy for negative g.  The exponential and reciprocal
+// are the hardware's, good to a few fp32 units and flushing denormals, far below
+// the bf16 rounding that follows; the epilogues that use them are bound by
+// instructions, not by their own data.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// 1 / (1 + exp(-z)), z given as z log2(e).
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  return make_float2(rcp_approx(1.0f + ex2_approx(-z.x)), rcp_approx(1.0f + ex2_approx(-z.y)));
+}
 
 template <int ACT>
-__device__ __forceinline__ void gate(float g, float& p, float& d) {
+__device__ __forceinline__ void gate(float2 g, float2& p, float2& d) {
+  const float2 one = splat2(1.0f);
   if (ACT == ADALN_ACT_SILU) {
-    p = sigmoid(g);
-    d = p * (1.0f + g * (1.0f - p));
+    p = sigmoid2(mul2(g, splat2(kLog2e)));
+    d = mul2(p, fma2(g, fma2(p, splat2(-1.0f), one), one));
   } else if (ACT == ADALN_ACT_GELU_TANH) {
     const float k = 0.7978845608028654f, c = 0.044715f;
-    const float g2 = g * g;
-    p = sigmoid(2.0f * k * g * (1.0f + c * g2));
-    const float q = p * (1.0f - p);
-    d = q > 0.0f ? p + 2.0f * k * g * q * (1.0f + 3.0f * c * g2) : p;
+    const float2 g2 = mul2(g, g);
+    p = sigmoid2(mul2(g, fma2(g2, splat2(2.0f * k * c * kLog2e), splat2(2.0f * k * kLog2e))));
+    const float2 q = mul2(p, fma2(p, splat2(-1.0f), one));
+    const float2 t = mul2(mul2(g, q), fma2(g2, splat2(6.0f * k * c), splat2(2.0f * k)));
+    // (Where q has vanished g^2 may have overflowed: 0 * inf.)
+    d = make_float2(q.x > 0.0f ? p.x + t.x : p.x, q.y > 0.0f ? p.y + t.y : p.y);
   } else {
-    p = 0.5f * erfcf(-0.7071067811865476f * g);
-    d = p + g * 0.3989422804014327f * __expf(-0.5f * g * g);
+    p = make_float2(0.5f * erfcf(-0.7071067811865476f * g.x), 0.5f * erfcf(-0.7071067811865476f * g.y));
+    const float2 e = mul2(mul2(g, g), splat2(-0.5f * kLog2e));
+    const float2 n = mul2(g, splat2(0.3989422804014327f));
+    d = make_float2(fmaf(n.x, ex2_approx(e.x), p.x), fmaf(n.y, ex2_approx(e.y), p.y));
   }
 }
 

@@ -220,9 +220,9 @@ __global__ void __launch_bounds__(kThreads) ffn_skinny_kernel(const __grid_const
     if (f >= a.rows) continue;
     const int64_t o = (int64_t)t * a.rows + f;
     if (GATE) {
-      float p, d;
-      gate<ACT>(g, p, d);
-      const float h = g * p * u;
+      float2 p, d;
+      gate<ACT>(splat2(g), p, d);
+      const float h = g * p.x * u;
       const __nv_bfloat16 hi = __float2bfloat16_rn(h);
       a.out[0][o] = hi;
       // (An infinite h has no rest: inf - inf would make y NaN.)

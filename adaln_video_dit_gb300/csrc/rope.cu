@@ -234,28 +234,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   grid_wait();
   grid_launch_dependents();
 
-  if (kNorm) {
-    for (int i = threadIdx.x; i < entries; i += kThreads)
-      weights[i] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    if (sd.w != nullptr) {
-      __syncthreads();
-      for (int d = threadIdx.x; d < a.dh; d += kThreads) {
-        int at;
-        if (!HALF)
-          at = entry_of_pair(d >> 1) + 2 * (d & 1);
-        else if (d < 2 * a.P)
-          at = entry_of_pair(d < a.P ? d : d - a.P) + (d < a.P ? 0 : 2);
-        else
-          at = entry(nr + (d / N - 2 * nr) / 2, d % N) + (d / N - 2 * nr) % 2 * 2;
-        reinterpret_cast<float*>(weights)[at] =
-            E::SIZE == 2 ? __bfloat162float(static_cast<const __nv_bfloat16*>(sd.w)[d])
-                         : static_cast<const float*>(sd.w)[d];
-      }
-    }
-  }
-  for (int i = lane; i < 2 * entries; i += 32) angles[i] = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-  __syncthreads();
-
   // The angles of a token into table b, from its rows.
   auto fetch_angles = [&](const Rows& rows, int b) {
     float* const to = reinterpret_cast<float*>(angles + b * entries);
@@ -330,8 +308,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   Group cur;
   load(cur, t, h_begin);
   Rows rows;  // of the token after the one whose angles are on their way
+  if (t < a.T) rows.load(a, t, lane);
+  if (kNorm) {
+    for (int i = threadIdx.x; i < entries; i += kThreads)
+      weights[i] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (sd.w != nullptr) {
+      __syncthreads();
+      for (int d = threadIdx.x; d < a.dh; d += kThreads) {
+        int at;
+        if (!HALF)
+          at = entry_of_pair(d >> 1) + 2 * (d & 1);
+        else if (d < 2 * a.P)
+          at = entry_of_pair(d < a.P ? d : d - a.P) + (d < a.P ? 0 : 2);
+        else
+          at = entry(nr + (d / N - 2 * nr) / 2, d % N) + (d / N - 2 * nr) % 2 * 2;
+        reinterpret_cast<float*>(weights)[at] =
+            E::SIZE == 2 ? __bfloat162float(static_cast<const __nv_bfloat16*>(sd.w)[d])
+                         : static_cast<const float*>(sd.w)[d];
+      }
+    }
+  }
+  for (int i = lane; i < 2 * entries; i += 32) angles[i] = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+  __syncthreads();
   if (t < a.T) {
-    rows.load(a, t, lane);
     fetch_angles(rows, 0);
     if (t + step < a.T) rows.load(a, t + step, lane);
   }

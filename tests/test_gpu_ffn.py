@@ -199,6 +199,32 @@ def test_inputs_written_by_the_previous_kernel_are_seen(adaln):
         assert torch.equal(y, want), i
 
 
+def test_offsets_past_32_bits(adaln):
+    """T x F beyond 2^32 bytes in every hidden array (and 2^31 elements): rows at
+    both ends and around the 2^31st element of the hidden arrays are right, and
+    the weight gradients sum over all of them."""
+    T, D, F = 300000, 64, 8192
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.fail("needs 60 GB of device memory")
+    x, wg, wu, wd, dy = inputs(T, D, F, seed=12)
+    y, saved = adaln.adaln_ffn_fwd(x, wg, wu, wd, save=True)
+    dx, dwg, dwu, dwd = adaln.adaln_ffn_bwd(dy, x, wg, wu, wd, saved)
+    del saved
+    at = (1 << 31) // F
+    rows = torch.tensor([0, 1, 255, 256, at - 1, at, at + 1, T - 2, T - 1], device="cuda")
+    ref = reference(x[rows], wg, wu, wd, dy[rows], "silu")
+    for name, got in (("y", y), ("dx", dx)):
+        check(name, got[rows], *ref[name])
+    sums = {"dwg": 0, "dwu": 0, "dwd": 0}
+    for i in range(0, T, 30000):
+        part = reference(x[i:i + 30000], wg, wu, wd, dy[i:i + 30000], "silu")
+        sums = {k: v + part[k][0] for k, v in sums.items()}
+    for name, got in (("dwg", dwg), ("dwu", dwu), ("dwd", dwd)):
+        rel = float((got.double() - sums[name]).norm() / sums[name].norm())
+        assert rel <= 4e-3, f"{name}: normwise {rel:.3g}"
+    status_ok()
+
+
 @pytest.mark.parametrize("T", [1, 300])
 def test_in_a_cuda_graph(adaln, T):
     x, wg, wu, wd, dy = inputs(T, 256, 512, seed=6)
