@@ -145,7 +145,9 @@ def _stream_ptr(stream, device):
     building a torch.cuda.Stream for it costs 2 us."""
     if stream is not None:
         return stream.cuda_stream
-    index = device if isinstance(device, int) else device.index
+    if type(device) is int:
+        return torch._C._cuda_getCurrentRawStream(device)
+    index = device.index
     if index is None:
         index = torch.cuda.current_device()
     return torch._C._cuda_getCurrentRawStream(index)
@@ -308,78 +310,83 @@ def adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_row
     _check(rc, "adaln_fwd_bwd_host")
 
 
-def _heads(t, name, like=None):
-    """Check a [T, heads, dh] tensor (any strides, dh contiguous), with the
-    shape, dtype and device of `like`; its Heads."""
-    if not t.is_cuda:
+# The calls of the small operators are bound by this host code, so their checks
+# read each attribute of a tensor once (about 0.1 us each).
+
+
+def _heads(t, name, shape=None, dtype=None, dev=None):
+    """Check a [T, heads, dh] tensor (any strides, dh contiguous), and its shape,
+    dtype and device where given; its Heads."""
+    s = t.shape
+    if len(s) != 3:
+        raise ValueError(f"{name} must be [T, heads, dh], got {tuple(s)}")
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, heads, dh], got {tuple(t.shape)}")
-    if like is not None:
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-        _alike(t, name, like)
+    if shape is not None:
+        if s != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(s)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if d != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     ts, hs, ds = t.stride()
-    if ds != 1 and t.shape[2] != 1:
+    if ds != 1 and s[2] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     return Heads(t.data_ptr(), ts, hs)
 
 
-def _alike(t, name, like):
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-
-
-def _heads_out(t, name, like):
-    """An output like `like`: checked, or allocated contiguous; it and its Heads."""
-    if t is not None:
-        return t, _heads(t, name, like)
-    t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _, h, dh = like.shape
-    return t, Heads(t.data_ptr(), h * dh, dh)
-
-
-def _second(k, name, q, T, dh):
-    """Check the keys against the queries; their head count and Heads."""
-    if k is None:
-        return 0, None
+def _second(k, name, T, dh, dtype, dev):
+    """Check the keys against the queries; their shape and Heads."""
     kh = _heads(k, name)
-    if k.shape[0] != T or k.shape[2] != dh:
+    s = k.shape
+    if s[0] != T or s[2] != dh:
         raise ValueError("queries and keys must agree in tokens and head width")
-    _alike(k, name, q)
-    return k.shape[1], kh
+    if k.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {k.dtype}")
+    if k.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {k.device}")
+    return s, kh
+
+
+def _output(t, name, shape, dtype, dev, device):
+    """An output, checked or allocated contiguous, and its Heads."""
+    if t is not None:
+        return t, _heads(t, name, shape, dtype, dev)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 _Pairs = ctypes.c_int32 * MAX_ROPE_AXES
 
 
-def _rope(table, pos, axis_pairs, interleaved, T, like):
-    dev = like.get_device()
+def _rope(table, pos, axis_pairs, interleaved, T, dev):
     if table.get_device() != dev or pos.get_device() != dev:
-        raise ValueError(f"table and pos must be on {like.device}")
+        raise ValueError(f"table and pos must be on cuda:{dev}")
     if table.dtype != torch.float32 or not table.is_contiguous():
         raise ValueError("table must be contiguous float32")
     if pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ValueError("pos must be contiguous int32")
-    axes, P = len(axis_pairs), sum(axis_pairs)
+    axes, P, s = len(axis_pairs), sum(axis_pairs), table.shape
     if not 1 <= axes <= MAX_ROPE_AXES or min(axis_pairs) < 0:
         raise ValueError(f"axis_pairs must hold 1 to {MAX_ROPE_AXES} counts >= 0")
-    if table.dim() != 3 or table.shape[1:] != (P, 2):
-        raise ValueError(f"table must have shape [rows, {P}, 2], got {tuple(table.shape)}")
+    if len(s) != 3 or s[1] != P or s[2] != 2:
+        raise ValueError(f"table must have shape [rows, {P}, 2], got {tuple(s)}")
     if pos.shape != (T, axes):
         raise ValueError(f"pos must have shape {(T, axes)}, got {tuple(pos.shape)}")
-    return Rope(table.data_ptr(), pos.data_ptr(), table.shape[0], axes, _Pairs(*axis_pairs),
+    return Rope(table.data_ptr(), pos.data_ptr(), s[0], axes, _Pairs(*axis_pairs),
                 1 if interleaved else 0)
 
 
-def _weight(w, name, like):
+def _weight(w, name, dh, dtype, dev):
     if w is None:
         return None
-    _dev(w, name, like.dtype, like.shape[2:])
-    if w.get_device() != like.get_device():
-        raise ValueError(f"{name} must be on {like.device}, got {w.device}")
+    if w.get_device() != dev or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous on cuda:{dev}")
+    if w.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {w.dtype}")
+    if w.shape != (dh,):
+        raise ValueError(f"{name} must have shape {(dh,)}, got {tuple(w.shape)}")
     return w.data_ptr()
 
 
@@ -392,18 +399,23 @@ def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False
     each axis (P in all).  q and k may be strided views; q_out, k_out may be q, k.
     Returns (q_out, k_out), allocated contiguous when not given."""
     qh = _heads(q, "q")
-    T, hq, dh = q.shape
-    hk, kh = _second(k, "k", q, T, dh)
-    rope = _rope(table, pos, axis_pairs, interleaved, T, q)
-    wqp, wkp = _weight(wq, "wq", q), _weight(wk, "wk", q)
-    code = dtype_code(q.dtype)
-    q_out, qoh = _heads_out(q_out, "q_out", q)
-    koh = None
-    if kh is not None:
-        k_out, koh = _heads_out(k_out, "k_out", k)
+    qs, dt, dev = q.shape, q.dtype, q.get_device()
+    T, hq, dh = qs
+    hk, ks, kh = 0, None, None
+    if k is not None:
+        ks, kh = _second(k, "k", T, dh, dt, dev)
+        hk = ks[1]
+    rope = _rope(table, pos, axis_pairs, interleaved, T, dev)
+    wqp, wkp = _weight(wq, "wq", dh, dt, dev), _weight(wk, "wk", dh, dt, dev)
+    code = dtype_code(dt)
+    device, koh = q.device, None
+    q_out, qoh = _output(q_out, "q_out", qs, dt, dev, device)
+    if ks is not None:
+        k_out, koh = _output(k_out, "k_out", ks, dt, dev, device)
     rc = raw.adaln_qk_rope_fwd(qh, kh, T, hq, hk, dh, code, rope, 1 if norm else 0, wqp, wkp, eps,
-                               qoh, koh, _stream_ptr(stream, q.get_device()))
-    _check(rc, "adaln_qk_rope_fwd")
+                               qoh, koh, _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "adaln_qk_rope_fwd")
     return q_out, k_out
 
 
@@ -425,36 +437,45 @@ def adaln_qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved=True, 
     dk, dwk without k).  `workspace` is a uint8 CUDA tensor of at least
     adaln_qk_rope_bwd_workspace_size bytes (allocated when not given)."""
     doh = _heads(dq_out, "dq_out")
-    T, hq, dh = dq_out.shape
-    hk, dkoh = _second(dk_out, "dk_out", dq_out, T, dh)
-    rope = _rope(table, pos, axis_pairs, interleaved, T, dq_out)
-    code = dtype_code(dq_out.dtype)
-    wqp, wkp = _weight(wq, "wq", dq_out), _weight(wk, "wk", dq_out)
+    qs, dt, dev = dq_out.shape, dq_out.dtype, dq_out.get_device()
+    T, hq, dh = qs
+    hk, ks, dkoh = 0, None, None
+    if dk_out is not None:
+        ks, dkoh = _second(dk_out, "dk_out", T, dh, dt, dev)
+        hk = ks[1]
+    rope = _rope(table, pos, axis_pairs, interleaved, T, dev)
+    code, device = dtype_code(dt), dq_out.device
+    wqp, wkp = _weight(wq, "wq", dh, dt, dev), _weight(wk, "wk", dh, dt, dev)
     qh = kh = dkh = ws = None
     nbytes = 0
     if norm:
         if q is None or (k is None) != (dk_out is None):
             raise ValueError("the norm's backward needs the forward's q (and k)")
-        qh = _heads(q, "q", dq_out)
-        kh = _heads(k, "k", dk_out) if k is not None else None
-        dwq = (torch.empty(dh, device=q.device, dtype=torch.float32) if dwq is None
-               else _dev(dwq, "dwq", torch.float32, (dh,)))
+        qh = _heads(q, "q", qs, dt, dev)
         if k is not None:
-            dwk = (torch.empty(dh, device=q.device, dtype=torch.float32) if dwk is None
-                   else _dev(dwk, "dwk", torch.float32, (dh,)))
+            kh = _heads(k, "k", ks, dt, dev)
+            if dwk is None:
+                dwk = torch.empty(dh, device=device, dtype=torch.float32)
+            else:
+                _dev(dwk, "dwk", torch.float32, (dh,))
+        if dwq is None:
+            dwq = torch.empty(dh, device=device, dtype=torch.float32)
+        else:
+            _dev(dwq, "dwq", torch.float32, (dh,))
         if workspace is None:
             workspace = torch.empty(max(16, adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, code)),
-                                    device=q.device, dtype=torch.uint8)
+                                    device=device, dtype=torch.uint8)
         else:
             _dev(workspace, "workspace", torch.uint8)
         ws, nbytes = workspace.data_ptr(), workspace.numel()
-    dq, dqh = _heads_out(dq, "dq", dq_out)
-    if dkoh is not None:
-        dk, dkh = _heads_out(dk, "dk", dk_out)
+    dq, dqh = _output(dq, "dq", qs, dt, dev, device)
+    if ks is not None:
+        dk, dkh = _output(dk, "dk", ks, dt, dev, device)
     rc = raw.adaln_qk_rope_bwd(doh, dkoh, qh, kh, T, hq, hk, dh, code, rope, 1 if norm else 0, wqp,
                                wkp, eps, dqh, dkh, _ptr(dwq), _ptr(dwk), ws, nbytes,
-                               _stream_ptr(stream, dq_out.get_device()))
-    _check(rc, "adaln_qk_rope_bwd")
+                               _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "adaln_qk_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -492,15 +513,24 @@ def _act(act):
     return ACTS[act]
 
 
+def _matrix(t, name, shape, dtype, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous on cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
 def _ffn_args(x, wg, wu, wd):
-    _dev(x, "x")
+    """T, D, F, the dtype, the device's index, and the four pointers."""
     T, D = x.shape
-    F = wg.shape[0]
-    dt = x.dtype
-    _dev(wg, "wg", dt, (F, D))
-    _dev(wu, "wu", dt, (F, D))
-    _dev(wd, "wd", dt, (D, F))
-    return T, D, F
+    F, dt, dev = wg.shape[0], x.dtype, x.get_device()
+    if dev < 0 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA tensor")
+    return (T, D, F, dt, dev, x.data_ptr(), _matrix(wg, "wg", (F, D), dt, dev),
+            _matrix(wu, "wu", (F, D), dt, dev), _matrix(wd, "wd", (D, F), dt, dev))
 
 
 def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, workspace=None,
@@ -509,20 +539,26 @@ def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, wor
     act "silu", "gelu_tanh" or "gelu".  With `save` (or a `saved` buffer of
     adaln_ffn_saved_size bytes) also keeps what adaln_ffn_bwd needs.
     Returns (y, saved), saved None without."""
-    T, D, F = _ffn_args(x, wg, wu, wd)
-    code, dt = _act(act), dtype_code(x.dtype)
-    y = torch.empty_like(x) if y is None else _dev(y, "y", x.dtype, (T, D))
+    T, D, F, dtype, dev, xp, gp, up, dp = _ffn_args(x, wg, wu, wd)
+    act, dt, device = _act(act), dtype_code(dtype), x.device
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _matrix(y, "y", (T, D), dtype, dev)
+    sp = None
     if save or saved is not None:
         need = adaln_ffn_saved_size(T, D, F, dt)
         if saved is None:
-            saved = torch.empty(max(16, need), device=x.device, dtype=torch.uint8)
+            saved = torch.empty(max(16, need), device=device, dtype=torch.uint8)
         elif _dev(saved, "saved", torch.uint8).numel() < need:
             raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
-    workspace = _ffn_workspace(workspace, T, D, F, dt, False, x.device)
-    rc = raw.adaln_ffn_fwd(_ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), T, D, F, dt, code, _ptr(y),
-                           _ptr(saved), _ptr(workspace), workspace.numel(),
-                           _stream_ptr(stream, x.get_device()))
-    _check(rc, "adaln_ffn_fwd")
+        sp = saved.data_ptr()
+    workspace = _ffn_workspace(workspace, T, D, F, dt, False, device)
+    rc = raw.adaln_ffn_fwd(xp, gp, up, dp, T, D, F, dt, act, yp, sp, workspace.data_ptr(),
+                           workspace.numel(), _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "adaln_ffn_fwd")
     return y, saved
 
 
@@ -530,21 +566,23 @@ def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=N
                   workspace=None, stream=None):
     """Backward of adaln_ffn_fwd, from its inputs and what it saved.  Returns
     (dx, dwg, dwu, dwd), all bf16."""
-    T, D, F = _ffn_args(x, wg, wu, wd)
-    code, dt = _act(act), dtype_code(x.dtype)
-    _dev(dy, "dy", x.dtype, (T, D))
+    T, D, F, dtype, dev, xp, gp, up, dp = _ffn_args(x, wg, wu, wd)
+    act, dt = _act(act), dtype_code(dtype)
+    dyp = _matrix(dy, "dy", (T, D), dtype, dev)
     need = adaln_ffn_saved_size(T, D, F, dt)
     if _dev(saved, "saved", torch.uint8).numel() < need:
         raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
-    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", x.dtype, (T, D))
-    dwg = torch.empty_like(wg) if dwg is None else _dev(dwg, "dwg", x.dtype, (F, D))
-    dwu = torch.empty_like(wu) if dwu is None else _dev(dwu, "dwu", x.dtype, (F, D))
-    dwd = torch.empty_like(wd) if dwd is None else _dev(dwd, "dwd", x.dtype, (D, F))
+    dx = torch.empty_like(x) if dx is None else dx
+    dwg = torch.empty_like(wg) if dwg is None else dwg
+    dwu = torch.empty_like(wu) if dwu is None else dwu
+    dwd = torch.empty_like(wd) if dwd is None else dwd
+    outs = (_matrix(dx, "dx", (T, D), dtype, dev), _matrix(dwg, "dwg", (F, D), dtype, dev),
+            _matrix(dwu, "dwu", (F, D), dtype, dev), _matrix(dwd, "dwd", (D, F), dtype, dev))
     workspace = _ffn_workspace(workspace, T, D, F, dt, True, x.device)
-    rc = raw.adaln_ffn_bwd(_ptr(dy), _ptr(x), _ptr(wg), _ptr(wu), _ptr(wd), _ptr(saved), T, D, F,
-                           dt, code, _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(dwd), _ptr(workspace),
-                           workspace.numel(), _stream_ptr(stream, x.get_device()))
-    _check(rc, "adaln_ffn_bwd")
+    rc = raw.adaln_ffn_bwd(dyp, xp, gp, up, dp, saved.data_ptr(), T, D, F, dt, act, *outs,
+                           workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev))
+    if rc:
+        _check(rc, "adaln_ffn_bwd")
     return dx, dwg, dwu, dwd
 
 

@@ -1,5 +1,6 @@
 // C ABI of libadaln: argument checks (all before any CUDA call), launch-shape
 // cache, the per-device status word, and the kernel timing trace.
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <vector>
@@ -267,7 +268,13 @@ size_t bwd_workspace_need(int64_t T, int32_t D, int32_t nseg, adaln_dtype_t dtyp
 cudaError_t status_word(unsigned** out) { return status_ptr(out); }
 
 cudaError_t sm_count(int dev, int* sms) {
-  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<int> known[kMaxDevices];  // 0: not asked yet
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  *sms = known[dev].load(std::memory_order_relaxed);
+  if (*sms != 0) return cudaSuccess;
+  const cudaError_t e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 cudaError_t traced_call(int kernel, cudaStream_t st, cudaError_t (*launch)(void*), void* with) {
