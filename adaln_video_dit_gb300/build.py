@@ -16,8 +16,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libadaln.so")
 LIB_TUNING = os.path.join(HERE, "libadaln_tuning.so")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "ffn.cu", "ffn_skinny.cu", "host.cu", "noalloc.cu", "rope.cu",
-           "selftest.cu"]
-HEADERS = ["common.cuh", "ring.cuh", "tc.cuh", "ffn.cuh", "internal.h"]
+           "rope_bf16.cu", "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "selftest.cu"]
+HEADERS = ["common.cuh", "ring.cuh", "tc.cuh", "ffn.cuh", "rope.cuh", "internal.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -111,7 +111,8 @@ def _strip_comments(text):
 
 
 # Sources that no AdaLN kernel is made of.
-OTHER_OPERATORS = {"ffn.cu", "ffn.cuh", "ffn_skinny.cu", "rope.cu", "tc.cuh"}
+OTHER_OPERATORS = {"ffn.cu", "ffn.cuh", "ffn_skinny.cu", "rope.cu", "rope.cuh", "rope_bf16.cu",
+                   "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "tc.cuh"}
 
 
 def source_hash():

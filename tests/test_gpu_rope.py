@@ -9,7 +9,9 @@ Tolerances, from the arithmetic (u = 2^-24, the fp32 rounding unit):
   |n| bounds the forward;
   dx adds two terms of sizes r |h| and r |x r| mean|h x r|, each with the
   forward's error and one more sum of that length: 128 u of their sum;
-  dw sums its terms in chains of at most 64 here: 80 u of the sum of |terms|;
+  dw sums its terms in chains of at most 64 here (128 in the cases of 12000
+  tokens: tokens of a lane, lanes, warps and partial sums): 80 u (144 u) of the
+  sum of |terms|;
   a bf16 output adds its one rounding, 2^-8 of the element.
 """
 import pytest
@@ -139,6 +141,17 @@ CASES = [
     (33, 3, 2, 64, 64, 3, False, "bf16", "head_major"),
     (257, 17, 0, 64, 64, 3, True, "bf16", "dense"),
     (2000, 3, 1, 64, 48, 3, False, "bf16", "dense"),
+    # halves that only 8- or 4-byte vectors fit
+    (67, 5, 2, 80, 40, 3, False, "bf16", "packed"),
+    (67, 3, 1, 200, 100, 3, False, "bf16", "dense"),
+    (67, 3, 1, 40, 36, 3, False, "f32", "dense"),
+    (67, 3, 1, 68, 36, 3, False, "bf16", "dense"),
+    # many tokens of few heads: several tokens side by side in a warp
+    (12001, 3, 1, 64, 64, 3, True, "bf16", "packed"),
+    (12001, 8, 1, 32, 32, 3, False, "f32", "dense"),
+    (12001, 2, 5, 80, 80, 3, False, "f32", "packed"),
+    (12001, 4, 1, 72, 36, 3, False, "bf16", "dense"),
+    (12001, 1, 2, 256, 128, 3, True, "bf16", "dense"),
 ]
 
 
@@ -206,7 +219,7 @@ def test_against_64_bits(adaln, case, norm, weights):
         close(dev[n]["out"], ref["y"], ref["ys"], 64, n + " out")
         close(dev[n]["dx"], ref["dx"], ref["dxs"], 128, "d" + n)
         if norm:
-            close(dw, ref["dw"], ref["dws"], 80, "dw")
+            close(dw, ref["dw"], ref["dws"], 80 if T < 10000 else 144, "dw")
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
@@ -254,6 +267,10 @@ def test_positions_outside_the_table_are_recorded(adaln):
     ps = torch.zeros(40, 1, dtype=torch.int32, device="cuda") + 2
     want, _ = adaln.adaln_qk_rope_fwd(q, None, tb, ps, axis_pairs=(32,))
     status_ok()
+    many = torch.zeros(12000, 1, dtype=torch.int32, device="cuda")  # several tokens to a warp
+    many[7001] = 6
+    adaln.adaln_qk_rope_fwd(torch.randn(12000, 1, 64, device="cuda"), None, tb, many, axis_pairs=(32,))
+    assert adaln.adaln_get_status() == (adaln.ADALN_ERR_POS, adaln.ADALN_DEV_POS_RANGE)
     for bad in (6, -2, 2 ** 31 - 1, -2 ** 31):
         ps[17] = bad
         out, _ = adaln.adaln_qk_rope_fwd(q, None, tb, ps, axis_pairs=(32,))
