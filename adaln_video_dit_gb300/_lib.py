@@ -523,6 +523,14 @@ def _matrix(t, name, shape, dtype, dev):
     return t.data_ptr()
 
 
+def _matrix_out(t, name, like, dtype, dev):
+    """An output like `like`: checked, or allocated; it and its pointer."""
+    if t is not None:
+        return t, _matrix(t, name, like.shape, dtype, dev)
+    t = torch.empty_like(like)
+    return t, t.data_ptr()
+
+
 def _ffn_args(x, wg, wu, wd):
     """T, D, F, the dtype, the device's index, and the four pointers."""
     T, D = x.shape
@@ -541,11 +549,7 @@ def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, wor
     Returns (y, saved), saved None without."""
     T, D, F, dtype, dev, xp, gp, up, dp = _ffn_args(x, wg, wu, wd)
     act, dt, device = _act(act), dtype_code(dtype), x.device
-    if y is None:
-        y = torch.empty_like(x)
-        yp = y.data_ptr()
-    else:
-        yp = _matrix(y, "y", (T, D), dtype, dev)
+    y, yp = _matrix_out(y, "y", x, dtype, dev)
     sp = None
     if save or saved is not None:
         need = adaln_ffn_saved_size(T, D, F, dt)
@@ -572,15 +576,13 @@ def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=N
     need = adaln_ffn_saved_size(T, D, F, dt)
     if _dev(saved, "saved", torch.uint8).numel() < need:
         raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
-    dx = torch.empty_like(x) if dx is None else dx
-    dwg = torch.empty_like(wg) if dwg is None else dwg
-    dwu = torch.empty_like(wu) if dwu is None else dwu
-    dwd = torch.empty_like(wd) if dwd is None else dwd
-    outs = (_matrix(dx, "dx", (T, D), dtype, dev), _matrix(dwg, "dwg", (F, D), dtype, dev),
-            _matrix(dwu, "dwu", (F, D), dtype, dev), _matrix(dwd, "dwd", (D, F), dtype, dev))
+    dx, dxp = _matrix_out(dx, "dx", x, dtype, dev)
+    dwg, dwgp = _matrix_out(dwg, "dwg", wg, dtype, dev)
+    dwu, dwup = _matrix_out(dwu, "dwu", wu, dtype, dev)
+    dwd, dwdp = _matrix_out(dwd, "dwd", wd, dtype, dev)
     workspace = _ffn_workspace(workspace, T, D, F, dt, True, x.device)
-    rc = raw.adaln_ffn_bwd(dyp, xp, gp, up, dp, saved.data_ptr(), T, D, F, dt, act, *outs,
-                           workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev))
+    rc = raw.adaln_ffn_bwd(dyp, xp, gp, up, dp, saved.data_ptr(), T, D, F, dt, act, dxp, dwgp,
+                           dwup, dwdp, workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev))
     if rc:
         _check(rc, "adaln_ffn_bwd")
     return dx, dwg, dwu, dwd

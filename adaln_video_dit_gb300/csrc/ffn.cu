@@ -18,14 +18,25 @@
 //
 // Roundings to bf16: h, dg and du, once each, because the matrix instructions
 // take 16-bit operands; and the outputs.  g and u themselves are kept for the
-// backward as fp32 cut to 24 bits (16 bits of one array and the next 8 of
-// another: 2^-15 relative), not as bf16: with 8 bits of mantissa their rounding
-// would enter dg, du and h beside those arrays' own.
+// backward as fp32 cut to 24 bits (2^-15 relative), not as bf16: with 8 bits of
+// mantissa their rounding would enter dg, du and h beside those arrays' own.
 //
 // A kernel is persistent, one CTA pair per two SMs: a 256 x 256 tile a pair
-// (narrower ones where that fills the pairs better), k steps of 64 through a ring of TMA-filled stages; per CTA one producer warp,
-// one issuing warp (even CTA) and eight epilogue warps, two accumulators in
-// tensor memory so that a tile's epilogue runs under the next tile's products.
+// (narrower ones where that fills the pairs better), k steps of 64 through a
+// ring of TMA-filled stages; per CTA one producer warp, one issuing warp (even
+// CTA) and eight epilogue warps, two accumulators in tensor memory so that a
+// tile's epilogue runs under the next tile's products.
+//
+// Bound: the tensor cores from a few hundred tokens on, below that the weights'
+// bytes.  Measured (one GB300; 1725 TFLOP/s is what the library's bf16 product
+// sustains under the power limit, 1947 in a burst): T = 32760, D = 5120, F =
+// 13824 forward 7.9 ms, 1750 TFLOP/s; T = 8192 forward and backward 6.4 ms, 1640;
+// T = 8192, D = 1536, F = 4096 forward 166 us, 1860, forward and backward 642 us,
+// 1445.  There (k = 1536) the products are busy for 96 % of the weight
+// gradients' and dx's launch, 87 % of y's (192 tiles are 2.5 rounds of 76 pairs),
+// 73 % of the projections' while saving and 53 % of the gate's gradient: the
+// last two move 10 and 14 bytes through L2 per 1000 operations where the first
+// moves 7, and all three run at the same 15 TB/s of it.
 #include <cmath>
 #include <mutex>
 
@@ -774,12 +785,10 @@ Tiling choose_tiling(int64_t M, int N, int kb, bool gate, bool b_mn, bool may_sp
 
 cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2], int segs, int64_t M,
                         int N, bool gate, const Tiling& t, int64_t k0, int64_t k1, void* out) {
-  cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-    const bool have_a = i < segs, have_b = b[i].p != nullptr;
-    e = operand_map(&p->a[i], have_a ? a[i] : a[0], 128);
-    if (e == cudaSuccess) e = operand_map(&p->b[i], have_b ? b[i] : b[0], t.w);
-  }
+  cudaError_t e = operand_map(&p->a[0], a[0], 128);
+  if (e == cudaSuccess) e = operand_map(&p->b[0], b[0], t.w);
+  if (e == cudaSuccess && segs > 1) e = operand_map(&p->a[1], a[1], 128);
+  if (e == cudaSuccess && b[1].p != nullptr) e = operand_map(&p->b[1], b[1], t.w);
   if (e == cudaSuccess && out) e = block_map(&p->out, out, M, N);
   p->partial = nullptr;
   Dims& s = p->s;

@@ -1,7 +1,11 @@
 /*
- * libadaln -- fused AdaLN LayerNorm-Modulate for GB300 (sm_103a).
+ * libadaln -- operators of video diffusion transformer blocks for GB300
+ * (sm_103a): the fused AdaLN LayerNorm-Modulate, described here, and, further
+ * down, rotary positions with the norm of queries and keys (adaln_qk_rope_*)
+ * and the gated feed-forward block (adaln_ffn_*), which share its conventions
+ * on ownership, streams, errors and the status word.
  *
- * The operator is the fused adaptive LayerNorm of video / MMDiT diffusion
+ * The AdaLN is the fused adaptive LayerNorm of video / MMDiT diffusion
  * transformers described in "AdaptiveLoad: Towards Efficient Video Diffusion
  * Transformer Training", Technical summary, section 2.B ("Fused
  * LayerNorm-Modulate CUDA kernels"): normalisation and modulation in a single
@@ -252,11 +256,12 @@ typedef struct {
 /*
  * Forward, one launch.  q [T, hq, dh] and k [T, hk, dh] (hk or hq may be 0,
  * its pointers NULL) may be views of a packed projection; q_out, k_out may be
- * the inputs themselves (in place), but may not overlap them otherwise.
- * wq, wk [dh] have the element type `dtype`; NULL means ones.  Head rows of
- * whole 16-byte vectors at 16-byte aligned addresses (and at most 64 of them;
- * for halves, P elements also a whole number of vectors) take a vector path,
- * everything else a scalar one with the same results up to fp32 rounding.
+ * the inputs themselves (in place), but may not overlap them otherwise, nor
+ * themselves or each other.  wq, wk [dh] have the element type `dtype`; NULL
+ * means ones.  Heads of at most 64 whole 16-byte vectors at 16-byte aligned
+ * addresses take a vector path (for halves, P elements are then whole vectors
+ * too, of 16, 8 or 4 bytes, aligned as such), everything else a scalar one with
+ * the same results up to fp32 rounding.
  * A position outside [-1, rows) is treated as -1 and recorded in the status
  * word (ADALN_DEV_POS_RANGE).
  *
