@@ -12,13 +12,13 @@ The binding is imported lazily so that the input generators load without a GPU.
 
 __all__ = ["inputs", "lib"]
 
-_binding = None
+_lib_module = None
 
 
 def lib():
     """The ctypes binding of libadaln.so (raises if the library is missing)."""
-    global _binding
-    if _binding is None:
+    global _lib_module
+    if _lib_module is None:
         from . import _lib
-        _binding = _lib
-    return _binding
+        _lib_module = _lib
+    return _lib_module

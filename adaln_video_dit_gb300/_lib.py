@@ -1,6 +1,7 @@
 """ctypes binding of libadaln.so (C ABI: include/adaln.h).
 
-Argument marshalling only: every step of the operator runs in the library's
+Argument marshalling only (for the rotary and feed-forward calls in the compiled
+_binding, csrc/binding.cpp): every step of the operators runs in the library's
 CUDA kernels.  torch supplies device memory, streams and output allocation.
 The functions carry the C names.  There is no fallback: if libadaln.so is
 missing or a call fails, an exception is raised.
@@ -122,6 +123,19 @@ def _load():
 raw = _load()
 
 
+def _load_binding():
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError("_binding.so is missing beside libadaln.so; build both with "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    entries = ("adaln_qk_rope_fwd", "adaln_qk_rope_bwd", "adaln_qk_rope_bwd_workspace_size",
+               "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size")
+    _binding.setup(torch, torch._C._cuda_getCurrentRawStream, AdalnError,
+                   {n: ctypes.cast(getattr(raw, n), ctypes.c_void_p).value for n in entries})
+    return _binding
+
+
 def strerror(code):
     return raw.adaln_strerror(int(code)).decode()
 
@@ -129,6 +143,9 @@ def strerror(code):
 def _check(rc, what):
     if rc != ADALN_OK:
         raise AdalnError(rc, what)
+
+
+_binding = _load_binding()
 
 
 def dtype_code(t):
@@ -310,86 +327,6 @@ def adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_row
     _check(rc, "adaln_fwd_bwd_host")
 
 
-# The calls of the small operators are bound by this host code, so their checks
-# read each attribute of a tensor once (about 0.1 us each).
-
-
-def _heads(t, name, shape=None, dtype=None, dev=None):
-    """Check a [T, heads, dh] tensor (any strides, dh contiguous), and its shape,
-    dtype and device where given; its Heads."""
-    s = t.shape
-    if len(s) != 3:
-        raise ValueError(f"{name} must be [T, heads, dh], got {tuple(s)}")
-    d = t.get_device()
-    if d < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if shape is not None:
-        if s != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(s)}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if d != dev:
-            raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    ts, hs, ds = t.stride()
-    if ds != 1 and s[2] != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return Heads(t.data_ptr(), ts, hs)
-
-
-def _second(k, name, T, dh, dtype, dev):
-    """Check the keys against the queries; their shape and Heads."""
-    kh = _heads(k, name)
-    s = k.shape
-    if s[0] != T or s[2] != dh:
-        raise ValueError("queries and keys must agree in tokens and head width")
-    if k.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {k.dtype}")
-    if k.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {k.device}")
-    return s, kh
-
-
-def _output(t, name, shape, dtype, dev, device):
-    """An output, checked or allocated contiguous, and its Heads."""
-    if t is not None:
-        return t, _heads(t, name, shape, dtype, dev)
-    t = torch.empty(shape, dtype=dtype, device=device)
-    return t, Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
-
-
-_Pairs = ctypes.c_int32 * MAX_ROPE_AXES
-
-
-def _rope(table, pos, axis_pairs, interleaved, T, dev):
-    if table.get_device() != dev or pos.get_device() != dev:
-        raise ValueError(f"table and pos must be on cuda:{dev}")
-    if table.dtype != torch.float32 or not table.is_contiguous():
-        raise ValueError("table must be contiguous float32")
-    if pos.dtype != torch.int32 or not pos.is_contiguous():
-        raise ValueError("pos must be contiguous int32")
-    axes, P, s = len(axis_pairs), sum(axis_pairs), table.shape
-    if not 1 <= axes <= MAX_ROPE_AXES or min(axis_pairs) < 0:
-        raise ValueError(f"axis_pairs must hold 1 to {MAX_ROPE_AXES} counts >= 0")
-    if len(s) != 3 or s[1] != P or s[2] != 2:
-        raise ValueError(f"table must have shape [rows, {P}, 2], got {tuple(s)}")
-    if pos.shape != (T, axes):
-        raise ValueError(f"pos must have shape {(T, axes)}, got {tuple(pos.shape)}")
-    return Rope(table.data_ptr(), pos.data_ptr(), s[0], axes, _Pairs(*axis_pairs),
-                1 if interleaved else 0)
-
-
-def _weight(w, name, dh, dtype, dev):
-    if w is None:
-        return None
-    if w.get_device() != dev or not w.is_contiguous():
-        raise ValueError(f"{name} must be contiguous on cuda:{dev}")
-    if w.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {w.dtype}")
-    if w.shape != (dh,):
-        raise ValueError(f"{name} must have shape {(dh,)}, got {tuple(w.shape)}")
-    return w.data_ptr()
-
-
 def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False, wq=None,
                       wk=None, eps=1e-6, q_out=None, k_out=None, stream=None):
     """Rotary positions of q [T, hq, dh] and k [T, hk, dh] (k may be None), after
@@ -398,25 +335,8 @@ def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False
     pos [T, axes] int32 rows of it (-1: unrotated), axis_pairs the pairs of
     each axis (P in all).  q and k may be strided views; q_out, k_out may be q, k.
     Returns (q_out, k_out), allocated contiguous when not given."""
-    qh = _heads(q, "q")
-    qs, dt, dev = q.shape, q.dtype, q.get_device()
-    T, hq, dh = qs
-    hk, ks, kh = 0, None, None
-    if k is not None:
-        ks, kh = _second(k, "k", T, dh, dt, dev)
-        hk = ks[1]
-    rope = _rope(table, pos, axis_pairs, interleaved, T, dev)
-    wqp, wkp = _weight(wq, "wq", dh, dt, dev), _weight(wk, "wk", dh, dt, dev)
-    code = dtype_code(dt)
-    device, koh = q.device, None
-    q_out, qoh = _output(q_out, "q_out", qs, dt, dev, device)
-    if ks is not None:
-        k_out, koh = _output(k_out, "k_out", ks, dt, dev, device)
-    rc = raw.adaln_qk_rope_fwd(qh, kh, T, hq, hk, dh, code, rope, 1 if norm else 0, wqp, wkp, eps,
-                               qoh, koh, _stream_ptr(stream, dev))
-    if rc:
-        _check(rc, "adaln_qk_rope_fwd")
-    return q_out, k_out
+    return _binding.qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved, norm, wq, wk, eps, q_out,
+                                k_out, stream)
 
 
 def adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, dtype):
@@ -436,47 +356,8 @@ def adaln_qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved=True, 
     Returns (dq, dk, dwq, dwk); dwq, dwk are fp32 [dh], None without norm (and
     dk, dwk without k).  `workspace` is a uint8 CUDA tensor of at least
     adaln_qk_rope_bwd_workspace_size bytes (allocated when not given)."""
-    doh = _heads(dq_out, "dq_out")
-    qs, dt, dev = dq_out.shape, dq_out.dtype, dq_out.get_device()
-    T, hq, dh = qs
-    hk, ks, dkoh = 0, None, None
-    if dk_out is not None:
-        ks, dkoh = _second(dk_out, "dk_out", T, dh, dt, dev)
-        hk = ks[1]
-    rope = _rope(table, pos, axis_pairs, interleaved, T, dev)
-    code, device = dtype_code(dt), dq_out.device
-    wqp, wkp = _weight(wq, "wq", dh, dt, dev), _weight(wk, "wk", dh, dt, dev)
-    qh = kh = dkh = ws = None
-    nbytes = 0
-    if norm:
-        if q is None or (k is None) != (dk_out is None):
-            raise ValueError("the norm's backward needs the forward's q (and k)")
-        qh = _heads(q, "q", qs, dt, dev)
-        if k is not None:
-            kh = _heads(k, "k", ks, dt, dev)
-            if dwk is None:
-                dwk = torch.empty(dh, device=device, dtype=torch.float32)
-            else:
-                _dev(dwk, "dwk", torch.float32, (dh,))
-        if dwq is None:
-            dwq = torch.empty(dh, device=device, dtype=torch.float32)
-        else:
-            _dev(dwq, "dwq", torch.float32, (dh,))
-        if workspace is None:
-            workspace = torch.empty(max(16, adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, code)),
-                                    device=device, dtype=torch.uint8)
-        else:
-            _dev(workspace, "workspace", torch.uint8)
-        ws, nbytes = workspace.data_ptr(), workspace.numel()
-    dq, dqh = _output(dq, "dq", qs, dt, dev, device)
-    if ks is not None:
-        dk, dkh = _output(dk, "dk", ks, dt, dev, device)
-    rc = raw.adaln_qk_rope_bwd(doh, dkoh, qh, kh, T, hq, hk, dh, code, rope, 1 if norm else 0, wqp,
-                               wkp, eps, dqh, dkh, _ptr(dwq), _ptr(dwk), ws, nbytes,
-                               _stream_ptr(stream, dev))
-    if rc:
-        _check(rc, "adaln_qk_rope_bwd")
-    return dq, dk, dwq, dwk
+    return _binding.qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved, norm, q, k, wq,
+                                wk, eps, dq, dk, dwq, dwk, workspace, stream)
 
 
 def adaln_ffn_saved_size(T, D, F, dtype=torch.bfloat16):
@@ -497,48 +378,10 @@ def adaln_ffn_workspace_size(T, D, F, dtype=torch.bfloat16):
     return f.value, b.value
 
 
-def _ffn_workspace(t, T, D, F, dt, backward, device):
-    """A call's workspace: the given one, checked, or a new one of the size needed."""
-    if t is not None:
-        return _dev(t, "workspace", torch.uint8)
-    n = ctypes.c_size_t(0)
-    f, b = (None, ctypes.byref(n)) if backward else (ctypes.byref(n), None)
-    _check(raw.adaln_ffn_workspace_size(T, D, F, dt, f, b), "adaln_ffn_workspace_size")
-    return torch.empty(max(16, n.value), device=device, dtype=torch.uint8)
-
-
 def _act(act):
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
     return ACTS[act]
-
-
-def _matrix(t, name, shape, dtype, dev):
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous on cuda:{dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _matrix_out(t, name, like, dtype, dev):
-    """An output like `like`: checked, or allocated; it and its pointer."""
-    if t is not None:
-        return t, _matrix(t, name, like.shape, dtype, dev)
-    t = torch.empty_like(like)
-    return t, t.data_ptr()
-
-
-def _ffn_args(x, wg, wu, wd):
-    """T, D, F, the dtype, the device's index, and the four pointers."""
-    T, D = x.shape
-    F, dt, dev = wg.shape[0], x.dtype, x.get_device()
-    if dev < 0 or not x.is_contiguous():
-        raise ValueError("x must be a contiguous CUDA tensor")
-    return (T, D, F, dt, dev, x.data_ptr(), _matrix(wg, "wg", (F, D), dt, dev),
-            _matrix(wu, "wu", (F, D), dt, dev), _matrix(wd, "wd", (D, F), dt, dev))
 
 
 def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, workspace=None,
@@ -547,45 +390,14 @@ def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, wor
     act "silu", "gelu_tanh" or "gelu".  With `save` (or a `saved` buffer of
     adaln_ffn_saved_size bytes) also keeps what adaln_ffn_bwd needs.
     Returns (y, saved), saved None without."""
-    T, D, F, dtype, dev, xp, gp, up, dp = _ffn_args(x, wg, wu, wd)
-    act, dt, device = _act(act), dtype_code(dtype), x.device
-    y, yp = _matrix_out(y, "y", x, dtype, dev)
-    sp = None
-    if save or saved is not None:
-        need = adaln_ffn_saved_size(T, D, F, dt)
-        if saved is None:
-            saved = torch.empty(max(16, need), device=device, dtype=torch.uint8)
-        elif _dev(saved, "saved", torch.uint8).numel() < need:
-            raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
-        sp = saved.data_ptr()
-    workspace = _ffn_workspace(workspace, T, D, F, dt, False, device)
-    rc = raw.adaln_ffn_fwd(xp, gp, up, dp, T, D, F, dt, act, yp, sp, workspace.data_ptr(),
-                           workspace.numel(), _stream_ptr(stream, dev))
-    if rc:
-        _check(rc, "adaln_ffn_fwd")
-    return y, saved
+    return _binding.ffn_fwd(x, wg, wu, wd, _act(act), save, y, saved, workspace, stream)
 
 
 def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=None, dwd=None,
                   workspace=None, stream=None):
     """Backward of adaln_ffn_fwd, from its inputs and what it saved.  Returns
     (dx, dwg, dwu, dwd), all bf16."""
-    T, D, F, dtype, dev, xp, gp, up, dp = _ffn_args(x, wg, wu, wd)
-    act, dt = _act(act), dtype_code(dtype)
-    dyp = _matrix(dy, "dy", (T, D), dtype, dev)
-    need = adaln_ffn_saved_size(T, D, F, dt)
-    if _dev(saved, "saved", torch.uint8).numel() < need:
-        raise ValueError(f"saved holds {saved.numel()} bytes, {need} are needed")
-    dx, dxp = _matrix_out(dx, "dx", x, dtype, dev)
-    dwg, dwgp = _matrix_out(dwg, "dwg", wg, dtype, dev)
-    dwu, dwup = _matrix_out(dwu, "dwu", wu, dtype, dev)
-    dwd, dwdp = _matrix_out(dwd, "dwd", wd, dtype, dev)
-    workspace = _ffn_workspace(workspace, T, D, F, dt, True, x.device)
-    rc = raw.adaln_ffn_bwd(dyp, xp, gp, up, dp, saved.data_ptr(), T, D, F, dt, act, dxp, dwgp,
-                           dwup, dwdp, workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev))
-    if rc:
-        _check(rc, "adaln_ffn_bwd")
-    return dx, dwg, dwu, dwd
+    return _binding.ffn_bwd(dy, x, wg, wu, wd, saved, _act(act), dx, dwg, dwu, dwd, workspace, stream)
 
 
 def adaln_get_status(stream=None, device=None):

@@ -2,7 +2,8 @@
 
 Each translation unit is compiled in parallel, then linked into one shared
 library beside this file.  No cmake, no torch extension machinery: the
-library exports a plain C ABI (include/adaln.h).
+library exports a plain C ABI (include/adaln.h).  Beside it goes _binding.so,
+the argument marshalling of the calls whose cost is their host code.
 """
 import concurrent.futures as cf
 import os
@@ -15,6 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libadaln.so")
 LIB_TUNING = os.path.join(HERE, "libadaln_tuning.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "ffn.cu", "ffn_skinny.cu", "host.cu", "noalloc.cu", "rope.cu",
            "rope_bf16.cu", "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "selftest.cu"]
 HEADERS = ["common.cuh", "ring.cuh", "tc.cuh", "ffn.cuh", "rope.cuh", "internal.h"]
@@ -35,12 +38,13 @@ def nvcc():
 def _deps():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
     files.append(os.path.join(ROOT, "include", "adaln.h"))
+    files.append(BINDING_SOURCE)
     files.append(os.path.abspath(__file__))
     return files
 
 
 def _stale(lib):
-    if not os.path.exists(lib):
+    if not os.path.exists(lib) or (lib == LIB and not os.path.exists(BINDING)):
         return True
     t = os.path.getmtime(lib)
     return any(os.path.getmtime(f) > t for f in _deps())
@@ -70,8 +74,11 @@ def build(force=False, verbose=False, ptxas_info=False, tuning=False):
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = None if tuning else ex.submit(build_binding)
         results = list(ex.map(compile_one, SOURCES))
+        if binding:
+            binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():
@@ -84,6 +91,19 @@ def build(force=False, verbose=False, ptxas_info=False, tuning=False):
     os.replace(tmp, lib)
     return lib
 
+
+
+def build_binding():
+    """Compile the argument marshalling extension (plain CPython, no torch header)."""
+    import sysconfig
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-I" + sysconfig.get_paths()["include"], BINDING_SOURCE, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def _strip_comments(text):
@@ -112,7 +132,7 @@ def _strip_comments(text):
 
 # Sources that no AdaLN kernel is made of.
 OTHER_OPERATORS = {"ffn.cu", "ffn.cuh", "ffn_skinny.cu", "rope.cu", "rope.cuh", "rope_bf16.cu",
-                   "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "tc.cuh"}
+                   "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "tc.cuh", "binding.cpp"}
 
 
 def source_hash():

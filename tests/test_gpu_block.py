@@ -78,3 +78,45 @@ def test_example_block_trains(adaln):
     assert all(map(lambda v: v == v, losses))
     assert losses[-1] < losses[0]
     status_ok()
+
+
+def test_calls_and_refusals_keep_no_references(adaln):
+    """The compiled marshalling owns what it takes and no more: after many calls,
+    refused ones among them, no tensor and no byte of device memory is left over."""
+    import gc
+    import sys
+
+    q = torch.randn(4, 2, 64, device="cuda")
+    table = torch.zeros(3, 32, 2, device="cuda")
+    pos = torch.zeros(4, 1, dtype=torch.int32, device="cuda")
+    x = torch.randn(4, 64, device="cuda").bfloat16()
+    w = [torch.randn(*s, device="cuda").bfloat16() for s in ((96, 64), (96, 64), (64, 96))]
+
+    def calls():
+        adaln.adaln_qk_rope_fwd(q, q, table, pos, (32,))
+        adaln.adaln_qk_rope_bwd(q, q, table, pos, (32,), norm=True, q=q, k=q)
+        _, saved = adaln.adaln_ffn_fwd(x, *w, save=True)
+        adaln.adaln_ffn_bwd(x, x, *w, saved)
+        for bad in (lambda: adaln.adaln_qk_rope_fwd(q.half(), None, table, pos, (32,)),
+                    lambda: adaln.adaln_qk_rope_fwd(q, None, table, pos, (31,)),
+                    lambda: adaln.adaln_qk_rope_fwd(q, None, table, pos, 7),
+                    lambda: adaln.adaln_qk_rope_fwd(q, "no tensor", table, pos, (32,)),
+                    lambda: adaln.adaln_qk_rope_fwd(q, None, table, pos, (32,), norm=True, eps=-1.0),
+                    lambda: adaln.adaln_qk_rope_bwd(q, q, table, pos, (32,), norm=True, q=q),
+                    lambda: adaln.adaln_ffn_fwd(x, w[0], w[1], w[1]),
+                    lambda: adaln.adaln_ffn_fwd(x.float(), *(t.float() for t in w)),
+                    lambda: adaln.adaln_ffn_bwd(x, x, *w, None)):
+            with pytest.raises((AttributeError, TypeError, ValueError, adaln.AdalnError)):
+                bad()
+
+    def state():
+        torch.cuda.synchronize()
+        gc.collect()
+        return (torch.cuda.memory_allocated(), *map(sys.getrefcount, (
+            q, table, pos, x, *w, torch.float32, torch.bfloat16, torch.uint8, adaln.AdalnError)))
+
+    calls()
+    before = state()
+    for _ in range(20):
+        calls()
+    assert state() == before
