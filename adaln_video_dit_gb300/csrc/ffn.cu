@@ -30,9 +30,9 @@
 // Bound: the tensor cores from a few hundred tokens on, below that the weights'
 // bytes.  Measured (one GB300; 1725 TFLOP/s is what the library's bf16 product
 // sustains under the power limit, 1947 in a burst): T = 32760, D = 5120, F =
-// 13824 forward 7.9 ms, 1750 TFLOP/s; T = 8192 forward and backward 6.4 ms, 1640;
-// T = 8192, D = 1536, F = 4096 forward 166 us, 1860, forward and backward 642 us,
-// 1445.  There (k = 1536) the products are busy for 96 % of the weight
+// 13824 forward 7.8 ms, 1785 TFLOP/s; T = 8192 forward and backward 6.2 ms, 1676;
+// T = 8192, D = 1536, F = 4096 forward 168 us, 1840, forward and backward 628 us,
+// 1477.  There (k = 1536) the products are busy for 96 % of the weight
 // gradients' and dx's launch, 87 % of y's (192 tiles are 2.5 rounds of 76 pairs),
 // 73 % of the projections' while saving and 53 % of the gate's gradient: the
 // last two move 10 and 14 bytes through L2 per 1000 operations where the first
