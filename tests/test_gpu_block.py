@@ -120,3 +120,52 @@ def test_calls_and_refusals_keep_no_references(adaln):
     for _ in range(20):
         calls()
     assert state() == before
+
+
+def test_calls_from_two_threads_on_two_streams(adaln):
+    """Both operators at once on two streams, each thread with its own tensors:
+    every result equals the serial one."""
+    import threading
+
+    def make(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+        return dict(q=r(900, 6, 64), k=r(900, 2, 64), dq=r(900, 6, 64), dk=r(900, 2, 64),
+                    w=r(64), table=torch.randn(9, 32, 2, device="cuda", generator=g),
+                    pos=torch.randint(-1, 9, (900, 1), device="cuda", generator=g).int(),
+                    x=[r(t, 256) for t in (1, 20, 300)], dy=[r(t, 256) for t in (1, 20, 300)],
+                    ffn=(r(512, 256), r(512, 256), r(256, 512)))
+
+    def work(s):
+        out = [*adaln.adaln_qk_rope_fwd(s["q"], s["k"], s["table"], s["pos"], (32,), norm=True,
+                                        wq=s["w"])]
+        out += adaln.adaln_qk_rope_bwd(s["dq"], s["dk"], s["table"], s["pos"], (32,), norm=True,
+                                       q=s["q"], k=s["k"], wq=s["w"])
+        for x, dy in zip(s["x"], s["dy"]):
+            y, saved = adaln.adaln_ffn_fwd(x, *s["ffn"], save=True)
+            out += [y, *adaln.adaln_ffn_bwd(dy, x, *s["ffn"], saved)]
+        return out
+
+    states = [make(1), make(2)]
+    want = [[t.clone() for t in work(s)] for s in states]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(15):
+                    got = work(states[i])
+                    stream.synchronize()
+                    wrong.extend(k for k, (a, b) in enumerate(zip(got, want[i])) if not torch.equal(a, b))
+        except Exception as e:  # noqa: BLE001 (reported by the assertion below)
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:5]
+    status_ok()
