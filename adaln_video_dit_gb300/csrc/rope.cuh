@@ -260,9 +260,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   grid_wait();
   grid_launch_dependents();
 
-  // Angles of pair p from table row `row` (-1: unrotated) into a table.
-  auto put_angle = [&](float4* table, int p, int row) {
-    float* const at = reinterpret_cast<float*>(table) + entry_of_pair(p);
+  // This lane's share of a token's pairs, p = lane, lane + 32, ...: f(p, its index
+  // into a table, its axis).  The norm's backward, which is the furthest from the
+  // memory's rate, keeps those of the first two (heads of up to 128 elements have no
+  // more): 16384 tokens of 24 + 24 heads x 64 bf16, both passes, 102.4 -> 101.1 us.
+  // The other kernels work them out anew: with more registers held the rotation of
+  // the joint stream went from 135.8 to 138.0 us, the long video's norm from 203 to 208.
+  const int at0 = entry_of_pair(min(lane, a.P - 1)), at1 = entry_of_pair(min(lane + 32, a.P - 1));
+  const int axis0 = axis_of(a, lane), axis1 = axis_of(a, lane + 32);
+  auto each_pair = [&](auto f) {
+    if constexpr (kGrad) {
+      if (lane < a.P) f(lane, at0, axis0);
+      if (lane + 32 < a.P) f(lane + 32, at1, axis1);
+    }
+    for (int p = lane + (kGrad ? 64 : 0); p < a.P; p += 32) f(p, entry_of_pair(p), axis_of(a, p));
+  };
+  // Angles of pair p from table row `row` (-1: unrotated) into a table at `index`.
+  auto put_angle = [&](float4* table, int index, int p, int row) {
+    float* const at = reinterpret_cast<float*>(table) + index;
     if (row >= 0) {
       const float* from = reinterpret_cast<const float*>(a.table + (int64_t)row * a.P + p);
       cp_async4(at, from);
@@ -280,8 +295,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   auto fetch_angles = [&](const Rows& rows, int b) {
     float4* const set = angles + b * batch * entries;
     if (!few) {
-      for (int p = lane; p < a.P; p += 32)
-        put_angle(set, p, pick(axis_of(a, p), rows.r[0], rows.r[1], rows.r[2], rows.r[3]));
+      each_pair([&](int p, int at, int axis) {
+        put_angle(set, at, p, pick(axis, rows.r[0], rows.r[1], rows.r[2], rows.r[3]));
+      });
       return;
     }
     int n = 0, p = lane;
@@ -290,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       int r[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) r[k] = k < a.axes ? __shfl_sync(~0u, rows.r[k], n & 31) : -1;
-      if (n < tokens) put_angle(set + n * entries, p, pick(axis_of(a, p), r[0], r[1], r[2], r[3]));
+      if (n < tokens)
+        put_angle(set + n * entries, entry_of_pair(p), p, pick(axis_of(a, p), r[0], r[1], r[2], r[3]));
       p += 32;
     }
   };
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (always) return true;
     const float* const from = reinterpret_cast<const float*>(angles + b * batch * entries);
     bool z = false;
-    for (int p = lane; p < a.P; p += 32) z |= from[entry_of_pair(p) + 2] == 0.0f;
+    each_pair([&](int, int at, int) { z |= from[at + 2] == 0.0f; });
     return (bool)__any_sync(~0u, z);
   };
 
