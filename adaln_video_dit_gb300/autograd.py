@@ -130,14 +130,17 @@ class QKNormRope(torch.nn.Module):
 
 class GatedFFNFunction(torch.autograd.Function):
     """y = (act(x wg') * (x wu')) wd', saving x and the two projections (24 bits
-    a value); without a gradient to come, nothing."""
+    a value); without a gradient to come, nothing.  `grad` is whether gradients
+    were on at the call: in here they are always off, and needs_input_grad is
+    True for a parameter under no_grad() too."""
 
     @staticmethod
-    def forward(ctx, x, wg, wu, wd, act):
+    def forward(ctx, x, wg, wu, wd, act, grad):
         shape = x.shape
         x2 = x.reshape(-1, shape[-1]).contiguous()
         wg, wu, wd = wg.contiguous(), wu.contiguous(), wd.contiguous()
-        y, saved = _lib.adaln_ffn_fwd(x2, wg, wu, wd, act=act, save=any(ctx.needs_input_grad))
+        y, saved = _lib.adaln_ffn_fwd(x2, wg, wu, wd, act=act,
+                                      save=grad and any(ctx.needs_input_grad))
         ctx.save_for_backward(x2, wg, wu, wd, saved)
         ctx.act, ctx.shape = act, shape
         return y.reshape(shape)
@@ -147,13 +150,13 @@ class GatedFFNFunction(torch.autograd.Function):
         x2, wg, wu, wd, saved = ctx.saved_tensors
         dy2 = dy.reshape(x2.shape).to(x2.dtype).contiguous()
         dx, dwg, dwu, dwd = _lib.adaln_ffn_bwd(dy2, x2, wg, wu, wd, saved, act=ctx.act)
-        return dx.reshape(ctx.shape), dwg, dwu, dwd, None
+        return dx.reshape(ctx.shape), dwg, dwu, dwd, None, None
 
 
 def gated_ffn(x, wg, wu, wd, act="silu"):
     """The gated feed-forward block of bf16 x [..., D] with wg, wu [F, D], wd
     [D, F]; act "silu", "gelu_tanh" or "gelu" (differentiable)."""
-    return GatedFFNFunction.apply(x, wg, wu, wd, act)
+    return GatedFFNFunction.apply(x, wg, wu, wd, act, torch.is_grad_enabled())
 
 
 class GatedFFN(torch.nn.Module):

@@ -124,3 +124,27 @@ def test_ffn_only_what_is_missing_is_refused(lib):
     assert lib.raw.adaln_ffn_saved_size(40, 64, 40, lib.ADALN_BF16, None) == lib.ADALN_ERR_NULL
     assert lib.raw.adaln_ffn_workspace_size(40, 64, 40, lib.ADALN_BF16, None, None) == lib.ADALN_ERR_NULL
     assert lib.raw.adaln_ffn_workspace_size(40, 64, 41, lib.ADALN_BF16, None, None) == lib.ADALN_ERR_DIM
+
+
+def test_gated_ffn_saves_only_for_a_gradient(lib, monkeypatch):
+    """Nothing is saved under no_grad() or inference_mode(), where the weights
+    still require a gradient, nor for frozen weights."""
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    asked = []
+
+    def fake(x, wg, wu, wd, act, save):
+        asked.append(save)
+        return torch.zeros_like(x), torch.zeros(1, dtype=torch.uint8) if save else None
+
+    monkeypatch.setattr(autograd._lib, "adaln_ffn_fwd", fake)
+    m, x = autograd.GatedFFN(8, 16), torch.zeros(3, 8, dtype=torch.bfloat16)
+    assert m(x).requires_grad
+    with torch.no_grad():
+        assert not m(x).requires_grad
+    with torch.inference_mode():
+        m(x)
+    m.requires_grad_(False)
+    m(x)
+    m(x.clone().requires_grad_())
+    assert asked == [True, False, False, False, True]
