@@ -327,6 +327,17 @@ def adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_row
     _check(rc, "adaln_fwd_bwd_host")
 
 
+def _on(stream, call, *args):
+    """A call of the binding on `stream` (the device's current one when None).
+    What it allocates, outputs and workspaces, then belongs to that stream too:
+    the current stream's allocator could hand a workspace that this call has
+    dropped, or an output's memory, to work that is not ordered with the call."""
+    if stream is None:
+        return call(*args, None)
+    with torch.cuda.stream(stream):
+        return call(*args, stream)
+
+
 def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False, wq=None,
                       wk=None, eps=1e-6, q_out=None, k_out=None, stream=None):
     """Rotary positions of q [T, hq, dh] and k [T, hk, dh] (k may be None), after
@@ -335,8 +346,8 @@ def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False
     pos [T, axes] int32 rows of it (-1: unrotated), axis_pairs the pairs of
     each axis (P in all).  q and k may be strided views; q_out, k_out may be q, k.
     Returns (q_out, k_out), allocated contiguous when not given."""
-    return _binding.qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved, norm, wq, wk, eps, q_out,
-                                k_out, stream)
+    return _on(stream, _binding.qk_rope_fwd, q, k, table, pos, axis_pairs, interleaved, norm, wq, wk,
+               eps, q_out, k_out)
 
 
 def adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, dtype):
@@ -356,8 +367,8 @@ def adaln_qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved=True, 
     Returns (dq, dk, dwq, dwk); dwq, dwk are fp32 [dh], None without norm (and
     dk, dwk without k).  `workspace` is a uint8 CUDA tensor of at least
     adaln_qk_rope_bwd_workspace_size bytes (allocated when not given)."""
-    return _binding.qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved, norm, q, k, wq,
-                                wk, eps, dq, dk, dwq, dwk, workspace, stream)
+    return _on(stream, _binding.qk_rope_bwd, dq_out, dk_out, table, pos, axis_pairs, interleaved,
+               norm, q, k, wq, wk, eps, dq, dk, dwq, dwk, workspace)
 
 
 def adaln_ffn_saved_size(T, D, F, dtype=torch.bfloat16):
@@ -390,14 +401,15 @@ def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, wor
     act "silu", "gelu_tanh" or "gelu".  With `save` (or a `saved` buffer of
     adaln_ffn_saved_size bytes) also keeps what adaln_ffn_bwd needs.
     Returns (y, saved), saved None without."""
-    return _binding.ffn_fwd(x, wg, wu, wd, _act(act), save, y, saved, workspace, stream)
+    return _on(stream, _binding.ffn_fwd, x, wg, wu, wd, _act(act), save, y, saved, workspace)
 
 
 def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=None, dwd=None,
                   workspace=None, stream=None):
     """Backward of adaln_ffn_fwd, from its inputs and what it saved.  Returns
     (dx, dwg, dwu, dwd), all bf16."""
-    return _binding.ffn_bwd(dy, x, wg, wu, wd, saved, _act(act), dx, dwg, dwu, dwd, workspace, stream)
+    return _on(stream, _binding.ffn_bwd, dy, x, wg, wu, wd, saved, _act(act), dx, dwg, dwu, dwd,
+               workspace)
 
 
 def adaln_get_status(stream=None, device=None):

@@ -169,3 +169,34 @@ def test_calls_from_two_threads_on_two_streams(adaln):
         t.join()
     assert not wrong, wrong[:5]
     status_ok()
+
+
+def test_what_a_call_on_a_given_stream_allocates_is_that_streams(adaln):
+    """Each call on a stream that is busy, given as an argument; the current
+    stream then overwrites whatever memory its allocator has free."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+    q, dq, w = r(900, 6, 64), r(900, 6, 64), r(64)
+    table, pos = torch.randn(9, 32, 2, device="cuda", generator=g), torch.zeros(
+        900, 1, dtype=torch.int32, device="cuda")
+    x, dy, ffn = r(300, 256), r(300, 256), (r(512, 256), r(512, 256), r(256, 512))
+    saved = adaln.adaln_ffn_fwd(x, *ffn, save=True)[1]
+    calls = [lambda s: adaln.adaln_qk_rope_fwd(q, None, table, pos, (32,), norm=True, wq=w, stream=s),
+             lambda s: adaln.adaln_qk_rope_bwd(dq, None, table, pos, (32,), norm=True, q=q, wq=w,
+                                               stream=s),
+             lambda s: adaln.adaln_ffn_fwd(x, *ffn, save=True, stream=s)[:1],
+             lambda s: adaln.adaln_ffn_bwd(dy, x, *ffn, saved, stream=s)]
+    side, busy = torch.cuda.Stream(), r(4096, 4096)
+    for call in calls:
+        want = [t for t in call(None) if t is not None]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy @ busy
+        got = [t for t in call(side) if t is not None]
+        junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+                for n in (512, 4096, 1 << 17, 1 << 19, 1 << 20, 3 << 20, 8 << 20) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        del junk
+    status_ok()
