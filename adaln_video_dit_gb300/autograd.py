@@ -15,6 +15,7 @@ modulation row.  For a batch x [B, N, D] with one modulation row per sample,
 `sample_seg_ids(B, N)` gives seg_id.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -88,6 +89,7 @@ class QKNormRopeFunction(torch.autograd.Function):
         return _lib.adaln_qk_rope_fwd(q, k, table, pos, *ctx.how, wq=wq, wk=wk, eps=eps)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, wq, wk, table, pos = ctx.saved_tensors
         dq_out, dk_out = (d if d is None or d.stride(-1) == 1 else d.contiguous()
@@ -146,6 +148,7 @@ class GatedFFNFunction(torch.autograd.Function):
         return y.reshape(shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x2, wg, wu, wd, saved = ctx.saved_tensors
         dy2 = dy.reshape(x2.shape).to(x2.dtype).contiguous()

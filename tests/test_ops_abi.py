@@ -148,3 +148,23 @@ def test_gated_ffn_saves_only_for_a_gradient(lib, monkeypatch):
     m(x)
     m(x.clone().requires_grad_())
     assert asked == [True, False, False, False, True]
+
+
+def test_gradients_of_gradients_are_refused(lib, monkeypatch):
+    """The backward passes have no derivative: asking for one is an error, not a zero."""
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    monkeypatch.setattr(autograd._lib, "adaln_ffn_fwd", lambda x, *a, **kw: (x * 1, x * 1))
+    monkeypatch.setattr(autograd._lib, "adaln_ffn_bwd",
+                        lambda dy, x, wg, wu, wd, *a, **kw: (dy * x, wg * 1, wu * 1, wd * 1))
+    monkeypatch.setattr(autograd._lib, "adaln_qk_rope_fwd", lambda q, k, *a, **kw: (q * 1, None))
+    monkeypatch.setattr(autograd._lib, "adaln_qk_rope_bwd",
+                        lambda dq, dk, *a, **kw: (dq * 1, None, None, None))
+    x = torch.ones(2, 8, dtype=torch.bfloat16, requires_grad=True)
+    q = torch.ones(2, 1, 8, requires_grad=True)
+    table, pos = torch.ones(1, 4, 2), torch.zeros(2, 1, dtype=torch.int32)
+    for out, leaf in ((autograd.GatedFFN(8, 16)(x), x),
+                      (autograd.qk_norm_rope(q, None, None, None, table, pos, (4,))[0], q)):
+        first, = torch.autograd.grad((out * out).sum(), leaf, create_graph=True)
+        with pytest.raises(RuntimeError, match="twice"):
+            first.sum().backward()
