@@ -344,6 +344,14 @@ int check_heads(const adaln_heads_t* h, int heads, int64_t T, int es, int* width
   return ADALN_OK;
 }
 
+// An output's: no token or head may begin inside the one before it.
+int check_out(const adaln_heads_t* h, int heads, int64_t T, int dh, int es, int* width) {
+  const int rc = check_heads(h, heads, T, es, width);
+  if (rc != ADALN_OK || heads == 0 || T == 0) return rc;
+  const bool apart = (T <= 1 || h->token_stride >= dh) && (heads <= 1 || h->head_stride >= dh);
+  return apart ? ADALN_OK : ADALN_ERR_DIM;
+}
+
 Tensor tensor_of(const adaln_heads_t* h, int es) {
   if (!h) return Tensor{nullptr, 0, 0};
   return Tensor{static_cast<const char*>(h->ptr), h->token_stride * es, h->head_stride * es};
@@ -472,7 +480,7 @@ int adaln_qk_rope_fwd(const adaln_heads_t* q, const adaln_heads_t* k, int64_t T,
   for (int i = 0; i < rope->axes; ++i) pairs += rope->pairs[i];
   int width = width_of(dh, es, pairs, !rope->interleaved);
   if ((rc = check_heads(q, hq, T, es, &width)) || (rc = check_heads(k, hk, T, es, &width)) ||
-      (rc = check_heads(q_out, hq, T, es, &width)) || (rc = check_heads(k_out, hk, T, es, &width)))
+      (rc = check_out(q_out, hq, T, dh, es, &width)) || (rc = check_out(k_out, hk, T, dh, es, &width)))
     return rc;
   if (norm) {
     if (!std::isfinite(eps) || eps < 0.0f) return ADALN_ERR_ARG;
@@ -520,7 +528,7 @@ int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t* dk_out,
   for (int i = 0; i < rope->axes; ++i) pairs += rope->pairs[i];
   int width = width_of(dh, es, pairs, !rope->interleaved);
   if ((rc = check_heads(dq_out, hq, T, es, &width)) || (rc = check_heads(dk_out, hk, T, es, &width)) ||
-      (rc = check_heads(dq, hq, T, es, &width)) || (rc = check_heads(dk, hk, T, es, &width)))
+      (rc = check_out(dq, hq, T, dh, es, &width)) || (rc = check_out(dk, hk, T, dh, es, &width)))
     return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!norm) {

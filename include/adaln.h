@@ -267,7 +267,8 @@ typedef struct {
  *
  * Errors: ADALN_ERR_DTYPE; ADALN_ERR_DIM for T < 0, dh outside
  * [1, ADALN_MAX_HEAD_DIM], head counts outside [0, ADALN_MAX_HEADS] or both 0,
- * axes, rows or pairs out of range, or a negative stride; ADALN_ERR_NULL;
+ * axes, rows or pairs out of range, a negative stride, or an output whose
+ * tokens or heads are less than dh apart; ADALN_ERR_NULL;
  * ADALN_ERR_ALIGN for a pointer below its element's alignment; ADALN_ERR_ARG
  * for a bad eps (with norm).
  */
@@ -307,7 +308,8 @@ ADALN_API int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t
  * x, y, dy, dx [T, D]; Wg, Wu and their gradients [F, D]; Wd and its gradient
  * [D, F]; all bf16 (dtype must be ADALN_BF16), row-major and contiguous,
  * 16-byte aligned.  D and F are multiples of 8 up to ADALN_FFN_MAX_DIM, T is
- * at most ADALN_FFN_MAX_T.  Sums are fp32; the hidden product h and, in the
+ * at most ADALN_FFN_MAX_T.  Outputs, saved values and workspace may not overlap
+ * each other or an input.  Sums are fp32; the hidden product h and, in the
  * backward, the gradients of the two projections are rounded to bf16 once,
  * like the outputs.
  */

@@ -168,3 +168,19 @@ def test_gradients_of_gradients_are_refused(lib, monkeypatch):
         first, = torch.autograd.grad((out * out).sum(), leaf, create_graph=True)
         with pytest.raises(RuntimeError, match="twice"):
             first.sum().backward()
+
+
+def test_rope_outputs_that_overlap_themselves_are_refused(lib):
+    H = lib.Heads
+    for out in (H(A, 0, 128), H(A, 1024, 0), H(A, 127, 128), H(A, 1024, 127)):
+        for bad in (dict(qo=out), dict(ko=out)):
+            assert rope_fwd(lib, **bad) == lib.ADALN_ERR_DIM
+        for bad in (dict(dq=out), dict(dk=out)):
+            assert rope_bwd(lib, **bad) == lib.ADALN_ERR_DIM
+            assert rope_bwd(lib, norm=0, dwq=None, dwk=None, **bad) == lib.ADALN_ERR_DIM
+    # One token or one head has no next one, and an input may repeat (the calls
+    # below get as far as the next refusal).
+    far = dict(eps=-1.0)
+    assert rope_fwd(lib, T=1, qo=H(A, 0, 128), **far) == lib.ADALN_ERR_ARG
+    assert rope_fwd(lib, hq=1, qo=H(A, 1024, 0), **far) == lib.ADALN_ERR_ARG
+    assert rope_fwd(lib, q=H(A, 0, 128), k=H(A, 1024, 0), **far) == lib.ADALN_ERR_ARG
