@@ -344,12 +344,30 @@ int check_heads(const adaln_heads_t* h, int heads, int64_t T, int es, int* width
   return ADALN_OK;
 }
 
-// An output's: no token or head may begin inside the one before it.
+// Whether no two of [T, heads] rows of dh elements meet: neither neighbours along
+// one axis nor, where one axis's rows do not lie wholly between two of the other's,
+// any (t, h) and (t', h').  Those meet if t' - t and h - h' of the same sign bring
+// the two offsets within dh of each other, so for each distance in heads the
+// tokens on either side of it are looked at.
+bool rows_apart(int64_t T, int64_t ts, int heads, int64_t hs, int dh) {
+  if (T > 1 && ts < dh) return false;
+  if (heads > 1 && hs < dh) return false;
+  if (T <= 1 || heads <= 1) return true;
+  typedef __int128 wide;  // strides are the caller's: their products may pass 64 bits
+  if (ts >= (wide)(heads - 1) * hs + dh || hs >= (wide)(T - 1) * ts + dh) return true;
+  for (int j = 1; j < heads; ++j) {
+    const wide far = (wide)j * hs, i = far / ts;
+    if (i < T && far - i * ts < dh) return false;
+    if (i + 1 < T && (i + 1) * ts - far < dh) return false;
+  }
+  return true;
+}
+
+// An output's: its rows may not overlap each other.
 int check_out(const adaln_heads_t* h, int heads, int64_t T, int dh, int es, int* width) {
   const int rc = check_heads(h, heads, T, es, width);
   if (rc != ADALN_OK || heads == 0 || T == 0) return rc;
-  const bool apart = (T <= 1 || h->token_stride >= dh) && (heads <= 1 || h->head_stride >= dh);
-  return apart ? ADALN_OK : ADALN_ERR_DIM;
+  return rows_apart(T, h->token_stride, heads, h->head_stride, dh) ? ADALN_OK : ADALN_ERR_DIM;
 }
 
 Tensor tensor_of(const adaln_heads_t* h, int es) {

@@ -265,10 +265,10 @@ typedef struct {
  * A position outside [-1, rows) is treated as -1 and recorded in the status
  * word (ADALN_DEV_POS_RANGE).
  *
- * Errors: ADALN_ERR_DTYPE; ADALN_ERR_DIM for T < 0, dh outside
+ * Errors: ADALN_ERR_DTYPE; ADALN_ERR_DIM for T outside [0, 2^31), dh outside
  * [1, ADALN_MAX_HEAD_DIM], head counts outside [0, ADALN_MAX_HEADS] or both 0,
- * axes, rows or pairs out of range, a negative stride, or an output whose
- * tokens or heads are less than dh apart; ADALN_ERR_NULL;
+ * axes, rows or pairs out of range, a negative stride, or an output two of whose
+ * heads (of one token or of two) overlap; ADALN_ERR_NULL;
  * ADALN_ERR_ALIGN for a pointer below its element's alignment; ADALN_ERR_ARG
  * for a bad eps (with norm).
  */

@@ -184,3 +184,33 @@ def test_rope_outputs_that_overlap_themselves_are_refused(lib):
     assert rope_fwd(lib, T=1, qo=H(A, 0, 128), **far) == lib.ADALN_ERR_ARG
     assert rope_fwd(lib, hq=1, qo=H(A, 1024, 0), **far) == lib.ADALN_ERR_ARG
     assert rope_fwd(lib, q=H(A, 0, 128), k=H(A, 1024, 0), **far) == lib.ADALN_ERR_ARG
+
+
+def test_rope_outputs_that_overlap_across_both_axes_are_refused(lib):
+    """Strides that are each at least dh may still bring two heads of different
+    tokens together: every small layout, against the list of its elements."""
+    H = lib.Heads
+    for out, heads in ((H(A, 128, 128), 8), (H(A, 256, 128), 8), (H(A, 128, 256), 8),
+                       (H(A, 300, 200), 4), (H(A, 1023, 128), 8)):
+        assert rope_fwd(lib, qo=out, hq=heads) == lib.ADALN_ERR_DIM
+        assert rope_fwd(lib, ko=out, hk=heads) == lib.ADALN_ERR_DIM
+        assert rope_bwd(lib, dq=out, hq=heads) == lib.ADALN_ERR_DIM
+        assert rope_bwd(lib, norm=0, dwq=None, dwk=None, dk=out, hk=heads) == lib.ADALN_ERR_DIM
+    rope = rope_of(lib, axes=1, pairs=(1, 0, 0, 0))
+    refused = 0
+    for T in (1, 2, 3, 5):
+        for heads in (1, 2, 4):
+            for ts in range(0, 14):
+                for hs in range(0, 14):
+                    at = [t * ts + h * hs + d for t in range(T) for h in range(heads)
+                          for d in range(2)]
+                    rc = rope_fwd(lib, rope=rope, T=T, dh=2, hk=0, k=None, ko=None, hq=heads,
+                                  qo=H(A, ts, hs), eps=-1.0)  # the next refusal, if not this one
+                    meet = len(set(at)) < len(at)
+                    assert rc == (lib.ADALN_ERR_DIM if meet else lib.ADALN_ERR_ARG), (T, heads, ts, hs)
+                    refused += meet
+    assert refused > 500
+    # Strides whose products pass 64 bits.
+    big = 1 << 62
+    assert rope_fwd(lib, qo=H(A, big, big), eps=-1.0) == lib.ADALN_ERR_DIM
+    assert rope_fwd(lib, qo=H(A, 128, big), eps=-1.0) == lib.ADALN_ERR_ARG
