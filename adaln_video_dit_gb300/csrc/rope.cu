@@ -239,6 +239,12 @@ void* scalar_kernel(int mode) {
                                : (void*)rope_scalar_kernel<E, kNormBwd, PAIRS>;
 }
 
+// The most shared memory that a plan of the vector path can need: per warp two
+// sets of three groups' tokens' tables, and the weights' table.  Tokens side by
+// side in a warp times entries of a token's table are at most M x 32 (M = 4 with
+// 16-byte vectors of bf16).
+constexpr int kMostShared = 4 * 32 * (int)sizeof(float4) * (2 * kWarps * 3 + 1);
+
 struct Plan {
   int width;      // words of a vector, 0: scalar path
   int lanes;      // lanes of a head (vector path)
@@ -447,7 +453,9 @@ int run(int mode, const adaln_heads_t* const (&x)[2], const adaln_heads_t* const
         table * (2 * kWarps * p.batch + (mode == kNormFwd || mode == kNormBwd ? 1 : 0));
     smem = tables > smem ? tables : smem;
     if (smem > 48 * 1024) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      // The same value by every call: calls of other sizes that share the kernel
+      // may set it between this line and the launch (another thread's).
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
       if (e != cudaSuccess) return launch_failed(e);
     }
   } else if (dh <= 128) {

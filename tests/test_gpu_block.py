@@ -200,3 +200,71 @@ def test_what_a_call_on_a_given_stream_allocates_is_that_streams(adaln):
         assert all(torch.equal(a, b) for a, b in zip(want, got))
         del junk
     status_ok()
+
+
+TWO_THREADS = r"""
+#include <thread>
+#include "adaln.h"
+struct Call {
+  adaln_heads_t in, out;
+  int32_t heads;
+  void* stream;
+};
+// `times` forward calls of each on a thread of its own; how many were refused.
+extern "C" int two_threads(decltype(&adaln_qk_rope_fwd) fwd, const Call* calls, int64_t T, int32_t dh,
+                           const adaln_rope_t* rope, const void* w, int times) {
+  int refused[2] = {};
+  auto run = [&](int i) {
+    const Call& c = calls[i];
+    for (int n = 0; n < times; ++n)
+      refused[i] += fwd(&c.in, nullptr, T, c.heads, 0, dh, ADALN_BF16, rope, 1, w, nullptr, 1e-6f,
+                        &c.out, nullptr, c.stream) != ADALN_OK;
+  };
+  std::thread a(run, 0), b(run, 1);
+  a.join();
+  b.join();
+  return refused[0] + refused[1];
+}
+"""
+
+
+def test_calls_of_two_sizes_from_two_threads(adaln, tmp_path):
+    """Calls that share a kernel but need different amounts of shared memory (one
+    and two heads, several tokens to a warp: 98,816 and 49,664 bytes), from two
+    native threads at once (Python's would take turns): every launch is allowed
+    its own."""
+    import ctypes
+    import subprocess
+
+    (tmp_path / "two.cpp").write_text(TWO_THREADS)
+    so = str(tmp_path / "two.so")
+    subprocess.run([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-shared", "-fPIC", "-pthread",
+                    "-I" + os.path.join(ROOT, "include"), str(tmp_path / "two.cpp"), "-o", so],
+                   check=True)
+    two = ctypes.CDLL(so).two_threads
+
+    class Call(ctypes.Structure):
+        _fields_ = [("inp", adaln.Heads), ("out", adaln.Heads), ("heads", ctypes.c_int32),
+                    ("stream", ctypes.c_void_p)]
+
+    T, dh = 5000, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+    table = torch.randn(9, 64, 2, device="cuda", generator=g)
+    pos = torch.randint(-1, 9, (T, 1), device="cuda", generator=g).int()
+    w = r(dh)
+    rope = adaln.Rope(table.data_ptr(), pos.data_ptr(), 9, 1, (ctypes.c_int32 * 4)(64, 0, 0, 0), 1)
+    q = [r(T, h, dh) for h in (1, 2)]
+    out = [torch.zeros_like(t) for t in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    heads = lambda t: adaln.Heads(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    calls = (Call * 2)(*(Call(heads(a), heads(b), a.shape[1], s.cuda_stream)
+                         for a, b, s in zip(q, out, streams)))
+    want = [adaln.adaln_qk_rope_fwd(t, None, table, pos, (64,), norm=True, wq=w)[0] for t in q]
+    torch.cuda.synchronize()
+    refused = two(ctypes.cast(adaln.raw.adaln_qk_rope_fwd, ctypes.c_void_p), calls,
+                  ctypes.c_int64(T), dh, ctypes.byref(rope), ctypes.c_void_p(w.data_ptr()), 5000)
+    torch.cuda.synchronize()
+    assert refused == 0
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    status_ok()
