@@ -186,11 +186,27 @@ def _dev(t, name, dtype=None, shape=None):
     return t
 
 
+def _on(stream, call, *args):
+    """A call on `stream` (the device's current one when None), which it takes as
+    its last argument.  What it allocates, outputs and workspaces, then belongs to
+    that stream too: the current stream's allocator could hand a workspace that
+    this call has dropped, or an output's memory, to work that is not ordered with
+    the call."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
+        return call(*args, stream)
+    with torch.cuda.stream(stream):
+        return call(*args, stream)
+
+
 def adaln_fwd(x, shift, scale, seg_id, eps, y=None, mean=None, rstd=None, stream=None):
     """y = (x - mean) * rstd * (1 + scale[seg_id]) + shift[seg_id].
 
     x [T, D]; shift, scale [nseg, D] (x's dtype); seg_id int32 [T].
     Returns (y, mean, rstd); outputs are allocated when not given."""
+    return _on(stream, _adaln_fwd, x, shift, scale, seg_id, eps, y, mean, rstd)
+
+
+def _adaln_fwd(x, shift, scale, seg_id, eps, y, mean, rstd, stream):
     T, D = x.shape
     nseg = shift.shape[0]
     dt = x.dtype
@@ -222,6 +238,10 @@ def adaln_bwd(dy, x, mean, rstd, scale, seg_id, dx=None, dshift=None, dscale=Non
     """Backward of adaln_fwd.  Returns (dx [T, D] in x's dtype, dshift, dscale
     [nseg, D] fp32).  `workspace` is a uint8 CUDA tensor of at least
     adaln_bwd_workspace_size bytes (allocated when not given)."""
+    return _on(stream, _adaln_bwd, dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale, workspace)
+
+
+def _adaln_bwd(dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale, workspace, stream):
     T, D = x.shape
     nseg = scale.shape[0]
     dt = x.dtype
@@ -255,6 +275,10 @@ def adaln_bwd_noalloc(dy, x, mean, rstd, scale, seg_id, dx=None, dshift=None, ds
     (ADALN_NOALLOC_SCRATCH_BYTES per device, shared by all calls; calls that
     overlap on the GPU race).  Outputs are allocated here only when not
     given; pass them in to allocate nothing."""
+    return _on(stream, _adaln_bwd_noalloc, dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale)
+
+
+def _adaln_bwd_noalloc(dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale, stream):
     T, D = x.shape
     nseg = scale.shape[0]
     dt = x.dtype
@@ -325,17 +349,6 @@ def adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_row
                                 _ptr(scratch), scratch.numel() * scratch.element_size(),
                                 _stream_ptr(stream, scratch.device))
     _check(rc, "adaln_fwd_bwd_host")
-
-
-def _on(stream, call, *args):
-    """A call of the binding on `stream` (the device's current one when None).
-    What it allocates, outputs and workspaces, then belongs to that stream too:
-    the current stream's allocator could hand a workspace that this call has
-    dropped, or an output's memory, to work that is not ordered with the call."""
-    if stream is None:
-        return call(*args, None)
-    with torch.cuda.stream(stream):
-        return call(*args, stream)
 
 
 def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False, wq=None,
