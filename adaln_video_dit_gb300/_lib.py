@@ -3,8 +3,9 @@
 Argument marshalling only (for the rotary and feed-forward calls in the compiled
 _binding, csrc/binding.cpp): every step of the operators runs in the library's
 CUDA kernels.  torch supplies device memory, streams and output allocation.
-The functions carry the C names.  There is no fallback: if libadaln.so is
-missing or a call fails, an exception is raised.
+The functions carry the C names and run on their tensors' device, whichever is
+current.  There is no fallback: if libadaln.so is missing or a call fails, an
+exception is raised.
 """
 import ctypes
 import os
@@ -174,9 +175,10 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
-def _dev(t, name, dtype=None, shape=None):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _dev(t, name, dtype=None, shape=None, device=None):
+    if not t.is_cuda if device is None else t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else
+                         f"{name} must be on cuda:{device}, not cuda:{t.get_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -186,15 +188,29 @@ def _dev(t, name, dtype=None, shape=None):
     return t
 
 
-def _on(stream, call, *args):
-    """A call on `stream` (the device's current one when None), which it takes as
-    its last argument.  What it allocates, outputs and workspaces, then belongs to
-    that stream too: the current stream's allocator could hand a workspace that
-    this call has dropped, or an output's memory, to work that is not ordered with
-    the call."""
-    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
+def _on(t, stream, call, *args):
+    """A call on tensor t's device and on `stream` (that device's current one when
+    None), which it takes as its last argument.
+
+    The library plans for and launches on the current device, so t's is made
+    current: the default stream has the same handle on every device, and a launch
+    on it from another one would run there, with t's addresses.
+
+    What the call allocates, outputs and workspaces, belongs to its stream too:
+    the current stream's allocator could hand a workspace that this call has
+    dropped, or an output's memory, to work that is not ordered with the call."""
+    index = t.get_device()
+    if index < 0:  # not a CUDA tensor, which the call refuses by name
         return call(*args, stream)
-    with torch.cuda.stream(stream):
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"the stream is cuda:{stream.device_index}'s, the tensors are on cuda:{index}")
+    if index == torch._C._cuda_getDevice():
+        if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(index):
+            return call(*args, stream)
+    elif stream is None:
+        with torch.cuda.device(index):
+            return call(*args, stream)
+    with torch.cuda.stream(stream):  # (makes its device current as well)
         return call(*args, stream)
 
 
@@ -203,20 +219,20 @@ def adaln_fwd(x, shift, scale, seg_id, eps, y=None, mean=None, rstd=None, stream
 
     x [T, D]; shift, scale [nseg, D] (x's dtype); seg_id int32 [T].
     Returns (y, mean, rstd); outputs are allocated when not given."""
-    return _on(stream, _adaln_fwd, x, shift, scale, seg_id, eps, y, mean, rstd)
+    return _on(x, stream, _adaln_fwd, x, shift, scale, seg_id, eps, y, mean, rstd)
 
 
 def _adaln_fwd(x, shift, scale, seg_id, eps, y, mean, rstd, stream):
     T, D = x.shape
     nseg = shift.shape[0]
-    dt = x.dtype
+    dt, dev = x.dtype, x.get_device()
     _dev(x, "x", dt)
-    _dev(shift, "shift", dt, (nseg, D))
-    _dev(scale, "scale", dt, (nseg, D))
-    _dev(seg_id, "seg_id", torch.int32, (T,))
-    y = torch.empty_like(x) if y is None else _dev(y, "y", dt, (T, D))
-    mean = torch.empty(T, device=x.device, dtype=torch.float32) if mean is None else _dev(mean, "mean", torch.float32, (T,))
-    rstd = torch.empty(T, device=x.device, dtype=torch.float32) if rstd is None else _dev(rstd, "rstd", torch.float32, (T,))
+    _dev(shift, "shift", dt, (nseg, D), dev)
+    _dev(scale, "scale", dt, (nseg, D), dev)
+    _dev(seg_id, "seg_id", torch.int32, (T,), dev)
+    y = torch.empty_like(x) if y is None else _dev(y, "y", dt, (T, D), dev)
+    mean = torch.empty(T, device=x.device, dtype=torch.float32) if mean is None else _dev(mean, "mean", torch.float32, (T,), dev)
+    rstd = torch.empty(T, device=x.device, dtype=torch.float32) if rstd is None else _dev(rstd, "rstd", torch.float32, (T,), dev)
     rc = raw.adaln_fwd(_ptr(x), _ptr(shift), _ptr(scale), _ptr(seg_id), T, D, nseg,
                        dtype_code(dt), float(eps), _ptr(y), _ptr(mean), _ptr(rstd),
                        _stream_ptr(stream, x.device))
@@ -238,28 +254,28 @@ def adaln_bwd(dy, x, mean, rstd, scale, seg_id, dx=None, dshift=None, dscale=Non
     """Backward of adaln_fwd.  Returns (dx [T, D] in x's dtype, dshift, dscale
     [nseg, D] fp32).  `workspace` is a uint8 CUDA tensor of at least
     adaln_bwd_workspace_size bytes (allocated when not given)."""
-    return _on(stream, _adaln_bwd, dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale, workspace)
+    return _on(x, stream, _adaln_bwd, dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale, workspace)
 
 
 def _adaln_bwd(dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale, workspace, stream):
     T, D = x.shape
     nseg = scale.shape[0]
-    dt = x.dtype
-    _dev(dy, "dy", dt, (T, D))
+    dt, dev = x.dtype, x.get_device()
+    _dev(dy, "dy", dt, (T, D), dev)
     _dev(x, "x", dt)
-    _dev(mean, "mean", torch.float32, (T,))
-    _dev(rstd, "rstd", torch.float32, (T,))
-    _dev(scale, "scale", dt, (nseg, D))
-    _dev(seg_id, "seg_id", torch.int32, (T,))
-    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", dt, (T, D))
+    _dev(mean, "mean", torch.float32, (T,), dev)
+    _dev(rstd, "rstd", torch.float32, (T,), dev)
+    _dev(scale, "scale", dt, (nseg, D), dev)
+    _dev(seg_id, "seg_id", torch.int32, (T,), dev)
+    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", dt, (T, D), dev)
     dshift = (torch.empty(nseg, D, device=x.device, dtype=torch.float32) if dshift is None
-              else _dev(dshift, "dshift", torch.float32, (nseg, D)))
+              else _dev(dshift, "dshift", torch.float32, (nseg, D), dev))
     dscale = (torch.empty(nseg, D, device=x.device, dtype=torch.float32) if dscale is None
-              else _dev(dscale, "dscale", torch.float32, (nseg, D)))
+              else _dev(dscale, "dscale", torch.float32, (nseg, D), dev))
     need = adaln_bwd_workspace_size(T, D, nseg, dt)
     if workspace is None:
         workspace = torch.empty(max(need, 16), device=x.device, dtype=torch.uint8)
-    _dev(workspace, "workspace")
+    _dev(workspace, "workspace", device=dev)
     rc = raw.adaln_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(scale), _ptr(seg_id),
                        T, D, nseg, dtype_code(dt), _ptr(dx), _ptr(dshift), _ptr(dscale),
                        _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -275,24 +291,24 @@ def adaln_bwd_noalloc(dy, x, mean, rstd, scale, seg_id, dx=None, dshift=None, ds
     (ADALN_NOALLOC_SCRATCH_BYTES per device, shared by all calls; calls that
     overlap on the GPU race).  Outputs are allocated here only when not
     given; pass them in to allocate nothing."""
-    return _on(stream, _adaln_bwd_noalloc, dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale)
+    return _on(x, stream, _adaln_bwd_noalloc, dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale)
 
 
 def _adaln_bwd_noalloc(dy, x, mean, rstd, scale, seg_id, dx, dshift, dscale, stream):
     T, D = x.shape
     nseg = scale.shape[0]
-    dt = x.dtype
-    _dev(dy, "dy", dt, (T, D))
+    dt, dev = x.dtype, x.get_device()
+    _dev(dy, "dy", dt, (T, D), dev)
     _dev(x, "x", dt)
-    _dev(mean, "mean", torch.float32, (T,))
-    _dev(rstd, "rstd", torch.float32, (T,))
-    _dev(scale, "scale", dt, (nseg, D))
-    _dev(seg_id, "seg_id", torch.int32, (T,))
-    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", dt, (T, D))
+    _dev(mean, "mean", torch.float32, (T,), dev)
+    _dev(rstd, "rstd", torch.float32, (T,), dev)
+    _dev(scale, "scale", dt, (nseg, D), dev)
+    _dev(seg_id, "seg_id", torch.int32, (T,), dev)
+    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", dt, (T, D), dev)
     dshift = (torch.empty(nseg, D, device=x.device, dtype=torch.float32) if dshift is None
-              else _dev(dshift, "dshift", torch.float32, (nseg, D)))
+              else _dev(dshift, "dshift", torch.float32, (nseg, D), dev))
     dscale = (torch.empty(nseg, D, device=x.device, dtype=torch.float32) if dscale is None
-              else _dev(dscale, "dscale", torch.float32, (nseg, D)))
+              else _dev(dscale, "dscale", torch.float32, (nseg, D), dev))
     rc = raw.adaln_bwd_noalloc(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(scale),
                                _ptr(seg_id), T, D, nseg, dtype_code(dt), _ptr(dx),
                                _ptr(dshift), _ptr(dscale), _stream_ptr(stream, x.device))
@@ -326,7 +342,13 @@ def adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_row
     """Forward + backward on host tensors (pinned for overlap), pipelined in row
     chunks.  `out` is a dict of preallocated host tensors y, mean, rstd, dx,
     dshift, dscale; `scratch` a uint8 CUDA tensor of at least
-    adaln_fwd_bwd_host_scratch_size bytes.  Asynchronous on `stream`."""
+    adaln_fwd_bwd_host_scratch_size bytes.  Runs on the scratch's device,
+    asynchronously on `stream`."""
+    _on(scratch, stream, _adaln_fwd_bwd_host, x, dy, shift, scale, seg_id, eps, out, scratch,
+        chunk_rows)
+
+
+def _adaln_fwd_bwd_host(x, dy, shift, scale, seg_id, eps, out, scratch, chunk_rows, stream):
     T, D = x.shape
     nseg = shift.shape[0]
     dt = x.dtype
@@ -359,12 +381,13 @@ def adaln_qk_rope_fwd(q, k, table, pos, axis_pairs, interleaved=True, norm=False
     pos [T, axes] int32 rows of it (-1: unrotated), axis_pairs the pairs of
     each axis (P in all).  q and k may be strided views; q_out, k_out may be q, k.
     Returns (q_out, k_out), allocated contiguous when not given."""
-    return _on(stream, _binding.qk_rope_fwd, q, k, table, pos, axis_pairs, interleaved, norm, wq, wk,
+    return _on(q, stream, _binding.qk_rope_fwd, q, k, table, pos, axis_pairs, interleaved, norm, wq, wk,
                eps, q_out, k_out)
 
 
 def adaln_qk_rope_bwd_workspace_size(T, hq, hk, dh, dtype):
-    """Workspace bytes adaln_qk_rope_bwd needs for the weights' gradients."""
+    """Workspace bytes adaln_qk_rope_bwd needs for the weights' gradients on the
+    current device."""
     n = ctypes.c_size_t(0)
     code = dtype if isinstance(dtype, int) else dtype_code(dtype)
     _check(raw.adaln_qk_rope_bwd_workspace_size(int(T), int(hq), int(hk), int(dh), code,
@@ -380,7 +403,7 @@ def adaln_qk_rope_bwd(dq_out, dk_out, table, pos, axis_pairs, interleaved=True, 
     Returns (dq, dk, dwq, dwk); dwq, dwk are fp32 [dh], None without norm (and
     dk, dwk without k).  `workspace` is a uint8 CUDA tensor of at least
     adaln_qk_rope_bwd_workspace_size bytes (allocated when not given)."""
-    return _on(stream, _binding.qk_rope_bwd, dq_out, dk_out, table, pos, axis_pairs, interleaved,
+    return _on(dq_out, stream, _binding.qk_rope_bwd, dq_out, dk_out, table, pos, axis_pairs, interleaved,
                norm, q, k, wq, wk, eps, dq, dk, dwq, dwk, workspace)
 
 
@@ -414,23 +437,28 @@ def adaln_ffn_fwd(x, wg, wu, wd, act="silu", save=False, y=None, saved=None, wor
     act "silu", "gelu_tanh" or "gelu".  With `save` (or a `saved` buffer of
     adaln_ffn_saved_size bytes) also keeps what adaln_ffn_bwd needs.
     Returns (y, saved), saved None without."""
-    return _on(stream, _binding.ffn_fwd, x, wg, wu, wd, _act(act), save, y, saved, workspace)
+    return _on(x, stream, _binding.ffn_fwd, x, wg, wu, wd, _act(act), save, y, saved, workspace)
 
 
 def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=None, dwd=None,
                   workspace=None, stream=None):
     """Backward of adaln_ffn_fwd, from its inputs and what it saved.  Returns
     (dx, dwg, dwu, dwd), all bf16."""
-    return _on(stream, _binding.ffn_bwd, dy, x, wg, wu, wd, saved, _act(act), dx, dwg, dwu, dwd,
+    return _on(x, stream, _binding.ffn_bwd, dy, x, wg, wu, wd, saved, _act(act), dx, dwg, dwu, dwd,
                workspace)
 
 
 def adaln_get_status(stream=None, device=None):
-    """Synchronise the stream, read and clear the device status word.
-    Returns (code, bits)."""
+    """Synchronise the stream, read and clear the status word of the device (the
+    stream's, or else the current one).  Returns (code, bits)."""
     bits = ctypes.c_uint32(0)
-    dev = device if device is not None else torch.cuda.current_device()
-    rc = raw.adaln_get_status(ctypes.byref(bits), _stream_ptr(stream, dev))
+    if device is None:
+        device = stream.device if stream is not None else torch.cuda.current_device()
+    with torch.cuda.device(device):
+        dev = torch.cuda.current_device()
+        if stream is not None and stream.device_index != dev:
+            raise ValueError(f"the stream is cuda:{stream.device_index}'s, not cuda:{dev}'s")
+        rc = raw.adaln_get_status(ctypes.byref(bits), _stream_ptr(stream, dev))
     return rc, bits.value
 
 

@@ -21,7 +21,8 @@ def lib(monkeypatch):
         log.append((what, current.device, current.stream[current.device]))
 
     @contextlib.contextmanager
-    def on_device(index):
+    def on_device(device):
+        index = device if isinstance(device, int) else device.index
         before, current.device = current.device, index
         yield
         current.device = before
@@ -83,6 +84,13 @@ class Tensor:
         return 1
 
 
+class Host(Tensor):
+    is_cuda = False
+
+    def __init__(self, *shape, dtype=None):
+        super().__init__(*shape, dtype=dtype or torch.float32)
+
+
 def adaln_calls(L, device=0, **kw):
     """Every AdaLN call, its outputs and workspace to be allocated."""
     x, m, v = (Tensor(*s, device=device) for s in ((6, 8), (2, 8), (6,)))
@@ -109,3 +117,46 @@ def test_a_call_on_a_given_stream_allocates_there(lib):
         assert (name, 0, 77) in whats and all(e[1:] == (0, 77) for e in whats), (name, lib.log)
         if name.startswith("adaln"):
             assert ("empty", 0, 77) in whats and ("stream", 77) in lib.log
+
+
+def test_a_call_runs_on_its_tensors_device(lib):
+    """With cuda:0 current, calls on cuda:1 (on its current stream, whose handle is
+    the same 0, or on a given one) allocate, size and launch on cuda:1."""
+    s = SimpleNamespace(cuda_stream=77, device_index=1, device=torch.device("cuda", 1))
+    for kw, stream in (({}, 0), ({"stream": s}, 77)):
+        for name, call in {**adaln_calls(lib, 1, **kw), **other_calls(lib, 1, **kw)}.items():
+            lib.log.clear()
+            call()
+            whats = [e for e in lib.log if e[0] != "stream"]
+            assert (name, 1, stream) in whats and all(e[1:] == (1, stream) for e in whats), (name, lib.log)
+            assert lib.torch.cuda.current_device() == 0
+    host = {n: Host(*s, dtype=d) for n, s, d in (
+        ("x", (6, 8), None), ("y", (6, 8), None), ("dx", (6, 8), None), ("mean", (6,), None),
+        ("rstd", (6,), None), ("dshift", (2, 8), None), ("dscale", (2, 8), None),
+        ("seg", (6,), torch.int32))}
+    lib.log.clear()
+    lib.adaln_fwd_bwd_host(host["x"], host["x"], host["dshift"], host["dshift"], host["seg"], 1e-6, host,
+                           Tensor(1, dtype=torch.uint8, device=1))
+    assert lib.log[0] == ("adaln_fwd_bwd_host", 1, 0)
+    for kw in (dict(device=1), dict(device=torch.device("cuda", 1)), dict(stream=s)):
+        lib.log.clear()
+        lib.adaln_get_status(**kw)
+        assert lib.log[0] == ("adaln_get_status", 1, 0) and lib.torch.cuda.current_device() == 0
+
+
+def test_tensors_and_streams_of_two_devices_are_refused(lib):
+    s = SimpleNamespace(cuda_stream=77, device_index=1, device=torch.device("cuda", 1))
+    for name, call in {**adaln_calls(lib, 0, stream=s), **other_calls(lib, 0, stream=s)}.items():
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    x, m = Tensor(6, 8), Tensor(2, 8)
+    seg, far = Tensor(6, dtype=torch.int32), Tensor(2, 8, device=1)
+    v, w = Tensor(6), Tensor(6, device=1)
+    for call in (lambda: lib.adaln_fwd(x, m, far, seg, 1e-6), lambda: lib.adaln_fwd(x, m, m, seg, 1e-6, mean=w),
+                 lambda: lib.adaln_bwd(x, x, w, v, m, seg), lambda: lib.adaln_bwd(x, x, v, v, far, seg),
+                 lambda: lib.adaln_bwd(x, x, v, v, m, seg, workspace=far),
+                 lambda: lib.adaln_bwd_noalloc(x, x, v, v, m, seg, dshift=far),
+                 lambda: lib.adaln_get_status(stream=s, device=0)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    assert not [e for e in lib.log if e[0] in lib.EXPORTS and "size" not in e[0]]
