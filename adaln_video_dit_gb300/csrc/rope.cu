@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_cons
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sh += __shfl_xor_sync(~0u, sh, o);
-        const float k = -r * r * r * (sh * a.inv_dh);
+        const float k = -(sh * a.inv_dh * r) * r * r;  // (r^3 alone may overflow)
 #pragma unroll
         for (int i = 0; i < kScalarPairs; ++i) {
           if (da[i] >= 0) dwa[i] = fmaf(ga[i], fa[i] * r, dwa[i]);

@@ -470,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             sx = head_sum<P>(sx, lane, j);
             sh = head_sum<P>(sh, lane, j);
             const float r = rsqrtf(fmaf(sx, a.inv_dh, a.eps));
-            const float2 k = splat2(-r * r * r * (sh * a.inv_dh)), r2 = splat2(r);
+            // (In this order: r^3 alone may overflow.)
+            const float2 k = splat2(-(sh * a.inv_dh * r) * r * r), r2 = splat2(r);
             // Lanes without a head hold zeros, so they add nothing to dw (g = 0)
             // as long as r is finite; eps = 0 would make it 0 * inf.
             const float2 rd = splat2(in ? r : 0.0f);

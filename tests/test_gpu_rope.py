@@ -391,3 +391,27 @@ def test_binding_refuses(adaln):
         adaln.adaln_qk_rope_bwd(q, None, tb, ps, axis_pairs=(32,), norm=True, q=q,
                                 workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.code == adaln.ADALN_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("dh,rot", [(64, 64), (80, 40), (37, 20), (200, 100)])
+def test_heads_of_tiny_values_without_eps(adaln, dh, rot):
+    """eps = 0 and heads of rms 1e-17 to 1e-9: r^3 passes the largest fp32 where the
+    gradients, of order r, do not.  The squares of the smallest are still normal."""
+    T, h, axes, inter = 40, 4, 2, dh % 3 == 1
+    close.bf16 = False
+    pairs, rows = split(rot // 2, axes), 9
+    table, pos = table_of(rows, rot // 2), positions(T, axes, rows, 2)
+    cos, sin = rotation(table, pos, pairs)
+    g = torch.Generator().manual_seed(dh)
+    rms = torch.tensor([1e-17, 1e-13, 1e-11, 1e-9])[:, None]
+    x, dy = torch.randn(T, h, dh, generator=g) * rms, torch.randn(T, h, dh, generator=g)
+    w = 1 + 0.3 * torch.randn(dh, generator=g)
+    how = dict(axis_pairs=pairs, interleaved=inter, norm=True, wq=w.cuda(), eps=0.0)
+    tb, ps = table.cuda(), pos.cuda()
+    out, _ = adaln.adaln_qk_rope_fwd(x.cuda(), None, tb, ps, **how)
+    dq, _, dw, _ = adaln.adaln_qk_rope_bwd(dy.cuda(), None, tb, ps, q=x.cuda(), **how)
+    ref = reference(x, w, dy, cos, sin, inter, True, 0.0)
+    close(out, ref["y"], ref["ys"], 64, "out")
+    close(dq, ref["dx"], ref["dxs"], 128, "dq")
+    close(dw, ref["dw"], ref["dws"], 80, "dw")
+    status_ok()
