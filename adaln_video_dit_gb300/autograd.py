@@ -96,8 +96,9 @@ class QKNormRopeFunction(torch.autograd.Function):
                           for d in (dq_out, dk_out))
         dq, dk, dwq, dwk = _lib.adaln_qk_rope_bwd(dq_out, dk_out, table, pos, *ctx.how, q=q, k=k,
                                                   wq=wq, wk=wk, eps=ctx.eps)
+        # (The keys' weight has no gradient where there are no keys.)
         return (dq, dk, dwq.to(wq.dtype) if wq is not None else None,
-                dwk.to(wk.dtype) if wk is not None else None) + (None,) * 6
+                dwk.to(wk.dtype) if wk is not None and dwk is not None else None) + (None,) * 6
 
 
 def qk_rope(q, k, table, pos, axis_pairs, interleaved=True):

@@ -214,3 +214,20 @@ def test_rope_outputs_that_overlap_across_both_axes_are_refused(lib):
     big = 1 << 62
     assert rope_fwd(lib, qo=H(A, big, big), eps=-1.0) == lib.ADALN_ERR_DIM
     assert rope_fwd(lib, qo=H(A, 128, big), eps=-1.0) == lib.ADALN_ERR_ARG
+
+
+def test_norm_of_queries_alone_has_a_backward(lib, monkeypatch):
+    """Without keys (a cross attention's queries) the keys' weight, which QKNormRope
+    holds all the same, is not used: it has no gradient, and the backward runs."""
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    monkeypatch.setattr(autograd._lib, "adaln_qk_rope_fwd", lambda q, k, *a, **kw: (q * 1, None))
+    monkeypatch.setattr(autograd._lib, "adaln_qk_rope_bwd",
+                        lambda dq, dk, *a, **kw: (dq * 1, None, torch.full((8,), 3.0), None))
+    m = autograd.QKNormRope(8, (4,))
+    q = torch.ones(2, 1, 8, requires_grad=True)
+    out, none = m(q, None, torch.ones(1, 4, 2), torch.zeros(2, 1, dtype=torch.int32))
+    assert none is None
+    out.sum().backward()
+    assert torch.equal(q.grad, torch.ones_like(q))
+    assert torch.equal(m.wq.grad, torch.full((8,), 3.0)) and m.wk.grad is None
