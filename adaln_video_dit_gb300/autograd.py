@@ -43,6 +43,7 @@ class AdaLNModulateFunction(torch.autograd.Function):
         return y.reshape(shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x2, mean, rstd, scale, seg_id = ctx.saved_tensors
         dy2 = dy.reshape(x2.shape)

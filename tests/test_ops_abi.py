@@ -231,3 +231,18 @@ def test_norm_of_queries_alone_has_a_backward(lib, monkeypatch):
     out.sum().backward()
     assert torch.equal(q.grad, torch.ones_like(q))
     assert torch.equal(m.wq.grad, torch.full((8,), 3.0)) and m.wk.grad is None
+
+
+def test_gradients_of_the_modulations_gradients_are_refused(lib, monkeypatch):
+    """The AdaLN's backward has no derivative either."""
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    monkeypatch.setattr(autograd._lib, "adaln_fwd", lambda x, *a: (x * 1, x[:, 0] * 1, x[:, 0] * 1))
+    monkeypatch.setattr(autograd._lib, "adaln_bwd",
+                        lambda dy, x, mean, rstd, scale, seg: (dy * x, scale * 1, scale * 1))
+    x = torch.ones(2, 8, requires_grad=True)
+    m, seg = torch.zeros(1, 8, requires_grad=True), torch.zeros(2, dtype=torch.int32)
+    out = autograd.adaln_modulate(x, m, m, seg)
+    first, = torch.autograd.grad((out * out).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="twice"):
+        first.sum().backward()
