@@ -511,7 +511,6 @@ int adaln_qk_rope_fwd(const adaln_heads_t* q, const adaln_heads_t* k, int64_t T,
   if (norm) {
     if (!std::isfinite(eps) || eps < 0.0f) return ADALN_ERR_ARG;
     if (!aligned_to(wq, es) || !aligned_to(wk, es)) return ADALN_ERR_ALIGN;
-    if (!aligned_to(wq, 16) || !aligned_to(wk, 16)) width = 0;
   }
   if (T == 0) return ADALN_OK;
   return run(norm ? kNormFwd : kRotate, {q, k}, {nullptr, nullptr}, {q_out, k_out}, T, {hq, hk},
@@ -568,7 +567,6 @@ int adaln_qk_rope_bwd(const adaln_heads_t* dq_out, const adaln_heads_t* dk_out,
   if (!std::isfinite(eps) || eps < 0.0f) return ADALN_ERR_ARG;
   if (!aligned_to(wq, es) || !aligned_to(wk, es) || !aligned_to(dwq, 4) || !aligned_to(dwk, 4))
     return ADALN_ERR_ALIGN;
-  if (!aligned_to(wq, 16) || !aligned_to(wk, 16)) width = 0;
   if ((dwq || dwk) && !workspace) return ADALN_ERR_NULL;
   if (!aligned_to(workspace, 16)) return ADALN_ERR_ALIGN;
   if (T == 0 && !dwq && !dwk) return ADALN_OK;

@@ -415,3 +415,24 @@ def test_heads_of_tiny_values_without_eps(adaln, dh, rot):
     close(dq, ref["dx"], ref["dxs"], 128, "dq")
     close(dw, ref["dw"], ref["dws"], 80, "dw")
     status_ok()
+
+
+@pytest.mark.parametrize("dt,dh,hk", [(torch.bfloat16, 128, 2), (torch.bfloat16, 72, 2),
+                                      (torch.float32, 64, 1), (torch.float32, 80, 3)])
+@pytest.mark.parametrize("T", [40, 6000])
+def test_weights_at_element_alignment_take_the_same_path(adaln, dt, dh, hk, T):
+    """Weights in the middle of a flat parameter buffer: the same bits as aligned
+    ones (the scalar path would round in another order)."""
+    g = torch.Generator(device="cuda").manual_seed(T + dh)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).to(dt)  # noqa: E731
+    q, k, dq, dk = r(T, 3, dh), r(T, hk, dh), r(T, 3, dh), r(T, hk, dh)
+    flat = r(2 * dh + 1)
+    wq, wk = flat[1:dh + 1], flat[dh + 1:]
+    assert wq.data_ptr() % 16 and wk.data_ptr() % flat.element_size() == 0
+    tb, ps = table_of(9, dh // 2).cuda(), positions(T, 3, 9, 2).cuda()
+    for inter in (True, False):
+        got, want = ([*adaln.adaln_qk_rope_fwd(q, k, tb, ps, split(dh // 2, 3), inter, True, *w),
+                      *adaln.adaln_qk_rope_bwd(dq, dk, tb, ps, split(dh // 2, 3), inter, True, q, k, *w)]
+                     for w in ((wq, wk), (wq.clone(), wk.clone())))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    status_ok()
