@@ -12,7 +12,8 @@ instead keeps the normalised activations and the gathered (1 + scale) rows.
 Layout: x is [..., D] (flattened to tokens [T, D]); shift and scale are
 [nseg, D]; seg_id is int32 [T], non-decreasing, mapping each token to its
 modulation row.  For a batch x [B, N, D] with one modulation row per sample,
-`sample_seg_ids(B, N)` gives seg_id.
+`sample_seg_ids(B, N)` gives seg_id.  The other operators' tensors may have any
+leading dimensions as well.
 """
 import torch
 from torch.autograd.function import once_differentiable
@@ -102,21 +103,35 @@ class QKNormRopeFunction(torch.autograd.Function):
                 dwk.to(wk.dtype) if wk is not None and dwk is not None else None) + (None,) * 6
 
 
+def _by_token(q, k, wq, wk, table, pos, *how):
+    """The node on tokens [T, heads, dh], from any leading dimensions and back."""
+    if q.dim() == 3 and pos.dim() == 2:
+        return QKNormRopeFunction.apply(q, k, wq, wk, table, pos, *how)
+
+    def flat(x):
+        return x.reshape(-1, *x.shape[-2:]) if x is not None else None
+
+    qo, ko = QKNormRopeFunction.apply(flat(q), flat(k), wq, wk, table, pos.reshape(-1, pos.shape[-1]),
+                                      *how)
+    return qo.reshape(q.shape), ko.reshape(k.shape) if k is not None else None
+
+
 def qk_rope(q, k, table, pos, axis_pairs, interleaved=True):
-    """Rotary positions of q [T, hq, dh] and k [T, hk, dh] (differentiable)."""
-    return QKNormRopeFunction.apply(q, k, None, None, table, pos, axis_pairs, interleaved, False,
-                                    0.0)
+    """Rotary positions of q [..., hq, dh] and k [..., hk, dh] (or None) with pos
+    [..., axes], flattened to tokens (differentiable)."""
+    return _by_token(q, k, None, None, table, pos, axis_pairs, interleaved, False, 0.0)
 
 
 def qk_norm_rope(q, k, wq, wk, table, pos, axis_pairs, interleaved=True, eps=1e-6):
-    """RMS norm of every head (weights wq, wk [dh], or None for ones), then the
-    rotary positions, in one pass (differentiable in q, k, wq, wk)."""
-    return QKNormRopeFunction.apply(q, k, wq, wk, table, pos, axis_pairs, interleaved, True,
-                                    float(eps))
+    """RMS norm of every head (weights wq, wk [dh] in q's dtype, or None for ones),
+    then the rotary positions, in one pass (differentiable in q, k, wq, wk); shapes
+    as for qk_rope."""
+    return _by_token(q, k, wq, wk, table, pos, axis_pairs, interleaved, True, float(eps))
 
 
 class QKNormRope(torch.nn.Module):
-    """Module form: holds the two weights; forward(q, k, table, pos) -> (q, k)."""
+    """Module form: holds the two weights, in the queries' and keys' dtype;
+    forward(q, k, table, pos) -> (q, k)."""
 
     def __init__(self, head_dim, axis_pairs, interleaved=True, eps=1e-6, device=None, dtype=None):
         super().__init__()

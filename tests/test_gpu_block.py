@@ -268,3 +268,24 @@ def test_calls_of_two_sizes_from_two_threads(adaln, tmp_path):
     assert refused == 0
     assert all(torch.equal(a, b) for a, b in zip(out, want))
     status_ok()
+
+
+def test_rotary_nodes_take_leading_dimensions(adaln):
+    from adaln_video_dit_gb300 import autograd as A
+    from adaln_video_dit_gb300 import rotary
+    B, N, h, dh = 3, 48, 2, 64
+    qkv = torch.randn(B, N, 3, h, dh, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(dh, device="cuda", dtype=torch.bfloat16)
+    pairs = rotary.split_pairs(dh // 2)
+    table = rotary.rope_table(10, pairs, device="cuda")
+    pos = rotary.grid_positions([(0, 2, 4, 6)] * B, device="cuda")
+    results = []
+    for shape, p in (((B, N, 3, h, dh), pos.view(B, N, 3)), ((B * N, 3, h, dh), pos)):
+        x = qkv.clone().view(shape).requires_grad_()
+        q, k, _ = x.unbind(-3)
+        qo, ko = A.qk_norm_rope(q, k, w, w, table, p, pairs)
+        assert qo.shape == q.shape and ko.shape == k.shape
+        (qo.float().square().sum() + ko.float().sum()).backward()
+        results.append([t.reshape(-1) for t in (qo, ko, x.grad)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    status_ok()

@@ -246,3 +246,30 @@ def test_gradients_of_the_modulations_gradients_are_refused(lib, monkeypatch):
     first, = torch.autograd.grad((out * out).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="twice"):
         first.sum().backward()
+
+
+def test_rotary_nodes_take_leading_dimensions(lib, monkeypatch):
+    """[..., heads, dh] with pos [..., axes], as the other nodes take [..., D]: the
+    call gets tokens, a packed projection's views without a copy."""
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    seen = []
+
+    def fwd(q, k, table, pos, *how, **kw):
+        seen.append((q.shape, q.stride(), q.data_ptr(), k if k is None else k.shape, pos.shape))
+        return q * 2, None if k is None else k * 3
+
+    monkeypatch.setattr(autograd._lib, "adaln_qk_rope_fwd", fwd)
+    monkeypatch.setattr(autograd._lib, "adaln_qk_rope_bwd", lambda dq, dk, *a, **kw: (
+        dq * 2, None if dk is None else dk * 3, None, None))
+    qkv = torch.randn(2, 5, 3, 4, 8, requires_grad=True)
+    q, k, _ = qkv.unbind(2)
+    table, pos = torch.ones(1, 4, 2), torch.zeros(2, 5, 1, dtype=torch.int32)
+    qo, ko = autograd.qk_norm_rope(q, k, None, None, table, pos, (4,))
+    assert seen == [((10, 4, 8), (96, 8, 1), qkv.data_ptr(), (10, 4, 8), (10, 1))]
+    assert torch.equal(qo, 2 * q) and torch.equal(ko, 3 * k)
+    (qo.sum() + ko.sum()).backward()
+    assert torch.equal(qkv.grad[:, :, 0], torch.full((2, 5, 4, 8), 2.0))
+    assert torch.equal(qkv.grad[:, :, 1], torch.full((2, 5, 4, 8), 3.0))
+    out, none = autograd.qk_rope(q[0, 0], None, table, pos[0, 0], (4,))  # one token's heads
+    assert none is None and out.shape == (4, 8) and seen[-1][0] == (1, 4, 8)
