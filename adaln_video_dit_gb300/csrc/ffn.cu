@@ -825,14 +825,15 @@ cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, int worth, cu
   });
 }
 
-cudaError_t launch_join(const Problem& p, void* to, cudaStream_t st) {
+cudaError_t launch_join(const Problem& p, void* to, int pairs, cudaStream_t st) {
   const float* partial = p.partial;
   int splits = p.s.splits;
   int64_t vecs = (int64_t)p.s.M * p.s.N / 4;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(to);
   void* params[4] = {&partial, &splits, &vecs, &out};
   const int64_t blocks = (vecs + 255) / 256;
-  const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
+  const int most = 2 * pairs * 8;  // resident at 256 threads: eight an SM
+  const int grid = (int)(blocks < most ? blocks : most);
   return traced_launch(ADALN_KERNEL_FFN, st, [&] {
     return launch_cluster((void*)ffn_join_kernel, grid, 256, 0, 1, params, st);
   });
@@ -950,7 +951,7 @@ int adaln_ffn_fwd(const void* x, const void* wg, const void* wu, const void* wd,
                   F, 0, y);
   a.p[0].partial = reinterpret_cast<float*>(ws + round256((size_t)T * F * 2));
   if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, 0, st);
-  if (e == cudaSuccess && plan.y.splits > 1) e = launch_join(a.p[0], y, st);
+  if (e == cudaSuccess && plan.y.splits > 1) e = launch_join(a.p[0], y, pairs, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
 
@@ -1013,7 +1014,7 @@ int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const void* wu,
   if (e == cudaSuccess)
     e = set_problem(&a.p[3], {dym, none}, {hm, none}, 1, D, F, false, plan.dw, T, 0, dwd);
   if (e == cudaSuccess) e = launch_gemm(a, kPlain, act, pairs, plan.worth, st);
-  if (e == cudaSuccess && plan.dx.splits > 1) e = launch_join(a.p[0], dx, st);
+  if (e == cudaSuccess && plan.dx.splits > 1) e = launch_join(a.p[0], dx, pairs, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
 
