@@ -289,3 +289,28 @@ def test_rotary_nodes_take_leading_dimensions(adaln):
         results.append([t.reshape(-1) for t in (qo, ko, x.grad)])
     assert all(torch.equal(a, b) for a, b in zip(*results))
     status_ok()
+
+
+def test_what_an_adaln_call_on_a_given_stream_allocates_is_that_streams(adaln):
+    """As above, for the AdaLN's calls."""
+    T, D = 900, 256
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+    x, dy, shift, scale, busy = r(T, D), r(T, D), r(2, D), r(2, D), r(4096, 4096)
+    seg = (torch.arange(T, device="cuda") >= 400).int()
+    _, mean, rstd = adaln.adaln_fwd(x, shift, scale, seg, 1e-6)
+    side = torch.cuda.Stream()
+    for call in (lambda s: adaln.adaln_fwd(x, shift, scale, seg, 1e-6, stream=s),
+                 lambda s: adaln.adaln_bwd(dy, x, mean, rstd, scale, seg, stream=s)):
+        want = call(None)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy @ busy
+        got = call(side)
+        junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+                for n in (512, 4096, 1 << 17, 1 << 19, 1 << 20, 3 << 20, 8 << 20) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        del junk
+    status_ok()
