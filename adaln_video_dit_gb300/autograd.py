@@ -175,7 +175,8 @@ class GatedFFNFunction(torch.autograd.Function):
 
 def gated_ffn(x, wg, wu, wd, act="silu"):
     """The gated feed-forward block of bf16 x [..., D] with wg, wu [F, D], wd
-    [D, F]; act "silu", "gelu_tanh" or "gelu" (differentiable)."""
+    [D, F], at 16-byte alignment; act "silu", "gelu_tanh" or "gelu"
+    (differentiable)."""
     return GatedFFNFunction.apply(x, wg, wu, wd, act, torch.is_grad_enabled())
 
 

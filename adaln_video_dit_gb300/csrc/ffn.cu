@@ -27,16 +27,21 @@
 // CTA) and eight epilogue warps, two accumulators in tensor memory so that a
 // tile's epilogue runs under the next tile's products.
 //
-// Bound: the tensor cores from a few hundred tokens on, below that the weights'
-// bytes.  Measured (one GB300; 1725 TFLOP/s is what the library's bf16 product
-// sustains under the power limit, 1947 in a burst): T = 32760, D = 5120, F =
-// 13824 forward 7.8 ms, 1785 TFLOP/s; T = 8192 forward and backward 6.2 ms, 1676;
-// T = 8192, D = 1536, F = 4096 forward 168 us, 1840, forward and backward 628 us,
-// 1477.  There (k = 1536) the products are busy for 96 % of the weight
-// gradients' and dx's launch, 87 % of y's (192 tiles are 2.5 rounds of 76 pairs),
-// 73 % of the projections' while saving and 53 % of the gate's gradient: the
-// last two move 10 and 14 bytes through L2 per 1000 operations where the first
-// moves 7, and all three run at the same 15 TB/s of it.
+// Bound: the tensor cores where there are tiles for every pair, the L2 rate
+// where a unit's operands are read for few products, idle pairs where neither
+// the tiles nor the splits of k that pay for their join fill them.  Measured (one
+// GB300; 1725 TFLOP/s is what the library's bf16 product sustains under the power
+// limit, 1947 in a burst; ranges over two runs): T = 32760, D = 5120, F = 13824
+// forward 7.7 to 7.8 ms, 1774 to 1815 TFLOP/s; T = 8192 forward and backward 6.2
+// to 6.3 ms, 1647 to 1690; T = 8192, D = 1536, F = 4096 forward 168 us, 1840,
+// forward and backward 625 to 642 us, 1445 to 1484.  There (k = 1536) the products
+// are busy for 96 % of the weight gradients' and dx's launch, 87 % of y's (192 tiles
+// are 2.5 rounds of 76 pairs), 73 % of the projections' while saving and 53 % of the
+// gate's gradient: the last two move 10 and 14 bytes through L2 per 1000 operations
+// where the first moves 7, and all three run at the same 15 TB/s of it.  T = 256,
+// D = 5120, F = 13824 forward 98 us: the projections at that rate too, y on 60 of 76
+// pairs.  T = 1111, D = 1000, F = 2728 forward and backward 90 us: y on 40 pairs, the
+// gate's gradient on 55, 1111 rows computed as 1280.
 #include <cmath>
 #include <mutex>
 

@@ -21,9 +21,13 @@
 // T = 36864 x 48 heads x 128, bf16, 135.8 us, 98 %; norm and rotation of T = 32760
 // x 80 heads x 128 read out of a packed projection 203.3 us, 97 %; norm, forward
 // and backward, of T = 16384 x 48 heads: 128 wide 84 % (bf16) and 92 % (fp32), 80
-// wide 70 and 92 %, 64 wide 71 and 94 %; halves in 8-byte vectors 51 to 63 %, in
-// 4-byte ones 26 % (the scalar path, which these took before, 4 %).  A call on
-// one token takes 2.6 us of the GPU.
+// wide 70 and 92 %, 64 wide 71 and 94 %.  Bf16, T = 16384 x 48 heads: halves in
+// 8-byte vectors (72 wide) rotation 64, norm 58, its backward 55 %; in 4-byte ones
+// (68 wide: 17 of 32 lanes at work) 35, 33 and 23 %; the scalar path (100 wide,
+// interleaved) 22, 18 and 22 %.  These are bound by their instructions and by what
+// they have in flight: a lane's loads are 2 to 8 times as narrow, so the issue
+// slots are 51 to 62 % busy (scalar 28 to 34 %) where the memory is half idle.
+// A call on one token takes 2.6 us of the GPU.
 //
 // Layout of the work: P lanes share a head, each holding two 16-byte vectors
 // of it that contain whole pairs (interleaved: vectors j and j + half, halves:
