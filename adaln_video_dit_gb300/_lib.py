@@ -1,7 +1,7 @@
 """ctypes binding of libadaln.so (C ABI: include/adaln.h).
 
-Argument marshalling only (for the rotary and feed-forward calls in the compiled
-_binding, csrc/binding.cpp): every step of the operators runs in the library's
+Argument marshalling only (for the rotary, feed-forward and dropout calls in the
+compiled _binding, csrc/binding.cpp): every step of the operators runs in the library's
 CUDA kernels.  torch supplies device memory, streams and output allocation.
 The functions carry the C names and run on their tensors' device, whichever is
 current.  There is no fallback: if libadaln.so is missing or a call fails, an
@@ -21,7 +21,7 @@ ADALN_F32, ADALN_BF16 = 0, 1
  ADALN_ERR_TIMEOUT, ADALN_ERR_POS) = range(11)
 ADALN_DEV_SEG_RANGE, ADALN_DEV_SEG_ORDER, ADALN_DEV_TIMEOUT, ADALN_DEV_POS_RANGE = 1, 2, 4, 8
 ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE = 0, 1, 2
-ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN = 3, 4
+ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN, ADALN_KERNEL_DROPOUT = 3, 4, 6
 ACTS = {"silu": 0, "gelu_tanh": 1, "gelu": 2}
 KERNEL_NAMES = {0: "adaln_fwd_kernel", 1: "adaln_bwd_rows_kernel",
                 2: "adaln_bwd_finalize_kernel"}
@@ -35,7 +35,8 @@ EXPORTS = ["adaln_fwd", "adaln_bwd_workspace_size", "adaln_bwd", "adaln_bwd_noal
            "adaln_selftest_wait_timeout", "adaln_fwd_bwd_host_scratch_size",
            "adaln_fwd_bwd_host", "adaln_qk_rope_fwd", "adaln_qk_rope_bwd_workspace_size",
            "adaln_qk_rope_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size",
-           "adaln_ffn_fwd", "adaln_ffn_bwd"]
+           "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_dropout_fwd",
+           "adaln_dropout_bwd_workspace_size", "adaln_dropout_bwd"]
 
 
 class AdalnError(RuntimeError):
@@ -55,6 +56,11 @@ class Rope(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("rows", ctypes.c_int32),
                 ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32 * MAX_ROPE_AXES),
                 ("interleaved", ctypes.c_int32)]
+
+
+class Rng(ctypes.Structure):
+    """adaln_rng_t: where a call's mask comes from."""
+    _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("state", ctypes.c_void_p)]
 
 
 def _load():
@@ -114,6 +120,14 @@ def _load():
     lib.adaln_ffn_bwd.restype = ci
     lib.adaln_ffn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, ci, ci, vp, vp, vp, vp,
                                   vp, ctypes.c_size_t, vp]
+    gp, f64 = ctypes.POINTER(Rng), ctypes.c_double
+    lib.adaln_dropout_fwd.restype = ci
+    lib.adaln_dropout_fwd.argtypes = [vp, vp, vp, vp, i64, i32, i32, ci, f64, gp, vp, vp]
+    lib.adaln_dropout_bwd_workspace_size.restype = ci
+    lib.adaln_dropout_bwd_workspace_size.argtypes = [i64, i32, i32, ci, sp]
+    lib.adaln_dropout_bwd.restype = ci
+    lib.adaln_dropout_bwd.argtypes = [vp, vp, vp, vp, i64, i32, i32, ci, f64, gp, vp, vp, vp,
+                                      ctypes.c_size_t, vp]
     lib.adaln_selftest_wait_timeout.restype = ci
     lib.adaln_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     lib.adaln_launch_shape.restype = ci
@@ -131,7 +145,8 @@ def _load_binding():
         raise ImportError("_binding.so is missing beside libadaln.so; build both with "
                           "`python -c 'import __graft_entry__ as g; g.build()'`") from e
     entries = ("adaln_qk_rope_fwd", "adaln_qk_rope_bwd", "adaln_qk_rope_bwd_workspace_size",
-               "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size")
+               "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size",
+               "adaln_dropout_fwd", "adaln_dropout_bwd", "adaln_dropout_bwd_workspace_size")
     _binding.setup(torch, torch._C._cuda_getCurrentRawStream, AdalnError,
                    {n: ctypes.cast(getattr(raw, n), ctypes.c_void_p).value for n in entries})
     return _binding
@@ -446,6 +461,34 @@ def adaln_ffn_bwd(dy, x, wg, wu, wd, saved, act="silu", dx=None, dwg=None, dwu=N
     (dx, dwg, dwu, dwd), all bf16."""
     return _on(x, stream, _binding.ffn_bwd, dy, x, wg, wu, wd, saved, _act(act), dx, dwg, dwu, dwd,
                workspace)
+
+
+def adaln_dropout_fwd(h, p, rng=None, x=None, gate=None, seg_id=None, y=None, stream=None):
+    """y = [x +] [gate[seg_id] *] dropout(h) for h [T, D]: elements dropped with
+    probability p, a mask that is never stored.  rng is (seed, offset), or an int64
+    CUDA tensor of the two, read when the call runs; the same values give the same
+    mask.  x [T, D] is the residual, gate [nseg, D] the segments' gates (h's dtype),
+    seg_id int32 [T].  y may be h or x."""
+    return _on(h, stream, _binding.dropout_fwd, h, p, rng, x, gate, seg_id, y)
+
+
+def adaln_dropout_bwd_workspace_size(T, D, nseg, dtype):
+    """Workspace bytes adaln_dropout_bwd needs for a gate's gradient on the current
+    device."""
+    n = ctypes.c_size_t(0)
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    _check(raw.adaln_dropout_bwd_workspace_size(int(T), int(D), int(nseg), code, ctypes.byref(n)),
+           "adaln_dropout_bwd_workspace_size")
+    return n.value
+
+
+def adaln_dropout_bwd(dy, p, rng=None, h=None, gate=None, seg_id=None, dh=None, dgate=None,
+                      workspace=None, stream=None):
+    """Backward of adaln_dropout_fwd with the same p, rng, gate and seg_id (x's
+    gradient is dy).  Returns (dh, dgate): dgate, fp32 [nseg, D], where the forward's
+    h is given for it, else None.  `workspace` is a uint8 CUDA tensor of at least
+    adaln_dropout_bwd_workspace_size bytes (allocated when not given)."""
+    return _on(dy, stream, _binding.dropout_bwd, dy, p, rng, h, gate, seg_id, dh, dgate, workspace)
 
 
 def adaln_get_status(stream=None, device=None):

@@ -1,5 +1,6 @@
 """The operators as autograd nodes: the fused AdaLN, the rotary positions and
-norm of queries and keys, and the gated feed-forward block.
+norm of queries and keys, the gated feed-forward block, and dropout with the gate
+and the residual of a branch.
 
 AdaptiveLoad (Technical summary, section 2.B, "graph simplification"): the
 LayerNorm -> multiply -> add chain of an adaLN modulation site collapses into
@@ -200,3 +201,71 @@ class GatedFFN(torch.nn.Module):
 
     def extra_repr(self):
         return f"dim={self.wg.shape[1]}, hidden={self.wg.shape[0]}, act={self.act!r}"
+
+
+class DropoutFunction(torch.autograd.Function):
+    """y = [x +] [gate[seg_id] *] dropout(h).  Saves the gate and, for its gradient,
+    h; the mask is made again from p and rng."""
+
+    @staticmethod
+    def forward(ctx, h, x, gate, seg_id, p, rng):
+        shape = h.shape
+        h2 = h.reshape(-1, shape[-1]).contiguous()
+        x2 = x.reshape(h2.shape).contiguous() if x is not None else None
+        gate = gate.contiguous() if gate is not None else None
+        of_gate = gate is not None and ctx.needs_input_grad[2]
+        held = torch.is_tensor(rng)
+        ctx.save_for_backward(h2 if of_gate else None, gate, seg_id, rng if held else None)
+        ctx.shape, ctx.p, ctx.rng = shape, p, None if held else rng
+        return _lib.adaln_dropout_fwd(h2, p, rng, x=x2, gate=gate, seg_id=seg_id).reshape(shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        h, gate, seg_id, rng = ctx.saved_tensors
+        dh = dgate = None
+        if ctx.needs_input_grad[0] or h is not None:
+            dy2 = dy.reshape(-1, ctx.shape[-1]).contiguous()
+            dh, dgate = _lib.adaln_dropout_bwd(dy2, ctx.p, ctx.rng if rng is None else rng, h=h, gate=gate,
+                                               seg_id=seg_id)
+            dh = dh.reshape(ctx.shape)
+        return (dh, dy if ctx.needs_input_grad[1] else None,
+                dgate.to(gate.dtype) if dgate is not None else None, None, None, None)
+
+
+def _draw(p, rng, device):
+    """The (seed, offset) of a mask: the given one, or one drawn on the device from
+    torch's generator there, which torch.manual_seed seeds, checkpointing restores
+    for a recomputation and a captured graph advances at each replay."""
+    if rng is not None or p == 0.0:
+        return rng
+    return torch.randint(1 << 62, (2,), device=device, dtype=torch.int64)
+
+
+def dropout(h, p, rng=None):
+    """Dropout of h [..., D] (differentiable): the same p and rng give the same mask.
+    rng is (seed, offset), an int64 CUDA tensor of the two (which may not be
+    changed before the backward), or None: drawn from torch's generator."""
+    return DropoutFunction.apply(h, None, None, None, float(p), _draw(p, rng, h.device))
+
+
+def gated_residual(x, h, gate, seg_id, p=0.0, rng=None):
+    """x + gate[seg_id] * dropout(h): the end of a branch of an adaLN-Zero block, for
+    x, h [..., D] and gate [nseg, D] of one dtype (differentiable in x, h, gate)."""
+    return DropoutFunction.apply(h, x, gate, seg_id, float(p), _draw(p, rng, h.device))
+
+
+class GatedResidual(torch.nn.Module):
+    """Module form: forward(x, h, gate, seg_id); drops in training mode only."""
+
+    def __init__(self, p=0.0):
+        super().__init__()
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p must be in [0, 1], got {p}")
+        self.p = float(p)
+
+    def forward(self, x, h, gate, seg_id, rng=None):
+        return gated_residual(x, h, gate, seg_id, self.p if self.training else 0.0, rng)
+
+    def extra_repr(self):
+        return f"p={self.p}"

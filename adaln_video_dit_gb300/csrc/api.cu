@@ -428,7 +428,7 @@ int adaln_trace_end(void) {
 }
 
 int adaln_trace_get(int kernel_id, int64_t* launches, double* total_ms) {
-  if (kernel_id < 0 || kernel_id >= ADALN_NUM_KERNELS) return ADALN_ERR_ARG;
+  if (kernel_id < 0 || kernel_id >= ADALN_NUM_KERNELS || kernel_id == 5) return ADALN_ERR_ARG;
   std::lock_guard<std::mutex> lk(g_trace_mu);
   if (launches) *launches = g_trace_count[kernel_id];
   if (total_ms) *total_ms = g_trace_ms[kernel_id];

@@ -1,4 +1,4 @@
-// Argument marshalling of the rotary and feed-forward calls, as a CPython
+// Argument marshalling of the rotary, feed-forward and dropout calls, as a CPython
 // extension (_binding): the checks, output allocation and struct building that
 // _lib.py's functions of the same names need.
 //
@@ -40,7 +40,7 @@ struct Ref {
 // ----- what setup() fills --------------------------------------------------------
 
 PyObject *g_empty, *g_empty_like, *g_raw_stream, *g_error;  // callables
-PyObject *g_bf16, *g_f32, *g_i32, *g_u8;                    // dtypes (singletons)
+PyObject *g_bf16, *g_f32, *g_i32, *g_i64, *g_u8;            // dtypes (singletons)
 PyObject *n_get_device, *n_shape, *n_dtype, *n_data_ptr, *n_stride, *n_is_contiguous, *n_device,
     *n_numel, *n_cuda_stream;
 PyObject* g_kw_dtype_device;
@@ -52,6 +52,9 @@ decltype(&adaln_ffn_fwd) f_ffn_fwd;
 decltype(&adaln_ffn_bwd) f_ffn_bwd;
 decltype(&adaln_ffn_saved_size) f_ffn_saved;
 decltype(&adaln_ffn_workspace_size) f_ffn_ws;
+decltype(&adaln_dropout_fwd) f_drop_fwd;
+decltype(&adaln_dropout_bwd) f_drop_bwd;
+decltype(&adaln_dropout_bwd_workspace_size) f_drop_ws;
 
 // ----- reading tensors --------------------------------------------------------------
 
@@ -602,6 +605,148 @@ PyObject* ffn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyTuple_Pack(4, dx.p, dwg.p, dwu.p, dwd.p);
 }
 
+// ----- dropout, gate and residual ------------------------------------------------------------
+
+// Where the mask comes from: None, (seed, offset), or an int64 [2] tensor of them.
+bool rng_of(PyObject* o, long dev, adaln_rng_t* r, bool* given) {
+  *r = adaln_rng_t{};
+  *given = !none(o);
+  if (!*given) return true;
+  if (PyTuple_Check(o)) {
+    if (PyTuple_GET_SIZE(o) != 2) {
+      PyErr_SetString(PyExc_ValueError, "rng must be (seed, offset) or an int64 tensor of the two");
+      return false;
+    }
+    uint64_t* to[2] = {&r->seed, &r->offset};
+    for (int i = 0; i < 2; ++i) {  // any 64-bit integer, signed or not
+      *to[i] = PyLong_AsUnsignedLongLongMask(PyTuple_GET_ITEM(o, i));
+      if (*to[i] == (uint64_t)-1 && PyErr_Occurred()) return false;
+    }
+    return true;
+  }
+  Tensor x;
+  if (!read(o, "rng", &x, false) || !on_device(x, "rng", dev) || !of_dtype(x, "rng", g_i64) ||
+      !of_shape(x, "rng", 1, 2) || !contiguous(o, "rng"))
+    return false;
+  r->state = static_cast<const int64_t*>(x.ptr);
+  return true;
+}
+
+struct Drop {
+  int64_t T, D, nseg = 1;
+  long dev;
+  PyObject* dtype;
+  int code;
+  double p;
+  adaln_rng_t rng;
+  bool drawn;
+  void *h, *gate = nullptr;
+  const int32_t* seg = nullptr;
+};
+
+// h (or dy), p, rng, gate and seg_id.
+bool drop_args(PyObject* h, const char* name, PyObject* p, PyObject* rng, PyObject* gate, PyObject* seg,
+               Drop* d) {
+  Tensor t;
+  if (!read(h, name, &t, false) || !contiguous(h, name)) return false;
+  if (t.ndim != 2 || t.shape[1] > INT32_MAX) {
+    PyErr_Format(PyExc_ValueError, "%s must be [T, D]", name);
+    return false;
+  }
+  d->T = t.shape[0], d->D = t.shape[1], d->dev = t.dev, d->dtype = t.dtype, d->h = t.ptr;
+  if ((d->code = dtype_code(t.dtype)) < 0) return false;
+  d->p = PyFloat_AsDouble(p);
+  if (d->p == -1.0 && PyErr_Occurred()) return false;
+  if (!rng_of(rng, t.dev, &d->rng, &d->drawn)) return false;
+  if (none(gate) != none(seg)) {
+    PyErr_SetString(PyExc_ValueError, "a gate and seg_id belong together");
+    return false;
+  }
+  if (none(gate)) return true;
+  Tensor g, s;
+  if (!read(gate, "gate", &g, false) || !on_device(g, "gate", d->dev) || !contiguous(gate, "gate") ||
+      !of_dtype(g, "gate", d->dtype) || !read(seg, "seg_id", &s, false) ||
+      !on_device(s, "seg_id", d->dev) || !contiguous(seg, "seg_id") || !of_dtype(s, "seg_id", g_i32) ||
+      !of_shape(s, "seg_id", 1, d->T))
+    return false;
+  if (g.ndim != 2 || g.shape[1] != d->D || g.shape[0] > INT32_MAX) {
+    PyErr_Format(PyExc_ValueError, "gate must have shape [nseg, %lld]", (long long)d->D);
+    return false;
+  }
+  d->nseg = g.shape[0], d->gate = g.ptr, d->seg = static_cast<const int32_t*>(s.ptr);
+  return true;
+}
+
+// dropout_fwd(h, p, rng, x, gate, seg_id, y, stream) -> y
+PyObject* dropout_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "8 arguments");
+    return nullptr;
+  }
+  Drop d;
+  Ref y;
+  void *x = nullptr, *yp, *stream;
+  if (!drop_args(a[0], "h", a[1], a[2], a[4], a[5], &d) ||
+      (!none(a[3]) && !matrix(a[3], "x", d.T, d.D, d.dtype, d.dev, &x)) ||
+      !matrix_out(a[6], "y", a[0], d.T, d.D, d.dtype, d.dev, &y, &yp) || !stream_of(a[7], d.dev, &stream))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_drop_fwd(d.h, x, d.gate, d.seg, d.T, (int32_t)d.D, (int32_t)d.nseg, (adaln_dtype_t)d.code, d.p,
+                  d.drawn ? &d.rng : nullptr, yp, stream);
+  Py_END_ALLOW_THREADS;
+  if (rc != ADALN_OK) return refused(rc, "adaln_dropout_fwd");
+  return y.take();
+}
+
+// dropout_bwd(dy, p, rng, h, gate, seg_id, dh, dgate, workspace, stream) -> (dh, dgate)
+PyObject* dropout_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10) {
+    PyErr_SetString(PyExc_TypeError, "10 arguments");
+    return nullptr;
+  }
+  Drop d;
+  Ref dh, dgate, work, device(PyObject_GetAttr(a[0], n_device));
+  void *h = nullptr, *dhp, *sum = nullptr, *ws = nullptr, *stream;
+  size_t bytes = 0;
+  if (!device || !drop_args(a[0], "dy", a[1], a[2], a[4], a[5], &d) ||
+      (!none(a[3]) && !matrix(a[3], "h", d.T, d.D, d.dtype, d.dev, &h)) ||
+      !matrix_out(a[6], "dh", a[0], d.T, d.D, d.dtype, d.dev, &dh, &dhp))
+    return nullptr;
+  if (!none(a[3]) && none(a[4])) {
+    PyErr_SetString(PyExc_ValueError, "h is for the gradient of a gate, and there is none");
+    return nullptr;
+  }
+  if (!none(a[3])) {
+    if (none(a[7])) {
+      Ref shape(Py_BuildValue("LL", (long long)d.nseg, (long long)d.D));
+      if (!shape) return nullptr;
+      dgate.set(new_tensor(shape.p, g_f32, device.p));
+      if (!dgate || !pointer(dgate.p, &sum)) return nullptr;
+    } else {
+      if (!matrix(a[7], "dgate", d.nseg, d.D, g_f32, d.dev, &sum)) return nullptr;
+      Py_INCREF(a[7]);
+      dgate.set(a[7]);
+    }
+    if (none(a[8])) {
+      const int rc = f_drop_ws(d.T, (int32_t)d.D, (int32_t)d.nseg, (adaln_dtype_t)d.code, &bytes);
+      if (rc != ADALN_OK) return refused(rc, "adaln_dropout_bwd_workspace_size");
+      work.set(new_bytes(bytes, device.p));
+      if (!work || !pointer(work.p, &ws)) return nullptr;
+    } else if (!buffer(a[8], "workspace", d.dev, &ws, &bytes)) {
+      return nullptr;
+    }
+  }
+  if (!stream_of(a[9], d.dev, &stream)) return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_drop_bwd(d.h, h, d.gate, d.seg, d.T, (int32_t)d.D, (int32_t)d.nseg, (adaln_dtype_t)d.code, d.p,
+                  d.drawn ? &d.rng : nullptr, dhp, static_cast<float*>(sum), ws, bytes, stream);
+  Py_END_ALLOW_THREADS;
+  if (rc != ADALN_OK) return refused(rc, "adaln_dropout_bwd");
+  return pair_or(dh, dgate);
+}
+
 // ----- module --------------------------------------------------------------------------------
 
 template <class F>
@@ -627,7 +772,8 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyObject** to;
     const char* name;
   } const attrs[] = {{&g_empty, "empty"}, {&g_empty_like, "empty_like"}, {&g_bf16, "bfloat16"},
-                     {&g_f32, "float32"}, {&g_i32, "int32"},             {&g_u8, "uint8"}},
+                     {&g_f32, "float32"}, {&g_i32, "int32"},             {&g_i64, "int64"},
+                     {&g_u8, "uint8"}},
       names[] = {{&n_get_device, "get_device"}, {&n_shape, "shape"},
                  {&n_dtype, "dtype"},           {&n_data_ptr, "data_ptr"},
                  {&n_stride, "stride"},         {&n_is_contiguous, "is_contiguous"},
@@ -646,7 +792,9 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !entry(a[3], "adaln_qk_rope_bwd_workspace_size", &f_qk_ws) ||
       !entry(a[3], "adaln_ffn_fwd", &f_ffn_fwd) || !entry(a[3], "adaln_ffn_bwd", &f_ffn_bwd) ||
       !entry(a[3], "adaln_ffn_saved_size", &f_ffn_saved) ||
-      !entry(a[3], "adaln_ffn_workspace_size", &f_ffn_ws))
+      !entry(a[3], "adaln_ffn_workspace_size", &f_ffn_ws) ||
+      !entry(a[3], "adaln_dropout_fwd", &f_drop_fwd) || !entry(a[3], "adaln_dropout_bwd", &f_drop_bwd) ||
+      !entry(a[3], "adaln_dropout_bwd_workspace_size", &f_drop_ws))
     return nullptr;
   Py_RETURN_NONE;
 }
@@ -657,10 +805,12 @@ PyMethodDef methods[] = {
     {"qk_rope_bwd", (PyCFunction)(void (*)(void))qk_rope_bwd, METH_FASTCALL, nullptr},
     {"ffn_fwd", (PyCFunction)(void (*)(void))ffn_fwd, METH_FASTCALL, nullptr},
     {"ffn_bwd", (PyCFunction)(void (*)(void))ffn_bwd, METH_FASTCALL, nullptr},
+    {"dropout_fwd", (PyCFunction)(void (*)(void))dropout_fwd, METH_FASTCALL, nullptr},
+    {"dropout_bwd", (PyCFunction)(void (*)(void))dropout_bwd, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding",
-                      "Argument marshalling of the rotary and feed-forward calls.", -1, methods,
+                      "Argument marshalling of the rotary, feed-forward and dropout calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

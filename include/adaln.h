@@ -1,9 +1,10 @@
 /*
  * libadaln -- operators of video diffusion transformer blocks for GB300
  * (sm_103a): the fused AdaLN LayerNorm-Modulate, described here, and, further
- * down, rotary positions with the norm of queries and keys (adaln_qk_rope_*)
- * and the gated feed-forward block (adaln_ffn_*), which share its conventions
- * on ownership, streams, errors and the status word.
+ * down, rotary positions with the norm of queries and keys (adaln_qk_rope_*),
+ * the gated feed-forward block (adaln_ffn_*) and dropout with the gate and the
+ * residual of a branch (adaln_dropout_*), which share its conventions on
+ * ownership, streams, errors and the status word.
  *
  * The AdaLN is the fused adaptive LayerNorm of video / MMDiT diffusion
  * transformers described in "AdaptiveLoad: Towards Efficient Video Diffusion
@@ -87,6 +88,7 @@ extern "C" {
 #define ADALN_MAX_ROPE_AXES 4
 #define ADALN_FFN_MAX_T (1 << 24)
 #define ADALN_FFN_MAX_DIM (1 << 18)
+#define ADALN_DROPOUT_MAX_D (1 << 18)
 
 typedef enum {
   ADALN_F32 = 0,  /* IEEE binary32 */
@@ -356,6 +358,64 @@ ADALN_API int adaln_ffn_bwd(const void* dy, const void* x, const void* wg, const
               void* dwd, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Dropout whose mask is never stored, with what stands around it where a branch
+ * of a block meets the residual stream:
+ *
+ *   y = [x +] [gate[b] *] m s h                        b = seg_id[t]
+ *
+ * The mask m comes from a counter-based generator (Philox-4x32, ten rounds; key =
+ * seed, counter = (t ceil(D / 8) + c, offset), 64 bits each, lowest word first):
+ * elements 8c .. 8c + 7 of token t take the eight 16-bit parts of its output,
+ * lowest first, and one is dropped (m = 0) where its part is below
+ * n = floor(65536 p + 1/2).  s = 65536 / (65536 - n).  So the same seed and
+ * offset give the same mask, in a backward too, whatever the element type and
+ * the device; p = 0 (or below 2^-17) drops nothing and p = 1 everything, and
+ * neither reads the generator's state.
+ */
+typedef struct {
+  uint64_t seed, offset;
+  const int64_t* state; /* device: (seed, offset) read from here when the call runs,
+                           instead of the two above (for captured graphs, whose
+                           replays then draw other masks); or NULL.  8-byte aligned */
+} adaln_rng_t;
+
+/*
+ * Forward, one launch.  h, x, y [T, D] and gate [nseg, D] have the element type
+ * `dtype`; x (the residual) and gate may be NULL, seg_id and nseg are used with a
+ * gate only.  y may be h or x itself, but may not overlap them otherwise.
+ * Arithmetic is fp32, y rounded once; a dropped element takes nothing from h or
+ * the gate, whatever they hold.  A bad seg_id is clamped and recorded
+ * (ADALN_DEV_SEG_RANGE, ADALN_DEV_SEG_ORDER).
+ *
+ * Errors: ADALN_ERR_DTYPE; ADALN_ERR_DIM for T outside [0, 2^31), D outside [1,
+ * ADALN_DROPOUT_MAX_D] or not of whole 16-byte vectors, T D above about 2^37, or
+ * (with a gate) a bad nseg; ADALN_ERR_ARG for p outside [0, 1]; ADALN_ERR_NULL (rng too, where the
+ * mask is drawn); ADALN_ERR_ALIGN (16 bytes, seg_id 4).
+ */
+ADALN_API int adaln_dropout_fwd(const void* h, const void* x, const void* gate,
+              const int32_t* seg_id, int64_t T, int32_t D, int32_t nseg, adaln_dtype_t dtype,
+              double p, const adaln_rng_t* rng, void* y, void* stream);
+
+/*
+ * Backward (dx is dy itself):
+ *
+ *   dh = [gate[b] *] m s dy,     dgate[b] = sum_{t: seg_id[t] = b} m s dy h
+ *
+ * Without dgate (NULL) one launch, and h and workspace are unused; with it (fp32
+ * [nseg, D], needs gate and the forward's h) a second one adds partial sums in a
+ * fixed order: bitwise reproducible for a given device and sizes.  dh may be dy or
+ * h itself.  `workspace`: at least adaln_dropout_bwd_workspace_size bytes, 16-byte
+ * aligned, the caller's.  T = 0 zeroes dgate.  Errors as for the forward;
+ * ADALN_ERR_WORKSPACE for a short workspace.
+ */
+ADALN_API int adaln_dropout_bwd_workspace_size(int64_t T, int32_t D, int32_t nseg,
+              adaln_dtype_t dtype, size_t* bytes);
+ADALN_API int adaln_dropout_bwd(const void* dy, const void* h, const void* gate,
+              const int32_t* seg_id, int64_t T, int32_t D, int32_t nseg, adaln_dtype_t dtype,
+              double p, const adaln_rng_t* rng, void* dh, float* dgate, void* workspace,
+              size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the status word: the one the
  * calling thread bound (adaln_status_bind), else the current device's.
  * *host_bits (if non-NULL) receives the ADALN_DEV_* bits.  Returns ADALN_OK,
@@ -389,15 +449,16 @@ ADALN_API const char* adaln_strerror(int code);
  * `capacity` launches.  adaln_trace_end() synchronises those events and sums
  * the elapsed time per kernel; adaln_trace_get() reads the sums.
  * Kernel ids: ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE;
- * ADALN_KERNEL_QK_ROPE and ADALN_KERNEL_FFN count every launch of the rotary
- * and of the feed-forward calls.
+ * ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN and ADALN_KERNEL_DROPOUT count every
+ * launch of the rotary, the feed-forward and the dropout calls (5 is no id).
  */
 #define ADALN_KERNEL_FWD 0
 #define ADALN_KERNEL_BWD_ROWS 1
 #define ADALN_KERNEL_BWD_FINALIZE 2
 #define ADALN_KERNEL_QK_ROPE 3
 #define ADALN_KERNEL_FFN 4
-#define ADALN_NUM_KERNELS 5
+#define ADALN_KERNEL_DROPOUT 6
+#define ADALN_NUM_KERNELS 7
 ADALN_API int adaln_trace_begin(int capacity);
 ADALN_API int adaln_trace_end(void);
 ADALN_API int adaln_trace_get(int kernel_id, int64_t* launches, double* total_ms);

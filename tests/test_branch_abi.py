@@ -1,0 +1,132 @@
+"""Host-side checks of the residual branch's entry points (dropout with gate and
+residual): refused before any CUDA call, no address is dereferenced; what the nodes
+save; and the generator of the tests' own reference against published values."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from philox import kept, philox
+
+A, B = 0x10000, 0x20000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from adaln_video_dit_gb300 import build
+    build.build()
+    from adaln_video_dit_gb300 import _lib
+    return _lib
+
+
+def test_the_reference_generator_gives_the_published_values():
+    """The known answers published with the generator."""
+    for c, k, want in (
+            ((0,) * 4, (0,) * 2, (0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8)),
+            ((0xFFFFFFFF,) * 4, (0xFFFFFFFF,) * 2, (0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD)),
+            ((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0),
+             (0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1))):
+        assert tuple(int(x) for x in philox(c, k)) == want
+    # (Of 2^20 draws the share kept is within five standard deviations of its mean.)
+    for p in (0.1, 0.5):
+        share = kept(np.arange(1024), 1024, p, 5, 9)[0].mean()
+        assert abs(share - (1 - p)) <= 5 * (p * (1 - p)) ** 0.5 / 1024
+
+
+def drop_fwd(lib, rng=True, **kw):
+    r = lib.Rng(1, 2, None) if rng is True else rng
+    a = dict(h=A, x=A, gate=A, seg=A, T=10, D=64, nseg=2, dt=lib.ADALN_BF16, p=0.1,
+             rng=ctypes.byref(r) if r is not None else None, y=B)
+    a.update(kw)
+    return lib.raw.adaln_dropout_fwd(*a.values(), None)
+
+
+def drop_bwd(lib, rng=True, **kw):
+    r = lib.Rng(1, 2, None) if rng is True else rng
+    a = dict(dy=A, h=A, gate=A, seg=A, T=10, D=64, nseg=2, dt=lib.ADALN_BF16, p=0.1,
+             rng=ctypes.byref(r) if r is not None else None, dh=B, dgate=B, ws=B, wsb=1 << 30)
+    a.update(kw)
+    return lib.raw.adaln_dropout_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [drop_fwd, drop_bwd])
+def test_dropout_refusals(lib, call):
+    assert call(lib, dt=2) == lib.ADALN_ERR_DTYPE
+    for bad in (dict(T=-1), dict(T=2 ** 31), dict(D=0), dict(D=12), dict(D=2 ** 18 + 8), dict(nseg=0),
+                dict(nseg=2 ** 24 + 1), dict(D=6, dt=lib.ADALN_F32), dict(T=2 ** 31 - 1, D=2 ** 8)):
+        assert call(lib, **bad) == lib.ADALN_ERR_DIM, bad
+    for p in (-0.1, 1.5, float("nan"), float("inf")):
+        assert call(lib, p=p) == lib.ADALN_ERR_ARG
+    assert call(lib, rng=None) == lib.ADALN_ERR_NULL
+    assert call(lib, rng=lib.Rng(0, 0, A + 4)) == lib.ADALN_ERR_ALIGN
+    assert call(lib, seg=None) == lib.ADALN_ERR_NULL
+    assert call(lib, gate=A + 8) == lib.ADALN_ERR_ALIGN
+    assert call(lib, seg=A + 2) == lib.ADALN_ERR_ALIGN
+
+
+def test_dropout_only_what_is_missing_is_refused(lib):
+    assert drop_fwd(lib, h=None) == lib.ADALN_ERR_NULL
+    assert drop_fwd(lib, y=None) == lib.ADALN_ERR_NULL
+    for k in ("h", "x", "y"):
+        assert drop_fwd(lib, **{k: A + 8}) == lib.ADALN_ERR_ALIGN, k
+    for k in ("dy", "h", "gate", "dh", "ws"):
+        assert drop_bwd(lib, **{k: None}) == lib.ADALN_ERR_NULL, k
+    for k in ("dy", "h", "dh", "dgate", "ws"):
+        assert drop_bwd(lib, **{k: A + 8}) == lib.ADALN_ERR_ALIGN, k
+    assert drop_fwd(lib, T=0, h=None, y=None) == lib.ADALN_OK
+    assert drop_bwd(lib, T=0, dy=None, dh=None, dgate=None) == lib.ADALN_OK
+    assert lib.raw.adaln_dropout_bwd_workspace_size(4, 64, 1, 1, None) == lib.ADALN_ERR_NULL
+    n = ctypes.c_size_t(0)
+    assert lib.raw.adaln_dropout_bwd_workspace_size(4, 60, 1, 1, ctypes.byref(n)) == lib.ADALN_ERR_DIM
+
+
+def test_kernel_ids(lib):
+    n, ms = ctypes.c_int64(-1), ctypes.c_double(-1)
+    got = [lib.raw.adaln_trace_get(i, ctypes.byref(n), ctypes.byref(ms)) for i in range(-1, 9)]
+    assert got[lib.ADALN_KERNEL_DROPOUT + 1] == lib.ADALN_OK
+    assert got[0] == got[6] == got[9] == lib.ADALN_ERR_ARG
+
+
+def test_dropout_saves_h_for_a_gates_gradient_only(lib, monkeypatch):
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    seen = []
+
+    def fwd(h, p, rng, x=None, gate=None, seg_id=None):
+        seen.append((tuple(h.shape), None if x is None else tuple(x.shape), p))
+        return h * 1
+
+    def bwd(dy, p, rng, h=None, gate=None, seg_id=None):
+        seen.append(("back", h is not None, rng))
+        return dy * 2, None if h is None else torch.full(gate.shape, 3.0)
+
+    monkeypatch.setattr(autograd._lib, "adaln_dropout_fwd", fwd)
+    monkeypatch.setattr(autograd._lib, "adaln_dropout_bwd", bwd)
+    h, x = (torch.ones(2, 3, 8, requires_grad=True) for _ in range(2))
+    gate, seg = torch.zeros(2, 8, requires_grad=True), torch.zeros(6, dtype=torch.int32)
+    autograd.gated_residual(x, h, gate, seg, 0.5, (1, 2)).sum().backward()
+    assert seen == [((6, 8), (6, 8), 0.5), ("back", True, (1, 2))]
+    assert torch.equal(h.grad, torch.full((2, 3, 8), 2.0)) and torch.equal(x.grad, torch.ones(2, 3, 8))
+    assert torch.equal(gate.grad, torch.full((2, 8), 3.0))
+    seen.clear()
+    autograd.gated_residual(x, h, gate.detach(), seg, 0.5, (1, 2)).sum().backward()
+    assert seen[1] == ("back", False, (1, 2))
+    seen.clear()  # a branch without a gradient costs no backward call
+    autograd.gated_residual(x, h.detach(), gate.detach(), seg, 0.5, (1, 2)).sum().backward()
+    assert len(seen) == 1
+    # A generator's state changed between forward and backward would give another mask.
+    rng = torch.tensor([1, 2])
+    y = autograd.dropout(h, 0.5, rng)
+    rng += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        y.sum().backward()
+    out = autograd.dropout(h, 0.5, (1, 2))
+    first, = torch.autograd.grad((out * out).sum(), h, create_graph=True)
+    with pytest.raises(RuntimeError, match="twice"):
+        first.sum().backward()
+    with pytest.raises(ValueError):
+        autograd.GatedResidual(1.5)
+    seen.clear()
+    m = autograd.GatedResidual(0.5).eval()
+    m(x, h, gate, seg)
+    assert seen[0][2] == 0.0
