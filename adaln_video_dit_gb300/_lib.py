@@ -1,7 +1,7 @@
 """ctypes binding of libadaln.so (C ABI: include/adaln.h).
 
-Argument marshalling only (for the rotary, feed-forward and dropout calls in the
-compiled _binding, csrc/binding.cpp): every step of the operators runs in the library's
+Argument marshalling only (but for the AdaLN calls in the compiled _binding,
+csrc/binding.cpp): every step of the operators runs in the library's
 CUDA kernels.  torch supplies device memory, streams and output allocation.
 The functions carry the C names and run on their tensors' device, whichever is
 current.  There is no fallback: if libadaln.so is missing or a call fails, an
@@ -9,6 +9,7 @@ exception is raised.
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -18,10 +19,11 @@ LIB_PATH = os.path.join(HERE, "libadaln.so")
 ADALN_F32, ADALN_BF16 = 0, 1
 (ADALN_OK, ADALN_ERR_NULL, ADALN_ERR_DIM, ADALN_ERR_ALIGN, ADALN_ERR_DTYPE,
  ADALN_ERR_SEG, ADALN_ERR_WORKSPACE, ADALN_ERR_CUDA, ADALN_ERR_ARG,
- ADALN_ERR_TIMEOUT, ADALN_ERR_POS) = range(11)
+ ADALN_ERR_TIMEOUT, ADALN_ERR_POS, ADALN_ERR_EXPERT) = range(12)
 ADALN_DEV_SEG_RANGE, ADALN_DEV_SEG_ORDER, ADALN_DEV_TIMEOUT, ADALN_DEV_POS_RANGE = 1, 2, 4, 8
+ADALN_DEV_EXPERT_RANGE = 16
 ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE = 0, 1, 2
-ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN, ADALN_KERNEL_DROPOUT = 3, 4, 6
+ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN, ADALN_KERNEL_DROPOUT, ADALN_KERNEL_EXPERTS = 3, 4, 6, 7
 ACTS = {"silu": 0, "gelu_tanh": 1, "gelu": 2}
 KERNEL_NAMES = {0: "adaln_fwd_kernel", 1: "adaln_bwd_rows_kernel",
                 2: "adaln_bwd_finalize_kernel"}
@@ -36,7 +38,9 @@ EXPORTS = ["adaln_fwd", "adaln_bwd_workspace_size", "adaln_bwd", "adaln_bwd_noal
            "adaln_fwd_bwd_host", "adaln_qk_rope_fwd", "adaln_qk_rope_bwd_workspace_size",
            "adaln_qk_rope_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size",
            "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_dropout_fwd",
-           "adaln_dropout_bwd_workspace_size", "adaln_dropout_bwd"]
+           "adaln_dropout_bwd_workspace_size", "adaln_dropout_bwd", "adaln_route_rows",
+           "adaln_route_workspace_size", "adaln_route", "adaln_expert_sort_fwd",
+           "adaln_expert_sort_bwd", "adaln_expert_combine_fwd", "adaln_expert_combine_bwd"]
 
 
 class AdalnError(RuntimeError):
@@ -56,6 +60,15 @@ class Rope(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("rows", ctypes.c_int32),
                 ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32 * MAX_ROPE_AXES),
                 ("interleaved", ctypes.c_int32)]
+
+
+class Route(NamedTuple):
+    """Where the (token, choice) pairs of a call lie when sorted by expert."""
+    row: torch.Tensor     # int32 [T, k]: a pair's row of a sorted array, -1 for none
+    starts: torch.Tensor  # int32 [E + 1]: an expert's first row; the end of the last
+    counts: torch.Tensor  # int32 [E]: an expert's pairs
+    rows: int             # rows of a sorted array
+    align: int            # what the starts are multiples of
 
 
 class Rng(ctypes.Structure):
@@ -128,6 +141,21 @@ def _load():
     lib.adaln_dropout_bwd.restype = ci
     lib.adaln_dropout_bwd.argtypes = [vp, vp, vp, vp, i64, i32, i32, ci, f64, gp, vp, vp, vp,
                                       ctypes.c_size_t, vp]
+    lib.adaln_route_rows.restype = ci
+    lib.adaln_route_rows.argtypes = [i64, i32, i32, i32, ctypes.POINTER(i64)]
+    lib.adaln_route_workspace_size.restype = ci
+    lib.adaln_route_workspace_size.argtypes = [i64, i32, i32, sp]
+    lib.adaln_route.restype = ci
+    lib.adaln_route.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.adaln_expert_sort_fwd.restype = ci
+    lib.adaln_expert_sort_fwd.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, i32, ci, i64, vp, vp]
+    lib.adaln_expert_sort_bwd.restype = ci
+    lib.adaln_expert_sort_bwd.argtypes = [vp, vp, i64, i32, i32, ci, i64, vp, vp]
+    lib.adaln_expert_combine_fwd.restype = ci
+    lib.adaln_expert_combine_fwd.argtypes = [vp, vp, vp, i64, i32, i32, ci, i64, vp, vp]
+    lib.adaln_expert_combine_bwd.restype = ci
+    lib.adaln_expert_combine_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, ci, i64,
+                                             vp, vp, vp]
     lib.adaln_selftest_wait_timeout.restype = ci
     lib.adaln_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     lib.adaln_launch_shape.restype = ci
@@ -146,7 +174,9 @@ def _load_binding():
                           "`python -c 'import __graft_entry__ as g; g.build()'`") from e
     entries = ("adaln_qk_rope_fwd", "adaln_qk_rope_bwd", "adaln_qk_rope_bwd_workspace_size",
                "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size",
-               "adaln_dropout_fwd", "adaln_dropout_bwd", "adaln_dropout_bwd_workspace_size")
+               "adaln_dropout_fwd", "adaln_dropout_bwd", "adaln_dropout_bwd_workspace_size",
+               "adaln_route_rows", "adaln_route_workspace_size", "adaln_route", "adaln_expert_sort_fwd",
+               "adaln_expert_sort_bwd", "adaln_expert_combine_fwd", "adaln_expert_combine_bwd")
     _binding.setup(torch, torch._C._cuda_getCurrentRawStream, AdalnError,
                    {n: ctypes.cast(getattr(raw, n), ctypes.c_void_p).value for n in entries})
     return _binding
@@ -489,6 +519,51 @@ def adaln_dropout_bwd(dy, p, rng=None, h=None, gate=None, seg_id=None, dh=None, 
     h is given for it, else None.  `workspace` is a uint8 CUDA tensor of at least
     adaln_dropout_bwd_workspace_size bytes (allocated when not given)."""
     return _on(dy, stream, _binding.dropout_bwd, dy, p, rng, h, gate, seg_id, dh, dgate, workspace)
+
+
+def adaln_route_rows(T, k, E, align=64):
+    """Rows that a sorted array of T tokens with k choices of E experts needs."""
+    n = ctypes.c_int64(0)
+    _check(raw.adaln_route_rows(int(T), int(k), int(E), int(align), ctypes.byref(n)), "adaln_route_rows")
+    return n.value
+
+
+def adaln_route_workspace_size(T, k, E):
+    """Workspace bytes of adaln_route (0 for few pairs)."""
+    n = ctypes.c_size_t(0)
+    _check(raw.adaln_route_workspace_size(int(T), int(k), int(E), ctypes.byref(n)),
+           "adaln_route_workspace_size")
+    return n.value
+
+
+def adaln_route(expert, E, align=64, row=None, starts=None, counts=None, workspace=None, stream=None):
+    """The Route of expert, int32 [T, k]: each token's choices among E experts (-1 for
+    none), sorted by expert, equal ones in the order of the tokens, each expert's start
+    a multiple of `align` rows."""
+    return Route(*_on(expert, stream, _binding.route, expert, E, align, row, starts, counts, workspace),
+                 align)
+
+
+def adaln_expert_sort_fwd(x, route, xs=None, stream=None):
+    """xs [route.rows, D] with x's tokens [T, D] at their choices' rows, zeros between
+    the experts; rows from route.starts[-1] on are not written."""
+    return _on(x, stream, _binding.expert_sort_fwd, x, route, xs)
+
+
+def adaln_expert_sort_bwd(dxs, route, dx=None, stream=None):
+    """Backward of adaln_expert_sort_fwd: dx [T, D], the sum of each token's rows."""
+    return _on(dxs, stream, _binding.expert_sort_bwd, dxs, route, dx)
+
+
+def adaln_expert_combine_fwd(ys, weight, route, y=None, stream=None):
+    """y [T, D]: each token's rows of ys [route.rows, D], weighted with weight, fp32
+    [T, k], and summed."""
+    return _on(ys, stream, _binding.expert_combine_fwd, ys, weight, route, y)
+
+
+def adaln_expert_combine_bwd(dy, ys, weight, route, dys=None, dweight=None, stream=None):
+    """Backward of adaln_expert_combine_fwd: (dys, dweight), dys as the sort's xs."""
+    return _on(dy, stream, _binding.expert_combine_bwd, dy, ys, weight, route, dys, dweight)
 
 
 def adaln_get_status(stream=None, device=None):

@@ -1,6 +1,6 @@
 """The operators as autograd nodes: the fused AdaLN, the rotary positions and
-norm of queries and keys, the gated feed-forward block, and dropout with the gate
-and the residual of a branch.
+norm of queries and keys, the gated feed-forward block, dropout with the gate and
+the residual of a branch, and tokens sorted by expert and back.
 
 AdaptiveLoad (Technical summary, section 2.B, "graph simplification"): the
 LayerNorm -> multiply -> add chain of an adaLN modulation site collapses into
@@ -269,3 +269,64 @@ class GatedResidual(torch.nn.Module):
 
     def extra_repr(self):
         return f"p={self.p}"
+
+
+def route(expert, num_experts, align=64):
+    """Where tokens go: expert [..., k] holds each token's choices (-1 for none), and
+    the Route sorts the (token, choice) pairs by expert, for expert_sort and
+    expert_combine."""
+    return _lib.adaln_route(expert.reshape(-1, expert.shape[-1]).to(torch.int32).contiguous(), num_experts,
+                            align)
+
+
+class ExpertSortFunction(torch.autograd.Function):
+    """xs[route.row[t, j]] = x[t].  Saves the route's indices."""
+
+    @staticmethod
+    def forward(ctx, x, row, starts, counts, rows, align):
+        x2 = x.reshape(-1, x.shape[-1]).contiguous()
+        ctx.save_for_backward(row, starts, counts)
+        ctx.rows, ctx.align, ctx.shape = rows, align, x.shape
+        return _lib.adaln_expert_sort_fwd(x2, _lib.Route(row, starts, counts, rows, align))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dxs):
+        r = _lib.Route(*ctx.saved_tensors, ctx.rows, ctx.align)
+        return (_lib.adaln_expert_sort_bwd(dxs.contiguous(), r).reshape(ctx.shape),) + (None,) * 5
+
+
+class ExpertCombineFunction(torch.autograd.Function):
+    """y[t] = sum_j weight[t, j] ys[route.row[t, j]].  Saves ys, the weights and the
+    route's indices."""
+
+    @staticmethod
+    def forward(ctx, ys, weight, row, starts, counts, rows, align):
+        w2 = weight.reshape(row.shape).float().contiguous()
+        ys = ys.contiguous()
+        ctx.save_for_backward(ys, w2, row, starts, counts)
+        ctx.rows, ctx.align, ctx.weight = rows, align, (weight.shape, weight.dtype)
+        y = _lib.adaln_expert_combine_fwd(ys, w2, _lib.Route(row, starts, counts, rows, align))
+        return y.reshape(*weight.shape[:-1], y.shape[-1])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        ys, weight, *indices = ctx.saved_tensors
+        dys, dw = _lib.adaln_expert_combine_bwd(dy.reshape(-1, dy.shape[-1]).contiguous(), ys, weight,
+                                                _lib.Route(*indices, ctx.rows, ctx.align))
+        return (dys, dw.reshape(ctx.weight[0]).to(ctx.weight[1])) + (None,) * 5
+
+
+def expert_sort(x, route):
+    """Tokens x [..., D] sorted by expert: [route.rows, D], each at the rows of its
+    choices, zeros between the experts' rows (differentiable).  Rows from
+    route.starts[-1] on hold nothing: they are not written, here or in a gradient."""
+    return ExpertSortFunction.apply(x, *route)
+
+
+def expert_combine(ys, weight, route):
+    """The experts' outputs ys [route.rows, D] brought back to their tokens, each
+    weighted with its choice's weight [..., k], and summed: [..., D]
+    (differentiable in ys and weight)."""
+    return ExpertCombineFunction.apply(ys, weight, *route)

@@ -19,7 +19,7 @@ LIB_TUNING = os.path.join(HERE, "libadaln_tuning.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "dropout.cu", "ffn.cu", "ffn_skinny.cu", "host.cu", "noalloc.cu", "rope.cu",
-           "rope_bf16.cu", "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "selftest.cu"]
+           "rope_bf16.cu", "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "route.cu", "selftest.cu"]
 HEADERS = ["common.cuh", "ring.cuh", "tc.cuh", "ffn.cuh", "rope.cuh", "internal.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -132,7 +132,7 @@ def _strip_comments(text):
 
 # Sources that no AdaLN kernel is made of.
 OTHER_OPERATORS = {"dropout.cu", "ffn.cu", "ffn.cuh", "ffn_skinny.cu", "rope.cu", "rope.cuh", "rope_bf16.cu",
-                   "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "tc.cuh", "binding.cpp"}
+                   "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "route.cu", "tc.cuh", "binding.cpp"}
 
 
 def source_hash():

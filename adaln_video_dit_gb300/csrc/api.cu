@@ -352,6 +352,7 @@ int adaln_get_status(uint32_t* host_bits, void* stream) {
   if (host_bits) *host_bits = bits;
   if (bits & (ADALN_DEV_SEG_RANGE | ADALN_DEV_SEG_ORDER)) return ADALN_ERR_SEG;
   if (bits & ADALN_DEV_POS_RANGE) return ADALN_ERR_POS;
+  if (bits & ADALN_DEV_EXPERT_RANGE) return ADALN_ERR_EXPERT;
   if (bits & ADALN_DEV_TIMEOUT) return ADALN_ERR_TIMEOUT;
   return ADALN_OK;
 }
@@ -375,6 +376,7 @@ const char* adaln_strerror(int code) {
     case ADALN_ERR_ARG: return "invalid argument (eps or trace capacity)";
     case ADALN_ERR_TIMEOUT: return "an internal pipeline wait gave up (device status)";
     case ADALN_ERR_POS: return "a rotary position outside the table (device status)";
+    case ADALN_ERR_EXPERT: return "an expert, or a sorted row, out of range (device status)";
     default: return "unknown status code";
   }
 }

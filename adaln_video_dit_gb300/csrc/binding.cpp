@@ -1,4 +1,4 @@
-// Argument marshalling of the rotary, feed-forward and dropout calls, as a CPython
+// Argument marshalling of every call but the AdaLN's, as a CPython
 // extension (_binding): the checks, output allocation and struct building that
 // _lib.py's functions of the same names need.
 //
@@ -55,6 +55,13 @@ decltype(&adaln_ffn_workspace_size) f_ffn_ws;
 decltype(&adaln_dropout_fwd) f_drop_fwd;
 decltype(&adaln_dropout_bwd) f_drop_bwd;
 decltype(&adaln_dropout_bwd_workspace_size) f_drop_ws;
+decltype(&adaln_route_rows) f_route_rows;
+decltype(&adaln_route_workspace_size) f_route_ws;
+decltype(&adaln_route) f_route;
+decltype(&adaln_expert_sort_fwd) f_sort_fwd;
+decltype(&adaln_expert_sort_bwd) f_sort_bwd;
+decltype(&adaln_expert_combine_fwd) f_combine_fwd;
+decltype(&adaln_expert_combine_bwd) f_combine_bwd;
 
 // ----- reading tensors --------------------------------------------------------------
 
@@ -747,6 +754,229 @@ PyObject* dropout_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return pair_or(dh, dgate);
 }
 
+// ----- tokens by expert and back ----------------------------------------------------------------
+
+// A contiguous tensor of this dtype and shape: checked and taken, or allocated.
+bool array_out(PyObject* given, const char* name, int ndim, int64_t rows, int64_t cols, PyObject* dtype,
+               PyObject* device, long dev, Ref* out, void** p) {
+  if (none(given)) {
+    Ref shape(ndim == 1 ? Py_BuildValue("(L)", (long long)rows)
+                        : Py_BuildValue("(LL)", (long long)rows, (long long)cols));
+    if (!shape) return false;
+    out->set(new_tensor(shape.p, dtype, device));
+    return *out && pointer(out->p, p);
+  }
+  Tensor x;
+  if (!read(given, name, &x, false) || !on_device(x, name, dev) || !contiguous(given, name) ||
+      !of_dtype(x, name, dtype) || !of_shape(x, name, ndim, rows, cols))
+    return false;
+  Py_INCREF(given);
+  out->set(given);
+  *p = x.ptr;
+  return true;
+}
+
+bool positive(PyObject* o, const char* name, int32_t* out) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) return false;
+  *out = v < 1 || v > INT32_MAX ? 0 : (int32_t)v;  // (0 is refused by the library)
+  return true;
+}
+
+// route(expert, E, align, row, starts, counts, workspace, stream)
+//   -> (row, starts, counts, rows)
+PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "8 arguments");
+    return nullptr;
+  }
+  Tensor x;
+  int32_t E, align;
+  if (!read(a[0], "expert", &x, false) || !of_dtype(x, "expert", g_i32) || !contiguous(a[0], "expert") ||
+      !positive(a[1], "E", &E) || !positive(a[2], "align", &align))
+    return nullptr;
+  if (x.ndim != 2) {
+    PyErr_SetString(PyExc_ValueError, "expert must be [T, k]");
+    return nullptr;
+  }
+  const int64_t T = x.shape[0];
+  const int32_t k = x.shape[1] > INT32_MAX ? 0 : (int32_t)x.shape[1];
+  int64_t rows = 0;
+  size_t bytes = 0;
+  int rc = f_route_rows(T, k, E, align, &rows);
+  if (rc == ADALN_OK) rc = f_route_ws(T, k, E, &bytes);
+  if (rc != ADALN_OK) return refused(rc, "adaln_route");
+  Ref device(PyObject_GetAttr(a[0], n_device)), row, starts, counts, work;
+  void *row_p, *starts_p, *counts_p, *ws = nullptr, *stream;
+  if (!device || !array_out(a[3], "row", 2, T, k, g_i32, device.p, x.dev, &row, &row_p) ||
+      !array_out(a[4], "starts", 1, (int64_t)E + 1, 0, g_i32, device.p, x.dev, &starts, &starts_p) ||
+      !array_out(a[5], "counts", 1, E, 0, g_i32, device.p, x.dev, &counts, &counts_p))
+    return nullptr;
+  if (!none(a[6])) {
+    if (!buffer(a[6], "workspace", x.dev, &ws, &bytes)) return nullptr;
+  } else if (bytes > 0) {
+    work.set(new_bytes(bytes, device.p));
+    if (!work || !pointer(work.p, &ws)) return nullptr;
+  }
+  if (!stream_of(a[7], x.dev, &stream)) return nullptr;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_route(static_cast<const int32_t*>(x.ptr), T, k, E, align, static_cast<int32_t*>(row_p),
+               static_cast<int32_t*>(starts_p), static_cast<int32_t*>(counts_p), ws, bytes, stream);
+  Py_END_ALLOW_THREADS;
+  if (rc != ADALN_OK) return refused(rc, "adaln_route");
+  Ref size(PyLong_FromLongLong(rows));
+  return size ? PyTuple_Pack(4, row.p, starts.p, counts.p, size.p) : nullptr;
+}
+
+struct Routed {
+  int64_t T, rows;
+  int32_t k, E, align;
+  const int32_t *row, *starts, *counts;
+};
+
+// (row, starts, counts, rows, align), on device `dev`.
+bool route_of(PyObject* o, long dev, Routed* r) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) {
+    PyErr_SetString(PyExc_TypeError, "a route, as adaln_route returns it, is needed");
+    return false;
+  }
+  Tensor row, starts, counts;
+  Tensor* const t[3] = {&row, &starts, &counts};
+  const char* const names[3] = {"row", "starts", "counts"};
+  for (int i = 0; i < 3; ++i) {
+    PyObject* const x = PyTuple_GET_ITEM(o, i);
+    if (!read(x, names[i], t[i], false) || !on_device(*t[i], names[i], dev) || !contiguous(x, names[i]) ||
+        !of_dtype(*t[i], names[i], g_i32))
+      return false;
+  }
+  if (row.ndim != 2 || counts.ndim != 1 || row.shape[1] > INT32_MAX || counts.shape[0] > INT32_MAX) {
+    PyErr_SetString(PyExc_ValueError, "row must be [T, k] and counts [E]");
+    return false;
+  }
+  if (!of_shape(starts, "starts", 1, counts.shape[0] + 1)) return false;
+  r->rows = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 3));
+  if (r->rows == -1 && PyErr_Occurred()) return false;
+  if (!positive(PyTuple_GET_ITEM(o, 4), "align", &r->align)) return false;
+  r->T = row.shape[0], r->k = (int32_t)row.shape[1], r->E = (int32_t)counts.shape[0];
+  r->row = static_cast<const int32_t*>(row.ptr);
+  r->starts = static_cast<const int32_t*>(starts.ptr);
+  r->counts = static_cast<const int32_t*>(counts.ptr);
+  return true;
+}
+
+struct Copied {
+  Tensor x;
+  int32_t D;
+  int code;
+  Routed r;
+};
+
+// x [T, D], or [rows, D] where `sorted`, and its route.
+bool copy_args(PyObject* x, const char* name, bool sorted, PyObject* route, Copied* c) {
+  if (!read(x, name, &c->x, false) || !contiguous(x, name) || !route_of(route, c->x.dev, &c->r)) return false;
+  if (c->x.ndim != 2 || c->x.shape[1] > INT32_MAX) {
+    PyErr_Format(PyExc_ValueError, "%s must be [%s, D]", name, sorted ? "rows" : "T");
+    return false;
+  }
+  c->D = (int32_t)c->x.shape[1];
+  return of_shape(c->x, name, 2, sorted ? c->r.rows : c->r.T, c->D) &&
+         (c->code = dtype_code(c->x.dtype)) >= 0;
+}
+bool weights_of(PyObject* w, const Copied& c, const float** out) {
+  void* p;
+  if (!matrix(w, "weight", c.r.T, c.r.k, g_f32, c.x.dev, &p)) return false;
+  *out = static_cast<const float*>(p);
+  return true;
+}
+
+// expert_sort_fwd(x, route, xs, stream) -> xs
+PyObject* expert_sort_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "4 arguments");
+    return nullptr;
+  }
+  Copied c;
+  void *to, *stream;
+  if (!copy_args(a[0], "x", false, a[1], &c)) return nullptr;
+  Ref out, device(PyObject_GetAttr(a[0], n_device));
+  if (!device || !array_out(a[2], "xs", 2, c.r.rows, c.D, c.x.dtype, device.p, c.x.dev, &out, &to) ||
+      !stream_of(a[3], c.x.dev, &stream))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_sort_fwd(c.x.ptr, c.r.row, c.r.starts, c.r.counts, c.r.T, c.r.k, c.r.E, c.r.align, c.D,
+                  (adaln_dtype_t)c.code, c.r.rows, to, stream);
+  Py_END_ALLOW_THREADS;
+  return rc != ADALN_OK ? refused(rc, "adaln_expert_sort_fwd") : out.take();
+}
+
+// expert_sort_bwd(dxs, route, dx, stream) -> dx
+PyObject* expert_sort_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "4 arguments");
+    return nullptr;
+  }
+  Copied c;
+  void *to, *stream;
+  if (!copy_args(a[0], "dxs", true, a[1], &c)) return nullptr;
+  Ref out, device(PyObject_GetAttr(a[0], n_device));
+  if (!device || !array_out(a[2], "dx", 2, c.r.T, c.D, c.x.dtype, device.p, c.x.dev, &out, &to) ||
+      !stream_of(a[3], c.x.dev, &stream))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_sort_bwd(c.x.ptr, c.r.row, c.r.T, c.r.k, c.D, (adaln_dtype_t)c.code, c.r.rows, to, stream);
+  Py_END_ALLOW_THREADS;
+  return rc != ADALN_OK ? refused(rc, "adaln_expert_sort_bwd") : out.take();
+}
+
+// expert_combine_fwd(ys, weight, route, y, stream) -> y
+PyObject* expert_combine_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 5) {
+    PyErr_SetString(PyExc_TypeError, "5 arguments");
+    return nullptr;
+  }
+  Copied c;
+  const float* weight;
+  void *to, *stream;
+  if (!copy_args(a[0], "ys", true, a[2], &c) || !weights_of(a[1], c, &weight)) return nullptr;
+  Ref out, device(PyObject_GetAttr(a[0], n_device));
+  if (!device || !array_out(a[3], "y", 2, c.r.T, c.D, c.x.dtype, device.p, c.x.dev, &out, &to) ||
+      !stream_of(a[4], c.x.dev, &stream))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_combine_fwd(c.x.ptr, weight, c.r.row, c.r.T, c.r.k, c.D, (adaln_dtype_t)c.code, c.r.rows, to,
+                     stream);
+  Py_END_ALLOW_THREADS;
+  return rc != ADALN_OK ? refused(rc, "adaln_expert_combine_fwd") : out.take();
+}
+
+// expert_combine_bwd(dy, ys, weight, route, dys, dweight, stream) -> (dys, dweight)
+PyObject* expert_combine_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "7 arguments");
+    return nullptr;
+  }
+  Copied c;
+  const float* weight;
+  void *ys, *to, *dw, *stream;
+  if (!copy_args(a[0], "dy", false, a[3], &c) || !weights_of(a[2], c, &weight) ||
+      !matrix(a[1], "ys", c.r.rows, c.D, c.x.dtype, c.x.dev, &ys))
+    return nullptr;
+  Ref dys, dweight, device(PyObject_GetAttr(a[0], n_device));
+  if (!device || !array_out(a[4], "dys", 2, c.r.rows, c.D, c.x.dtype, device.p, c.x.dev, &dys, &to) ||
+      !array_out(a[5], "dweight", 2, c.r.T, c.r.k, g_f32, device.p, c.x.dev, &dweight, &dw) ||
+      !stream_of(a[6], c.x.dev, &stream))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_combine_bwd(c.x.ptr, ys, weight, c.r.row, c.r.starts, c.r.counts, c.r.T, c.r.k, c.r.E, c.r.align,
+                     c.D, (adaln_dtype_t)c.code, c.r.rows, to, static_cast<float*>(dw), stream);
+  Py_END_ALLOW_THREADS;
+  return rc != ADALN_OK ? refused(rc, "adaln_expert_combine_bwd") : pair_or(dys, dweight);
+}
+
 // ----- module --------------------------------------------------------------------------------
 
 template <class F>
@@ -794,7 +1024,13 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !entry(a[3], "adaln_ffn_saved_size", &f_ffn_saved) ||
       !entry(a[3], "adaln_ffn_workspace_size", &f_ffn_ws) ||
       !entry(a[3], "adaln_dropout_fwd", &f_drop_fwd) || !entry(a[3], "adaln_dropout_bwd", &f_drop_bwd) ||
-      !entry(a[3], "adaln_dropout_bwd_workspace_size", &f_drop_ws))
+      !entry(a[3], "adaln_dropout_bwd_workspace_size", &f_drop_ws) ||
+      !entry(a[3], "adaln_route_rows", &f_route_rows) ||
+      !entry(a[3], "adaln_route_workspace_size", &f_route_ws) || !entry(a[3], "adaln_route", &f_route) ||
+      !entry(a[3], "adaln_expert_sort_fwd", &f_sort_fwd) ||
+      !entry(a[3], "adaln_expert_sort_bwd", &f_sort_bwd) ||
+      !entry(a[3], "adaln_expert_combine_fwd", &f_combine_fwd) ||
+      !entry(a[3], "adaln_expert_combine_bwd", &f_combine_bwd))
     return nullptr;
   Py_RETURN_NONE;
 }
@@ -807,10 +1043,15 @@ PyMethodDef methods[] = {
     {"ffn_bwd", (PyCFunction)(void (*)(void))ffn_bwd, METH_FASTCALL, nullptr},
     {"dropout_fwd", (PyCFunction)(void (*)(void))dropout_fwd, METH_FASTCALL, nullptr},
     {"dropout_bwd", (PyCFunction)(void (*)(void))dropout_bwd, METH_FASTCALL, nullptr},
+    {"route", (PyCFunction)(void (*)(void))route, METH_FASTCALL, nullptr},
+    {"expert_sort_fwd", (PyCFunction)(void (*)(void))expert_sort_fwd, METH_FASTCALL, nullptr},
+    {"expert_sort_bwd", (PyCFunction)(void (*)(void))expert_sort_bwd, METH_FASTCALL, nullptr},
+    {"expert_combine_fwd", (PyCFunction)(void (*)(void))expert_combine_fwd, METH_FASTCALL, nullptr},
+    {"expert_combine_bwd", (PyCFunction)(void (*)(void))expert_combine_bwd, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding",
-                      "Argument marshalling of the rotary, feed-forward and dropout calls.", -1, methods,
+                      "Argument marshalling of every call but the AdaLN's.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

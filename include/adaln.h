@@ -2,9 +2,10 @@
  * libadaln -- operators of video diffusion transformer blocks for GB300
  * (sm_103a): the fused AdaLN LayerNorm-Modulate, described here, and, further
  * down, rotary positions with the norm of queries and keys (adaln_qk_rope_*),
- * the gated feed-forward block (adaln_ffn_*) and dropout with the gate and the
- * residual of a branch (adaln_dropout_*), which share its conventions on
- * ownership, streams, errors and the status word.
+ * the gated feed-forward block (adaln_ffn_*), dropout with the gate and the
+ * residual of a branch (adaln_dropout_*) and tokens sorted by expert and back
+ * (adaln_route, adaln_expert_*), which share its conventions on ownership, streams,
+ * errors and the status word.
  *
  * The AdaLN is the fused adaptive LayerNorm of video / MMDiT diffusion
  * transformers described in "AdaptiveLoad: Towards Efficient Video Diffusion
@@ -89,6 +90,9 @@ extern "C" {
 #define ADALN_FFN_MAX_T (1 << 24)
 #define ADALN_FFN_MAX_DIM (1 << 18)
 #define ADALN_DROPOUT_MAX_D (1 << 18)
+#define ADALN_MAX_EXPERTS 256
+#define ADALN_MAX_TOPK 32
+#define ADALN_MAX_ROUTE_ALIGN 4096
 
 typedef enum {
   ADALN_F32 = 0,  /* IEEE binary32 */
@@ -106,7 +110,8 @@ typedef enum {
   ADALN_ERR_CUDA = 7,      /* a CUDA runtime call or launch failed */
   ADALN_ERR_ARG = 8,       /* eps negative or not finite; bad trace argument */
   ADALN_ERR_TIMEOUT = 9,   /* device status: an internal pipeline wait gave up */
-  ADALN_ERR_POS = 10       /* device status: a rotary position outside the table */
+  ADALN_ERR_POS = 10,      /* device status: a rotary position outside the table */
+  ADALN_ERR_EXPERT = 11    /* device status: an expert, or a sorted row, out of range */
 } adaln_status_t;
 
 /* Bits of the device status word (adaln_get_status). */
@@ -114,6 +119,8 @@ typedef enum {
 #define ADALN_DEV_SEG_ORDER 2u   /* seg_id decreased from one row to the next */
 #define ADALN_DEV_TIMEOUT 4u     /* a bounded wait on a copy pipeline expired */
 #define ADALN_DEV_POS_RANGE 8u   /* a rotary position was outside [-1, rows) */
+#define ADALN_DEV_EXPERT_RANGE 16u /* an expert was outside [-1, E), or a sorted row or
+                                      an expert's start outside what the call was given */
 
 /*
  * Forward (section 2.B, forward pass): per-row statistics reduced on chip and
@@ -416,10 +423,66 @@ ADALN_API int adaln_dropout_bwd(const void* dy, const void* h, const void* gate,
               size_t workspace_bytes, void* stream);
 
 /*
+ * Tokens sorted by expert, and back, for a feed-forward block that is a mixture of
+ * experts.  expert [T, k] holds each token's choices (-1: none, a padded token's
+ * say; a token may name an expert twice).  A sorted array [rows, D] has expert 0's
+ * pairs (t, j) first, in the order t k + j, then expert 1's, each expert's start
+ * rounded up to a multiple of `align` rows; its rows between an expert's last and
+ * the next one's start are zeros, and rows from starts[E] on are left as they were.
+ *
+ *   row [T, k]    each pair's row, -1 for expert -1
+ *   starts [E+1]  each expert's first row, and the end of the last one's
+ *   counts [E]    each expert's pairs
+ *
+ * all int32, in device memory: nothing here waits for the host.  `rows` is at least
+ * adaln_route_rows: T k + min(E, T k) (align - 1), rounded down to whole `align`.
+ * One launch; two above 16384 pairs, which need the workspace
+ * (adaln_route_workspace_size bytes, 0 otherwise, 16-byte aligned).  An expert
+ * outside [-1, E) counts as -1 and is recorded (ADALN_DEV_EXPERT_RANGE).  T = 0
+ * writes starts and counts.
+ *
+ * Errors: ADALN_ERR_DIM for T outside [0, 2^31), k outside [1, ADALN_MAX_TOPK], E
+ * outside [1, ADALN_MAX_EXPERTS], align outside [1, ADALN_MAX_ROUTE_ALIGN] or rows
+ * above 2^31 - 1; ADALN_ERR_NULL, ADALN_ERR_ALIGN, ADALN_ERR_WORKSPACE.
+ */
+ADALN_API int adaln_route_rows(int64_t T, int32_t k, int32_t E, int32_t align, int64_t* rows);
+ADALN_API int adaln_route_workspace_size(int64_t T, int32_t k, int32_t E, size_t* bytes);
+ADALN_API int adaln_route(const int32_t* expert, int64_t T, int32_t k, int32_t E, int32_t align,
+              int32_t* row, int32_t* starts, int32_t* counts, void* workspace,
+              size_t workspace_bytes, void* stream);
+
+/*
+ * xs[row[t, j]] = x[t], and the gradient dx[t] = sum_j dxs[row[t, j]] (fp32 sums, j
+ * in order).  x, dx [T, D] and xs, dxs [rows, D] have the element type `dtype`, D as
+ * for the dropout.  A row outside [-1, rows) is skipped and recorded
+ * (ADALN_DEV_EXPERT_RANGE).  T = 0 does nothing.  Outputs may not overlap inputs.
+ * Errors as above and ADALN_ERR_DTYPE.
+ */
+ADALN_API int adaln_expert_sort_fwd(const void* x, const int32_t* row, const int32_t* starts,
+              const int32_t* counts, int64_t T, int32_t k, int32_t E, int32_t align, int32_t D,
+              adaln_dtype_t dtype, int64_t rows, void* xs, void* stream);
+ADALN_API int adaln_expert_sort_bwd(const void* dxs, const int32_t* row, int64_t T, int32_t k,
+              int32_t D, adaln_dtype_t dtype, int64_t rows, void* dx, void* stream);
+
+/*
+ * y[t] = sum_j weight[t, j] ys[row[t, j]] with weight fp32 [T, k], and its gradients
+ * dys[row[t, j]] = weight[t, j] dy[t] (zeros between the experts, as in xs) and, fp32
+ * [T, k], dweight[t, j] = <dy[t], ys[row[t, j]]> (0 for expert -1).  No atomics:
+ * bitwise reproducible.  Otherwise as the sort.
+ */
+ADALN_API int adaln_expert_combine_fwd(const void* ys, const float* weight, const int32_t* row,
+              int64_t T, int32_t k, int32_t D, adaln_dtype_t dtype, int64_t rows, void* y,
+              void* stream);
+ADALN_API int adaln_expert_combine_bwd(const void* dy, const void* ys, const float* weight,
+              const int32_t* row, const int32_t* starts, const int32_t* counts, int64_t T,
+              int32_t k, int32_t E, int32_t align, int32_t D, adaln_dtype_t dtype, int64_t rows,
+              void* dys, float* dweight, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the status word: the one the
  * calling thread bound (adaln_status_bind), else the current device's.
  * *host_bits (if non-NULL) receives the ADALN_DEV_* bits.  Returns ADALN_OK,
- * ADALN_ERR_SEG, ADALN_ERR_POS, ADALN_ERR_TIMEOUT or ADALN_ERR_CUDA.  The device's word is
+ * ADALN_ERR_SEG, ADALN_ERR_POS, ADALN_ERR_EXPERT, ADALN_ERR_TIMEOUT or ADALN_ERR_CUDA.  The device's word is
  * shared by all calls on the device that use it since it was last cleared.
  */
 ADALN_API int adaln_get_status(uint32_t* host_bits, void* stream);
@@ -449,8 +512,9 @@ ADALN_API const char* adaln_strerror(int code);
  * `capacity` launches.  adaln_trace_end() synchronises those events and sums
  * the elapsed time per kernel; adaln_trace_get() reads the sums.
  * Kernel ids: ADALN_KERNEL_FWD, ADALN_KERNEL_BWD_ROWS, ADALN_KERNEL_BWD_FINALIZE;
- * ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN and ADALN_KERNEL_DROPOUT count every
- * launch of the rotary, the feed-forward and the dropout calls (5 is no id).
+ * ADALN_KERNEL_QK_ROPE, ADALN_KERNEL_FFN, ADALN_KERNEL_DROPOUT and
+ * ADALN_KERNEL_EXPERTS count every launch of the rotary, the feed-forward, the
+ * dropout and the experts' calls (5 is no id).
  */
 #define ADALN_KERNEL_FWD 0
 #define ADALN_KERNEL_BWD_ROWS 1
@@ -458,7 +522,8 @@ ADALN_API const char* adaln_strerror(int code);
 #define ADALN_KERNEL_QK_ROPE 3
 #define ADALN_KERNEL_FFN 4
 #define ADALN_KERNEL_DROPOUT 6
-#define ADALN_NUM_KERNELS 7
+#define ADALN_KERNEL_EXPERTS 7
+#define ADALN_NUM_KERNELS 8
 ADALN_API int adaln_trace_begin(int capacity);
 ADALN_API int adaln_trace_end(void);
 ADALN_API int adaln_trace_get(int kernel_id, int64_t* launches, double* total_ms);

@@ -130,3 +130,108 @@ def test_dropout_saves_h_for_a_gates_gradient_only(lib, monkeypatch):
     m = autograd.GatedResidual(0.5).eval()
     m(x, h, gate, seg)
     assert seen[0][2] == 0.0
+
+
+def route(lib, **kw):
+    a = dict(expert=A, T=10, k=2, E=4, align=64, row=B, starts=B, counts=B, ws=B, wsb=1 << 30)
+    a.update(kw)
+    return lib.raw.adaln_route(*a.values(), None)
+
+
+def sort_fwd(lib, **kw):
+    a = dict(x=A, row=A, starts=A, counts=A, T=10, k=2, E=4, align=64, D=64, dt=lib.ADALN_BF16, rows=256,
+             xs=B)
+    a.update(kw)
+    return lib.raw.adaln_expert_sort_fwd(*a.values(), None)
+
+
+def sort_bwd(lib, **kw):
+    a = dict(dxs=A, row=A, T=10, k=2, D=64, dt=lib.ADALN_BF16, rows=256, dx=B)
+    a.update(kw)
+    return lib.raw.adaln_expert_sort_bwd(*a.values(), None)
+
+
+def combine_fwd(lib, **kw):
+    a = dict(ys=A, weight=A, row=A, T=10, k=2, D=64, dt=lib.ADALN_BF16, rows=256, y=B)
+    a.update(kw)
+    return lib.raw.adaln_expert_combine_fwd(*a.values(), None)
+
+
+def combine_bwd(lib, **kw):
+    a = dict(dy=A, ys=A, weight=A, row=A, starts=A, counts=A, T=10, k=2, E=4, align=64, D=64,
+             dt=lib.ADALN_BF16, rows=256, dys=B, dw=B)
+    a.update(kw)
+    return lib.raw.adaln_expert_combine_bwd(*a.values(), None)
+
+
+def test_route_refusals(lib):
+    for bad in (dict(T=-1), dict(T=2 ** 31), dict(k=0), dict(k=33), dict(E=0), dict(E=257), dict(align=0),
+                dict(align=4097), dict(T=2 ** 31 - 1), dict(T=2 ** 30 - 1, E=256, align=4096)):
+        assert route(lib, **bad) == lib.ADALN_ERR_DIM, bad
+    for k in ("expert", "row", "starts", "counts"):
+        assert route(lib, **{k: None}) == lib.ADALN_ERR_NULL, k
+        assert route(lib, **{k: A + 2}) == lib.ADALN_ERR_ALIGN, k
+    big = dict(T=20000)
+    assert route(lib, ws=None, **big) == lib.ADALN_ERR_NULL
+    assert route(lib, ws=A + 8, **big) == lib.ADALN_ERR_ALIGN
+    assert route(lib, wsb=16, **big) == lib.ADALN_ERR_WORKSPACE
+    assert route(lib, T=0, starts=None) == lib.ADALN_ERR_NULL
+    n = ctypes.c_int64(0)
+    for (T, k, E, align), rows in (((10, 2, 4, 64), 256), ((0, 2, 4, 64), 0), ((1, 2, 8, 64), 128),
+                                   ((5, 3, 8, 1), 15), ((100, 1, 2, 64), 192)):
+        assert lib.raw.adaln_route_rows(T, k, E, align, ctypes.byref(n)) == lib.ADALN_OK
+        assert n.value == rows, (T, k, E, align)
+    assert lib.raw.adaln_route_rows(1, 1, 1, 1, None) == lib.ADALN_ERR_NULL
+    assert lib.adaln_route_workspace_size(8192, 2, 256) == 0 < lib.adaln_route_workspace_size(8193, 2, 1)
+
+
+@pytest.mark.parametrize("call", [sort_fwd, sort_bwd, combine_fwd, combine_bwd])
+def test_expert_copy_refusals(lib, call):
+    names = call(lib, T=0) == lib.ADALN_OK and {
+        sort_fwd: ("x", "row", "starts", "counts", "xs"), sort_bwd: ("dxs", "row", "dx"),
+        combine_fwd: ("ys", "weight", "row", "y"),
+        combine_bwd: ("dy", "ys", "weight", "row", "starts", "counts", "dys", "dw")}[call]
+    assert call(lib, dt=2) == lib.ADALN_ERR_DTYPE
+    for bad in (dict(T=-1), dict(T=2 ** 31), dict(k=0), dict(k=33), dict(D=0), dict(D=12), dict(D=2 ** 18 + 8),
+                dict(rows=-1), dict(rows=2 ** 31)):
+        assert call(lib, **bad) == lib.ADALN_ERR_DIM, bad
+    if "starts" in names:
+        for bad in (dict(E=0), dict(E=257), dict(align=0), dict(align=4097)):
+            assert call(lib, **bad) == lib.ADALN_ERR_DIM, bad
+    for k in names:
+        assert call(lib, **{k: None}) == lib.ADALN_ERR_NULL, k
+        assert call(lib, **{k: A + 2}) == lib.ADALN_ERR_ALIGN, k
+        assert call(lib, **{k: None}, T=0) == lib.ADALN_OK, k
+
+
+def test_expert_statuses(lib):
+    assert lib.strerror(lib.ADALN_ERR_EXPERT) != lib.strerror(12345)
+    n, ms = ctypes.c_int64(-1), ctypes.c_double(-1)
+    assert lib.raw.adaln_trace_get(lib.ADALN_KERNEL_EXPERTS, ctypes.byref(n), ctypes.byref(ms)) == lib.ADALN_OK
+
+
+def test_expert_nodes_keep_shapes_and_types(lib, monkeypatch):
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    L = autograd._lib
+    monkeypatch.setattr(L, "adaln_route", lambda e, E, align: L.Route(
+        e, torch.zeros(E + 1, dtype=torch.int32), torch.zeros(E, dtype=torch.int32), 7, align))
+    monkeypatch.setattr(L, "adaln_expert_sort_fwd", lambda x, r: torch.ones(r.rows, x.shape[1]))
+    monkeypatch.setattr(L, "adaln_expert_sort_bwd", lambda d, r: torch.full((len(r.row), d.shape[1]), 2.0))
+    monkeypatch.setattr(L, "adaln_expert_combine_fwd", lambda ys, w, r: torch.ones(len(r.row), ys.shape[1]))
+    monkeypatch.setattr(L, "adaln_expert_combine_bwd", lambda d, ys, w, r: (ys * 0 + 3, w * 0 + 4))
+    x = torch.zeros(2, 5, 8, requires_grad=True)
+    weight = torch.zeros(2, 5, 3, dtype=torch.bfloat16, requires_grad=True)
+    r = autograd.route(torch.zeros(2, 5, 3, dtype=torch.int64), 4)
+    assert r.row.shape == (10, 3) and r.row.dtype == torch.int32
+    xs = autograd.expert_sort(x, r)
+    xs.retain_grad()
+    y = autograd.expert_combine(xs, weight, r)
+    assert xs.shape == (7, 8) and y.shape == (2, 5, 8)
+    y.sum().backward()
+    assert torch.equal(xs.grad, torch.full((7, 8), 3.0)) and torch.equal(x.grad, torch.full((2, 5, 8), 2.0))
+    assert weight.grad.dtype == torch.bfloat16 and weight.grad.shape == (2, 5, 3)
+    for out, leaf in ((autograd.expert_sort(x, r), x), (autograd.expert_combine(xs.detach(), weight, r), weight)):
+        first, = torch.autograd.grad((out * out).sum(), leaf, create_graph=True)
+        with pytest.raises(RuntimeError, match="twice"):
+            first.sum().backward()
