@@ -40,7 +40,9 @@ EXPORTS = ["adaln_fwd", "adaln_bwd_workspace_size", "adaln_bwd", "adaln_bwd_noal
            "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_dropout_fwd",
            "adaln_dropout_bwd_workspace_size", "adaln_dropout_bwd", "adaln_route_rows",
            "adaln_route_workspace_size", "adaln_route", "adaln_expert_sort_fwd",
-           "adaln_expert_sort_bwd", "adaln_expert_combine_fwd", "adaln_expert_combine_bwd"]
+           "adaln_expert_sort_bwd", "adaln_expert_combine_fwd", "adaln_expert_combine_bwd",
+           "adaln_experts_ffn_saved_size", "adaln_experts_ffn_workspace_size",
+           "adaln_experts_ffn_fwd", "adaln_experts_ffn_bwd"]
 
 
 class AdalnError(RuntimeError):
@@ -156,6 +158,16 @@ def _load():
     lib.adaln_expert_combine_bwd.restype = ci
     lib.adaln_expert_combine_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, ci, i64,
                                              vp, vp, vp]
+    lib.adaln_experts_ffn_saved_size.restype = ci
+    lib.adaln_experts_ffn_saved_size.argtypes = [i64, i32, i32, i32, ci, sp]
+    lib.adaln_experts_ffn_workspace_size.restype = ci
+    lib.adaln_experts_ffn_workspace_size.argtypes = [i64, i32, i32, i32, ci, sp, sp]
+    lib.adaln_experts_ffn_fwd.restype = ci
+    lib.adaln_experts_ffn_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, i32, ci, ci, vp, vp, vp,
+                                          ctypes.c_size_t, vp]
+    lib.adaln_experts_ffn_bwd.restype = ci
+    lib.adaln_experts_ffn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, ci, ci, vp, vp,
+                                          vp, vp, vp, ctypes.c_size_t, vp]
     lib.adaln_selftest_wait_timeout.restype = ci
     lib.adaln_selftest_wait_timeout.argtypes = [ctypes.c_uint32, vp]
     lib.adaln_launch_shape.restype = ci
@@ -176,7 +188,9 @@ def _load_binding():
                "adaln_ffn_fwd", "adaln_ffn_bwd", "adaln_ffn_saved_size", "adaln_ffn_workspace_size",
                "adaln_dropout_fwd", "adaln_dropout_bwd", "adaln_dropout_bwd_workspace_size",
                "adaln_route_rows", "adaln_route_workspace_size", "adaln_route", "adaln_expert_sort_fwd",
-               "adaln_expert_sort_bwd", "adaln_expert_combine_fwd", "adaln_expert_combine_bwd")
+               "adaln_expert_sort_bwd", "adaln_expert_combine_fwd", "adaln_expert_combine_bwd",
+               "adaln_experts_ffn_saved_size", "adaln_experts_ffn_workspace_size",
+               "adaln_experts_ffn_fwd", "adaln_experts_ffn_bwd")
     _binding.setup(torch, torch._C._cuda_getCurrentRawStream, AdalnError,
                    {n: ctypes.cast(getattr(raw, n), ctypes.c_void_p).value for n in entries})
     return _binding
@@ -564,6 +578,45 @@ def adaln_expert_combine_fwd(ys, weight, route, y=None, stream=None):
 def adaln_expert_combine_bwd(dy, ys, weight, route, dys=None, dweight=None, stream=None):
     """Backward of adaln_expert_combine_fwd: (dys, dweight), dys as the sort's xs."""
     return _on(dy, stream, _binding.expert_combine_bwd, dy, ys, weight, route, dys, dweight)
+
+
+def adaln_experts_ffn_saved_size(rows, E, D, F, dtype=torch.bfloat16):
+    """Bytes that adaln_experts_ffn_fwd saves for adaln_experts_ffn_bwd."""
+    n = ctypes.c_size_t(0)
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    _check(raw.adaln_experts_ffn_saved_size(int(rows), int(E), int(D), int(F), code, ctypes.byref(n)),
+           "adaln_experts_ffn_saved_size")
+    return n.value
+
+
+def adaln_experts_ffn_workspace_size(rows, E, D, F, dtype=torch.bfloat16):
+    """Workspace bytes of (adaln_experts_ffn_fwd, adaln_experts_ffn_bwd) on the current
+    device."""
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    _check(raw.adaln_experts_ffn_workspace_size(int(rows), int(E), int(D), int(F), code, ctypes.byref(f),
+                                                ctypes.byref(b)), "adaln_experts_ffn_workspace_size")
+    return f.value, b.value
+
+
+def adaln_experts_ffn_fwd(xs, wg, wu, wd, starts, act="silu", save=False, ys=None, saved=None,
+                          workspace=None, stream=None):
+    """ys = (act(xs wg[e]') * (xs wu[e]')) wd[e]' on each expert's rows of bf16 xs [rows, D],
+    wg, wu [E, F, D], wd [E, D, F]; starts int32 [E + 1] as a Route of align 64 (or a
+    multiple) has them; rows from starts[-1] on are not written.  With `save` (or a
+    `saved` buffer of adaln_experts_ffn_saved_size bytes) also keeps what the backward
+    needs.  Returns (ys, saved), saved None without."""
+    return _on(xs, stream, _binding.experts_ffn_fwd, xs, wg, wu, wd, starts, _act(act), save, ys, saved,
+               workspace)
+
+
+def adaln_experts_ffn_bwd(dys, xs, wg, wu, wd, starts, saved, act="silu", dxs=None, dwg=None, dwu=None,
+                          dwd=None, workspace=None, stream=None):
+    """Backward of adaln_experts_ffn_fwd, from its inputs and what it saved.  Returns
+    (dxs, dwg, dwu, dwd), all bf16; the weight gradients of an expert without rows are
+    zeros.  xs and dys have zeros in the rows between the experts' tokens."""
+    return _on(xs, stream, _binding.experts_ffn_bwd, dys, xs, wg, wu, wd, starts, saved, _act(act), dxs,
+               dwg, dwu, dwd, workspace)
 
 
 def adaln_get_status(stream=None, device=None):

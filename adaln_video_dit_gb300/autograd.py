@@ -1,6 +1,6 @@
 """The operators as autograd nodes: the fused AdaLN, the rotary positions and
 norm of queries and keys, the gated feed-forward block, dropout with the gate and
-the residual of a branch, and tokens sorted by expert and back.
+the residual of a branch, and feed-forward blocks that are mixtures of experts.
 
 AdaptiveLoad (Technical summary, section 2.B, "graph simplification"): the
 LayerNorm -> multiply -> add chain of an adaLN modulation site collapses into
@@ -330,3 +330,70 @@ def expert_combine(ys, weight, route):
     weighted with its choice's weight [..., k], and summed: [..., D]
     (differentiable in ys and weight)."""
     return ExpertCombineFunction.apply(ys, weight, *route)
+
+
+class ExpertsFFNFunction(torch.autograd.Function):
+    """ys = (act(xs wg[e]') * (xs wu[e]')) wd[e]' on each expert's rows, saving xs and the
+    two projections; without a gradient to come, nothing (`grad`: as for the block)."""
+
+    @staticmethod
+    def forward(ctx, xs, wg, wu, wd, starts, act, grad):
+        xs, wg, wu, wd = xs.contiguous(), wg.contiguous(), wu.contiguous(), wd.contiguous()
+        ys, saved = _lib.adaln_experts_ffn_fwd(xs, wg, wu, wd, starts, act=act,
+                                               save=grad and any(ctx.needs_input_grad))
+        ctx.save_for_backward(xs, wg, wu, wd, starts, saved)
+        ctx.act = act
+        return ys
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dys):
+        xs, wg, wu, wd, starts, saved = ctx.saved_tensors
+        return (*_lib.adaln_experts_ffn_bwd(dys.to(xs.dtype).contiguous(), xs, wg, wu, wd, starts, saved,
+                                            act=ctx.act), None, None, None)
+
+
+def experts_ffn(xs, wg, wu, wd, route, act="silu"):
+    """The gated feed-forward block of each expert on its rows of bf16 xs [route.rows,
+    D], as expert_sort gives them (align a multiple of 64), with wg, wu [E, F, D], wd
+    [E, D, F] (differentiable).  Rows between the experts' are zeros, here and in the
+    gradients; rows from route.starts[-1] on hold nothing."""
+    return ExpertsFFNFunction.apply(xs, wg, wu, wd, route.starts, act, torch.is_grad_enabled())
+
+
+class MixtureFFN(torch.nn.Module):
+    """A mixture of `experts` gated feed-forward blocks (bf16, no biases), of which every
+    token of x [..., D] takes the top_k that a linear router gives the largest
+    softmax probabilities, weighted with those, scaled to a sum of one.  Tokens whose
+    `mask` [...] is false go to no expert: their output is zero.
+
+    The whole runs on the device: how many tokens an expert gets is never asked for."""
+
+    def __init__(self, dim, hidden, experts, top_k=2, act="silu", device=None):
+        super().__init__()
+        if act not in _lib.ACTS:
+            raise ValueError(f"act must be one of {sorted(_lib.ACTS)}, got {act!r}")
+        if not 1 <= top_k <= experts:
+            raise ValueError(f"top_k must be in [1, {experts}], got {top_k}")
+
+        def weight(rows, cols):
+            w = torch.empty(experts, rows, cols, device=device, dtype=torch.bfloat16)
+            return torch.nn.Parameter(torch.nn.init.normal_(w, std=cols ** -0.5))
+
+        self.wg, self.wu, self.wd = weight(hidden, dim), weight(hidden, dim), weight(dim, hidden)
+        self.router = torch.nn.Parameter(
+            torch.nn.init.normal_(torch.empty(experts, dim, device=device), std=dim ** -0.5))
+        self.experts, self.top_k, self.act = experts, top_k, act
+
+    def forward(self, x, mask=None):
+        # (The router's few products in 32 bits: its probabilities choose the experts.)
+        p, expert = (x.float() @ self.router.t()).softmax(-1).topk(self.top_k, -1)
+        if mask is not None:
+            expert = torch.where(mask[..., None], expert, -1)
+        r = route(expert, self.experts)
+        ys = experts_ffn(expert_sort(x, r), self.wg, self.wu, self.wd, r, self.act)
+        return expert_combine(ys, p / p.sum(-1, keepdim=True), r)
+
+    def extra_repr(self):
+        return (f"dim={self.wg.shape[2]}, hidden={self.wg.shape[1]}, experts={self.experts}, "
+                f"top_k={self.top_k}, act={self.act!r}")

@@ -62,6 +62,10 @@ decltype(&adaln_expert_sort_fwd) f_sort_fwd;
 decltype(&adaln_expert_sort_bwd) f_sort_bwd;
 decltype(&adaln_expert_combine_fwd) f_combine_fwd;
 decltype(&adaln_expert_combine_bwd) f_combine_bwd;
+decltype(&adaln_experts_ffn_saved_size) f_experts_saved;
+decltype(&adaln_experts_ffn_workspace_size) f_experts_ws;
+decltype(&adaln_experts_ffn_fwd) f_experts_fwd;
+decltype(&adaln_experts_ffn_bwd) f_experts_bwd;
 
 // ----- reading tensors --------------------------------------------------------------
 
@@ -977,6 +981,168 @@ PyObject* expert_combine_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return rc != ADALN_OK ? refused(rc, "adaln_expert_combine_bwd") : pair_or(dys, dweight);
 }
 
+// ----- the experts' feed-forward ------------------------------------------------------------------
+
+// A contiguous [E, rows, cols] tensor.
+bool matrices(PyObject* t, const char* name, int64_t E, int64_t rows, int64_t cols, PyObject* dtype,
+              long dev, void** out) {
+  Tensor x;
+  if (!read(t, name, &x, false) || !on_device(x, name, dev) || !contiguous(t, name) ||
+      !of_dtype(x, name, dtype) || !of_shape(x, name, 3, E, rows, cols))
+    return false;
+  *out = x.ptr;
+  return true;
+}
+bool matrices_out(PyObject* given, const char* name, PyObject* like, int64_t E, int64_t rows, int64_t cols,
+                  PyObject* dtype, long dev, Ref* out, void** p) {
+  if (none(given)) {
+    out->set(PyObject_CallOneArg(g_empty_like, like));
+    return *out && pointer(out->p, p);
+  }
+  if (!matrices(given, name, E, rows, cols, dtype, dev, p)) return false;
+  Py_INCREF(given);
+  out->set(given);
+  return true;
+}
+
+struct Experts {
+  int64_t rows, E, D, F;
+  long dev;
+  PyObject* dtype;
+  int code;
+  void *xs, *wg, *wu, *wd;
+  const int32_t* starts;
+};
+
+bool experts_args(PyObject* xs, PyObject* wg, PyObject* wu, PyObject* wd, PyObject* starts, Experts* f) {
+  Tensor t, g, s;
+  if (!read(xs, "xs", &t, false) || !contiguous(xs, "xs") || !read(wg, "wg", &g, false)) return false;
+  if (t.ndim != 2 || g.ndim != 3) {
+    PyErr_SetString(PyExc_ValueError, "xs must be [rows, D] and wg [E, F, D]");
+    return false;
+  }
+  f->rows = t.shape[0], f->D = t.shape[1], f->E = g.shape[0], f->F = g.shape[1];
+  f->dev = t.dev, f->dtype = t.dtype, f->xs = t.ptr;
+  if (!matrices(wg, "wg", f->E, f->F, f->D, t.dtype, t.dev, &f->wg) ||
+      !matrices(wu, "wu", f->E, f->F, f->D, t.dtype, t.dev, &f->wu) ||
+      !matrices(wd, "wd", f->E, f->D, f->F, t.dtype, t.dev, &f->wd) || !read(starts, "starts", &s, false) ||
+      !on_device(s, "starts", t.dev) || !contiguous(starts, "starts") || !of_dtype(s, "starts", g_i32) ||
+      !of_shape(s, "starts", 1, f->E + 1))
+    return false;
+  f->starts = static_cast<const int32_t*>(s.ptr);
+  f->code = dtype_code(t.dtype);
+  if (f->code < 0) return false;
+  if (f->E > INT32_MAX || f->D > INT32_MAX || f->F > INT32_MAX) {
+    PyErr_SetString(PyExc_ValueError, "E, D or F too large");
+    return false;
+  }
+  return true;
+}
+
+bool experts_workspace(PyObject* given, const Experts& f, bool backward, PyObject* device, Ref* work,
+                       void** p, size_t* bytes) {
+  if (!none(given)) return buffer(given, "workspace", f.dev, p, bytes);
+  const int rc = f_experts_ws(f.rows, (int32_t)f.E, (int32_t)f.D, (int32_t)f.F, (adaln_dtype_t)f.code,
+                              backward ? nullptr : bytes, backward ? bytes : nullptr);
+  if (rc != ADALN_OK) {
+    refused(rc, "adaln_experts_ffn_workspace_size");
+    return false;
+  }
+  if (*bytes < 16) *bytes = 16;
+  work->set(new_bytes(*bytes, device));
+  return *work && pointer(work->p, p);
+}
+
+bool experts_saved(PyObject* given, const Experts& f, size_t* need, void** p) {
+  const int rc = f_experts_saved(f.rows, (int32_t)f.E, (int32_t)f.D, (int32_t)f.F, (adaln_dtype_t)f.code, need);
+  if (rc != ADALN_OK) {
+    refused(rc, "adaln_experts_ffn_saved_size");
+    return false;
+  }
+  if (none(given)) return true;
+  size_t have = 0;
+  if (!buffer(given, "saved", f.dev, p, &have)) return false;
+  if (have >= *need) return true;
+  PyErr_Format(PyExc_ValueError, "saved holds %zu bytes, %zu are needed", have, *need);
+  return false;
+}
+
+// experts_ffn_fwd(xs, wg, wu, wd, starts, act, save, ys, saved, workspace, stream)
+//   -> (ys, saved)
+PyObject* experts_ffn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 11) {
+    PyErr_SetString(PyExc_TypeError, "11 arguments");
+    return nullptr;
+  }
+  Experts f;
+  int save;
+  if (!experts_args(a[0], a[1], a[2], a[3], a[4], &f) || !flag(a[6], &save)) return nullptr;
+  const long act = PyLong_AsLong(a[5]);
+  if (act == -1 && PyErr_Occurred()) return nullptr;
+  Ref device(PyObject_GetAttr(a[0], n_device)), ys, saved, work;
+  void *yp, *sp = nullptr, *ws, *stream;
+  size_t need = 0, bytes = 0;
+  if (!device || !matrix_out(a[7], "ys", a[0], f.rows, f.D, f.dtype, f.dev, &ys, &yp)) return nullptr;
+  if (save || !none(a[8])) {
+    if (!experts_saved(a[8], f, &need, &sp)) return nullptr;
+    if (none(a[8])) {
+      saved.set(new_bytes(need, device.p));
+      if (!saved || !pointer(saved.p, &sp)) return nullptr;
+    } else {
+      Py_INCREF(a[8]);
+      saved.set(a[8]);
+    }
+  }
+  if (!experts_workspace(a[9], f, false, device.p, &work, &ws, &bytes) ||
+      !stream_of(a[10], f.dev, &stream))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_experts_fwd(f.xs, f.wg, f.wu, f.wd, f.starts, f.rows, (int32_t)f.E, (int32_t)f.D, (int32_t)f.F,
+                     (adaln_dtype_t)f.code, (adaln_act_t)act, yp, sp, ws, bytes, stream);
+  Py_END_ALLOW_THREADS;
+  if (rc != ADALN_OK) return refused(rc, "adaln_experts_ffn_fwd");
+  return pair_or(ys, saved);
+}
+
+// experts_ffn_bwd(dys, xs, wg, wu, wd, starts, saved, act, dxs, dwg, dwu, dwd, workspace,
+//                 stream) -> (dxs, dwg, dwu, dwd)
+PyObject* experts_ffn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 14) {
+    PyErr_SetString(PyExc_TypeError, "14 arguments");
+    return nullptr;
+  }
+  Experts f;
+  void *dys, *sp = nullptr, *dxp, *dgp, *dup, *ddp, *ws, *stream;
+  size_t need = 0, bytes = 0;
+  if (!experts_args(a[1], a[2], a[3], a[4], a[5], &f) ||
+      !matrix(a[0], "dys", f.rows, f.D, f.dtype, f.dev, &dys))
+    return nullptr;
+  if (none(a[6])) {
+    PyErr_SetString(PyExc_ValueError, "the backward needs what the forward saved");
+    return nullptr;
+  }
+  const long act = PyLong_AsLong(a[7]);
+  if (act == -1 && PyErr_Occurred()) return nullptr;
+  Ref device(PyObject_GetAttr(a[1], n_device)), dxs, dwg, dwu, dwd, work;
+  if (!device || !experts_saved(a[6], f, &need, &sp) ||
+      !matrix_out(a[8], "dxs", a[1], f.rows, f.D, f.dtype, f.dev, &dxs, &dxp) ||
+      !matrices_out(a[9], "dwg", a[2], f.E, f.F, f.D, f.dtype, f.dev, &dwg, &dgp) ||
+      !matrices_out(a[10], "dwu", a[3], f.E, f.F, f.D, f.dtype, f.dev, &dwu, &dup) ||
+      !matrices_out(a[11], "dwd", a[4], f.E, f.D, f.F, f.dtype, f.dev, &dwd, &ddp) ||
+      !experts_workspace(a[12], f, true, device.p, &work, &ws, &bytes) ||
+      !stream_of(a[13], f.dev, &stream))
+    return nullptr;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = f_experts_bwd(dys, f.xs, f.wg, f.wu, f.wd, f.starts, sp, f.rows, (int32_t)f.E, (int32_t)f.D,
+                     (int32_t)f.F, (adaln_dtype_t)f.code, (adaln_act_t)act, dxp, dgp, dup, ddp, ws, bytes,
+                     stream);
+  Py_END_ALLOW_THREADS;
+  if (rc != ADALN_OK) return refused(rc, "adaln_experts_ffn_bwd");
+  return PyTuple_Pack(4, dxs.p, dwg.p, dwu.p, dwd.p);
+}
+
 // ----- module --------------------------------------------------------------------------------
 
 template <class F>
@@ -1030,7 +1196,11 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !entry(a[3], "adaln_expert_sort_fwd", &f_sort_fwd) ||
       !entry(a[3], "adaln_expert_sort_bwd", &f_sort_bwd) ||
       !entry(a[3], "adaln_expert_combine_fwd", &f_combine_fwd) ||
-      !entry(a[3], "adaln_expert_combine_bwd", &f_combine_bwd))
+      !entry(a[3], "adaln_expert_combine_bwd", &f_combine_bwd) ||
+      !entry(a[3], "adaln_experts_ffn_saved_size", &f_experts_saved) ||
+      !entry(a[3], "adaln_experts_ffn_workspace_size", &f_experts_ws) ||
+      !entry(a[3], "adaln_experts_ffn_fwd", &f_experts_fwd) ||
+      !entry(a[3], "adaln_experts_ffn_bwd", &f_experts_bwd))
     return nullptr;
   Py_RETURN_NONE;
 }
@@ -1048,6 +1218,8 @@ PyMethodDef methods[] = {
     {"expert_sort_bwd", (PyCFunction)(void (*)(void))expert_sort_bwd, METH_FASTCALL, nullptr},
     {"expert_combine_fwd", (PyCFunction)(void (*)(void))expert_combine_fwd, METH_FASTCALL, nullptr},
     {"expert_combine_bwd", (PyCFunction)(void (*)(void))expert_combine_bwd, METH_FASTCALL, nullptr},
+    {"experts_ffn_fwd", (PyCFunction)(void (*)(void))experts_ffn_fwd, METH_FASTCALL, nullptr},
+    {"experts_ffn_bwd", (PyCFunction)(void (*)(void))experts_ffn_bwd, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding",

@@ -79,6 +79,11 @@ inline size_t saved_bytes(int64_t T, int32_t F) {
 cudaError_t make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_cols,
                      int box_rows);
 
+// The same of `depth` such matrices, one after the other: 3-D, so that a box past
+// one's rows reads zeros and not the next one's.
+cudaError_t make_map(CUtensorMap* m, const void* p, int64_t depth, int64_t rows, int64_t cols,
+                     int box_cols, int box_rows);
+
 // Launch as a programmatic dependent, in clusters of `cluster` CTAs.
 cudaError_t launch_cluster(void* kernel, int grid, int threads, int smem, int cluster, void** params,
                            cudaStream_t st);

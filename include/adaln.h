@@ -3,9 +3,10 @@
  * (sm_103a): the fused AdaLN LayerNorm-Modulate, described here, and, further
  * down, rotary positions with the norm of queries and keys (adaln_qk_rope_*),
  * the gated feed-forward block (adaln_ffn_*), dropout with the gate and the
- * residual of a branch (adaln_dropout_*) and tokens sorted by expert and back
- * (adaln_route, adaln_expert_*), which share its conventions on ownership, streams,
- * errors and the status word.
+ * residual of a branch (adaln_dropout_*), tokens sorted by expert and back
+ * (adaln_route, adaln_expert_*) and the experts' feed-forward blocks on them
+ * (adaln_experts_ffn_*), which share its conventions on ownership, streams, errors
+ * and the status word.
  *
  * The AdaLN is the fused adaptive LayerNorm of video / MMDiT diffusion
  * transformers described in "AdaptiveLoad: Towards Efficient Video Diffusion
@@ -477,6 +478,41 @@ ADALN_API int adaln_expert_combine_bwd(const void* dy, const void* ys, const flo
               const int32_t* row, const int32_t* starts, const int32_t* counts, int64_t T,
               int32_t k, int32_t E, int32_t align, int32_t D, adaln_dtype_t dtype, int64_t rows,
               void* dys, float* dweight, void* stream);
+
+/*
+ * The gated feed-forward block of each expert on its rows of a sorted array (a
+ * route's with `align` a multiple of 64):
+ *
+ *   y = (act(x Wg[e]') * (x Wu[e]')) Wd[e]'            for expert e's rows x
+ *
+ * xs, ys, dys, dxs [rows, D]; Wg, Wu and their gradients [E, F, D]; Wd and its
+ * gradient [E, D, F], all bf16, contiguous, 16-byte aligned; starts int32 [E + 1] in
+ * device memory, multiples of 64 that do not decrease, within [0, rows].  Expert e's
+ * rows are those from starts[e] on to starts[e + 1], zero rows between the tokens'
+ * and the next expert's among them: xs and dys have zeros there (as the sort and the
+ * combination's backward write them), and ys and dxs get zeros.  Rows from starts[E]
+ * on are neither read into a result nor written.  Sums, roundings and what is saved
+ * are the feed-forward block's; so are D and F; rows is at most ADALN_FFN_MAX_T.
+ * Starts that break these rules are recorded (ADALN_DEV_EXPERT_RANGE); no access leaves
+ * the arrays, and the outputs of such a call are unspecified.
+ *
+ * Forward: two launches (a third where few rows make it worth splitting the sum over
+ * F).  Backward: two (or three) launches; the gradient of an expert without rows is
+ * zeros.  No atomics: bitwise reproducible for a given device and sizes.  Errors as
+ * for the feed-forward block.
+ */
+ADALN_API int adaln_experts_ffn_saved_size(int64_t rows, int32_t E, int32_t D, int32_t F,
+              adaln_dtype_t dtype, size_t* bytes);
+ADALN_API int adaln_experts_ffn_workspace_size(int64_t rows, int32_t E, int32_t D, int32_t F,
+              adaln_dtype_t dtype, size_t* fwd_bytes, size_t* bwd_bytes);
+ADALN_API int adaln_experts_ffn_fwd(const void* xs, const void* wg, const void* wu, const void* wd,
+              const int32_t* starts, int64_t rows, int32_t E, int32_t D, int32_t F,
+              adaln_dtype_t dtype, adaln_act_t act, void* ys, void* saved, void* workspace,
+              size_t workspace_bytes, void* stream);
+ADALN_API int adaln_experts_ffn_bwd(const void* dys, const void* xs, const void* wg, const void* wu,
+              const void* wd, const int32_t* starts, const void* saved, int64_t rows, int32_t E,
+              int32_t D, int32_t F, adaln_dtype_t dtype, adaln_act_t act, void* dxs, void* dwg,
+              void* dwu, void* dwd, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Synchronise `stream`, then read and clear the status word: the one the

@@ -235,3 +235,82 @@ def test_expert_nodes_keep_shapes_and_types(lib, monkeypatch):
         first, = torch.autograd.grad((out * out).sum(), leaf, create_graph=True)
         with pytest.raises(RuntimeError, match="twice"):
             first.sum().backward()
+
+
+def experts_fwd(lib, **kw):
+    a = dict(xs=A, wg=A, wu=A, wd=A, starts=A, rows=256, E=4, D=64, F=128, dt=lib.ADALN_BF16, act=0, ys=B,
+             saved=B, ws=B, wsb=1 << 30)
+    a.update(kw)
+    return lib.raw.adaln_experts_ffn_fwd(*a.values(), None)
+
+
+def experts_bwd(lib, **kw):
+    a = dict(dys=A, xs=A, wg=A, wu=A, wd=A, starts=A, saved=A, rows=256, E=4, D=64, F=128,
+             dt=lib.ADALN_BF16, act=0, dxs=B, dwg=B, dwu=B, dwd=B, ws=B, wsb=1 << 30)
+    a.update(kw)
+    return lib.raw.adaln_experts_ffn_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [experts_fwd, experts_bwd])
+def test_experts_ffn_refusals(lib, call):
+    assert call(lib, dt=lib.ADALN_F32) == lib.ADALN_ERR_DTYPE
+    for bad in (dict(rows=-1), dict(rows=2 ** 24 + 1), dict(E=0), dict(E=257), dict(D=0), dict(D=12),
+                dict(F=4), dict(F=100), dict(D=2 ** 18 + 8), dict(F=-8)):
+        assert call(lib, **bad) == lib.ADALN_ERR_DIM, bad
+    assert call(lib, act=3) == lib.ADALN_ERR_ARG
+    for k in ("xs", "wg", "wu", "wd", "ws"):
+        assert call(lib, **{k: None}) == lib.ADALN_ERR_NULL, k
+        assert call(lib, **{k: A + 8}) == lib.ADALN_ERR_ALIGN, k
+    assert call(lib, starts=None) == lib.ADALN_ERR_NULL
+    assert call(lib, starts=A + 2) == lib.ADALN_ERR_ALIGN
+
+
+def test_experts_ffn_only_what_is_missing_is_refused(lib):
+    assert experts_fwd(lib, ys=None) == lib.ADALN_ERR_NULL
+    assert experts_fwd(lib, saved=B + 8) == lib.ADALN_ERR_ALIGN
+    for k in ("dys", "saved", "dxs", "dwg", "dwu", "dwd"):
+        assert experts_bwd(lib, **{k: None}) == lib.ADALN_ERR_NULL, k
+        assert experts_bwd(lib, **{k: A + 8}) == lib.ADALN_ERR_ALIGN, k
+    assert experts_bwd(lib, rows=0, dwd=None) == lib.ADALN_ERR_NULL
+    for rows in (0, 63):  # no expert can have a row
+        assert experts_fwd(lib, rows=rows, xs=None, ys=None, ws=None, saved=None) == lib.ADALN_OK
+    n = ctypes.c_size_t(0)
+    f = lib.raw.adaln_experts_ffn_saved_size
+    assert f(64, 2, 64, 40, lib.ADALN_BF16, ctypes.byref(n)) == lib.ADALN_OK
+    assert n.value == 2 * 2 * 6144
+    assert f(64, 2, 64, 40, lib.ADALN_BF16, None) == lib.ADALN_ERR_NULL
+    g = lib.raw.adaln_experts_ffn_workspace_size
+    assert g(64, 2, 64, 40, lib.ADALN_BF16, None, None) == lib.ADALN_ERR_NULL
+    assert g(64, 2, 64, 41, lib.ADALN_BF16, None, None) == lib.ADALN_ERR_DIM
+
+
+def test_experts_ffn_saves_only_for_a_gradient(lib, monkeypatch):
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    asked = []
+
+    def fwd(xs, wg, wu, wd, starts, act, save):
+        asked.append(save)
+        return xs * 1, torch.zeros(1, dtype=torch.uint8) if save else None
+
+    monkeypatch.setattr(autograd._lib, "adaln_experts_ffn_fwd", fwd)
+    monkeypatch.setattr(autograd._lib, "adaln_experts_ffn_bwd", lambda dys, xs, wg, wu, wd, *a, **kw: (
+        dys * xs, wg * 1, wu * 1, wd * 1))
+    m = autograd.MixtureFFN(8, 16, 4)
+    r = lib.Route(None, torch.zeros(5, dtype=torch.int32), None, 64, 64)
+    x = torch.ones(64, 8, dtype=torch.bfloat16)
+    call = lambda t: autograd.experts_ffn(t, m.wg, m.wu, m.wd, r)  # noqa: E731
+    assert call(x).requires_grad
+    with torch.no_grad():
+        assert not call(x).requires_grad
+    m.requires_grad_(False)
+    call(x)
+    leaf = x.clone().requires_grad_()
+    out = call(leaf)
+    assert asked == [True, False, False, True]
+    first, = torch.autograd.grad((out * out).sum(), leaf, create_graph=True)
+    with pytest.raises(RuntimeError, match="twice"):
+        first.sum().backward()
+    for bad in (dict(top_k=0), dict(top_k=5), dict(act="relu")):
+        with pytest.raises(ValueError):
+            autograd.MixtureFFN(8, 16, 4, **bad)
