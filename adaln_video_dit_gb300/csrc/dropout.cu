@@ -30,6 +30,8 @@ namespace {
 
 constexpr int kRows = 4;       // rows in flight a thread
 constexpr int kThreads = 256;
+constexpr int kBwdBlocks = 3;  // the backward's blocks an SM
+constexpr int kBwdRows = 8;    // its least rows a thread
 
 // What is dropped: nothing (the generator is not run), by chance, everything.
 enum { kNone = 0, kSome = 1, kAll = 2 };
@@ -128,13 +130,16 @@ struct Kept {
   __device__ __forceinline__ Kept(const Philox& gen, uint64_t at, uint32_t limit) : limit(limit) {
     if (DROP == kSome) gen(at, w);
   }
-  // f where kept and `other` where not (elements 2 i and 2 i + 1): chosen, not
-  // multiplied by zero, so nothing of a dropped element, an infinity say, comes through.
-  __device__ __forceinline__ float2 pick(int i, float2 f, float2 other) const {
-    if (DROP == kNone) return f;
-    if (DROP == kAll) return other;
-    return make_float2(w[i] << 16 >= limit ? f.x : other.x,
-                       w[i] >= limit ? f.y : other.y);  // (limit's lower half is zero)
+  __device__ __forceinline__ bool first(int i) const {  // element 2 i
+    return DROP == kNone || (DROP == kSome && w[i] << 16 >= limit);
+  }
+  __device__ __forceinline__ bool second(int i) const {  // element 2 i + 1
+    return DROP == kNone || (DROP == kSome && w[i] >= limit);  // (limit's lower half is zero)
+  }
+  // f where kept and zero where not: chosen, not multiplied by zero, so nothing of a
+  // dropped element, an infinity say, comes through.
+  __device__ __forceinline__ float2 pick(int i, float2 f) const {
+    return make_float2(first(i) ? f.x : 0.0f, second(i) ? f.y : 0.0f);
   }
 };
 
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
       if (DROP != kAll) {
         q = DROP == kSome ? mul2(f[j], factor) : f[j];
         if (GATE) q = mul2(q, k[j]);
-        q = kept.pick(j, q, zero);
+        q = kept.pick(j, q);
       }
       f[j] = ADD ? add2(q, v[j]) : q;
     }
@@ -210,78 +215,126 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
   }
 }
 
-// The backward with dgate: thread (range, group) walks the range's rows.
+// 16 bytes from global to shared memory, in groups of this thread's own.
+__device__ __forceinline__ void copy_async(uint32_t to, const uint4* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The backward with dgate: thread (range, group) walks the range's rows.  The rows
+// ahead are on their way into shared memory, each thread's own vectors into its own
+// places (so nothing waits for another thread): the sums, the gate and the generator
+// leave no registers for them.
 template <class E, int DROP>
-__global__ void __launch_bounds__(kThreads) dropout_bwd_kernel(const __grid_constant__ DropArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) dropout_bwd_kernel(const __grid_constant__ DropArgs a) {
+  constexpr int V = Raw<E>::V, S = V == 1 ? 4 : 3;  // stages: 32 or 48 KB a block
+  __shared__ uint4 ring[S][2 * V][kThreads];
   grid_wait();
   grid_launch_dependents();
   const int D = a.D, groups = a.groups;
-  const uint64_t at = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  const uint32_t r = (uint32_t)(at / (uint32_t)groups);
+  const uint32_t at = blockIdx.x * (uint32_t)kThreads + threadIdx.x;  // (the host checks that it fits)
+  const uint32_t r = at / (uint32_t)groups;
   if (r >= (uint32_t)a.ranges) return;
-  const int g = (int)(at - (uint64_t)r * (uint32_t)groups);
-  const int64_t begin = part_begin(r, a.T, a.ranges), end = part_begin(r + 1, a.T, a.ranges);
+  const int g = (int)(at - r * (uint32_t)groups);
+  const int64_t begin = part_begin(r, a.T, a.ranges);
+  const int rows = (int)(part_begin(r + 1, a.T, a.ranges) - begin);
+  const int64_t pitch = (int64_t)D * E::SIZE / 16;  // vectors of a row
+  const bool whole = 8 * g + 4 < D;                 // the group has both its vectors
+  const uint4* dys = reinterpret_cast<const uint4*>(row_of<E>(a.h, begin, D)) + g * V;
+  const uint4* hs = reinterpret_cast<const uint4*>(row_of<E>(a.saved, begin, D)) + g * V;
+  unsigned char* out = row_of<E>(a.y, begin, D);
+  const int32_t* const seg = a.seg + begin;
+  const uint32_t mine = smem_addr(&ring[0][0][threadIdx.x]);
+  auto fetch = [&](int t, int s) {
+    if (DROP != kAll && t < rows) {
+      const uint32_t to = mine + s * (2 * V * kThreads * 16);
+      copy_async(to, dys);
+      copy_async(to + V * kThreads * 16, hs);
+      if (V > 1 && whole) {
+        copy_async(to + kThreads * 16, dys + 1);
+        copy_async(to + (V + 1) * kThreads * 16, hs + 1);
+      }
+      dys += pitch;
+      hs += pitch;
+    }
+    copy_commit();
+  };
+  for (int t = 0; t < S - 1; ++t) fetch(t, t);
   const Philox gen(a.rng);
-  Raw<E> gate;
+  const float2 factor = splat2(a.factor), zero = splat2(0.0f);
+  float2 gate[4];  // times the factor
   int held = -1;
-  float2 sum[4] = {};
+  float2 sum[4] = {};  // without it
   auto flush = [&] {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = mul2(sum[j], factor);
     float4* p = reinterpret_cast<float4*>(a.partials + ((int64_t)r + held) * D + 8 * g);
     p[0] = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
-    if (8 * g + 4 < D) p[1] = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
+    if (whole) p[1] = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
   };
-  const float2 factor = splat2(a.factor), zero = splat2(0.0f);
   // One thread of a row checks its segment and notes where segments start.
-  int before = begin > 0 ? a.seg[begin - 1] : -1, noted = begin > 0 ? clamped(before, a.nseg) : -1;
-  for (int64_t t0 = begin; t0 < end; t0 += kRows) {
-    Raw<E> dy[kRows], h[kRows];
-    int raw[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (t0 + i < end) {
-        raw[i] = a.seg[t0 + i];
-        if (DROP == kAll) continue;
-        dy[i].load(row_of<E>(a.h, t0 + i, D), g, D);
-        h[i].load(row_of<E>(a.saved, t0 + i, D), g, D);
-      }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int64_t t = t0 + i;
-      if (t >= end) break;
-      const int b = clamped(raw[i], a.nseg);
-      if (g == 0) {
-        const unsigned bad = wrong(raw[i], before, a.nseg);
-        if (bad) atomicOr(a.status, bad);
-        before = raw[i];
-        for (; noted < b; ++noted) a.seg_start[noted + 1] = (int32_t)t;
-      }
-      if (b != held) {
-        if (held >= 0) flush();
-        gate.load(row_of<E>(a.gate, b, D), g, D);
-        held = b;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j] = zero;
-      }
-      float2 f[4], v[4], k[4];
-      if (DROP != kAll) dy[i].get(f), h[i].get(v);
-      gate.get(k);
-      const Kept<DROP> kept(gen, (uint64_t)t * groups + g, a.limit);
+  int before = begin > 0 ? seg[-1] : -1, noted = begin > 0 ? clamped(before, a.nseg) : -1;
+  uint64_t place = (uint64_t)begin * groups + g;
+  int s = 0, next = seg[0];
+  for (int t = 0; t < rows; ++t) {
+    fetch(t + S - 1, s == 0 ? S - 1 : s - 1);
+    const int raw = next, b = clamped(raw, a.nseg);
+    if (t + 1 < rows) next = seg[t + 1];
+    if (g == 0) {
+      const unsigned bad = wrong(raw, before, a.nseg);
+      if (bad) atomicOr(a.status, bad);
+      before = raw;
+      for (; noted < b; ++noted) a.seg_start[noted + 1] = (int32_t)(begin + t);
+    }
+    if (b != held) {
+      if (held >= 0) flush();
+      Raw<E> x;
+      x.load(row_of<E>(a.gate, b, D), g, D);
+      x.get(gate);
+      held = b;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (DROP == kAll) {
-          f[j] = zero;
-          continue;
-        }
-        const float2 d = DROP == kSome ? mul2(f[j], factor) : f[j];
-        sum[j] = kept.pick(j, fma2(d, v[j], sum[j]), sum[j]);
-        f[j] = kept.pick(j, mul2(d, k[j]), zero);
+        gate[j] = mul2(gate[j], factor);
+        sum[j] = zero;
       }
-      Raw<E> out;
-      out.set(f);
-      out.store(row_of<E>(a.y, t, D), g, D);
     }
+    const Kept<DROP> kept(gen, place, a.limit);
+    place += groups;
+    copy_wait<S - 1>();
+    float2 f[4], v[4];
+    if (DROP != kAll) {
+      Raw<E> x;
+#pragma unroll
+      for (int n = 0; n < V; ++n) x.v[n] = ring[s][n][threadIdx.x];
+      x.get(f);
+#pragma unroll
+      for (int n = 0; n < V; ++n) x.v[n] = ring[s][V + n][threadIdx.x];
+      x.get(v);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (DROP == kAll) {
+        f[j] = zero;
+      } else if (DROP == kNone) {
+        sum[j] = fma2(f[j], v[j], sum[j]);
+        f[j] = mul2(f[j], gate[j]);
+      } else {
+        if (kept.first(j)) sum[j].x = fmaf(f[j].x, v[j].x, sum[j].x);
+        if (kept.second(j)) sum[j].y = fmaf(f[j].y, v[j].y, sum[j].y);
+        f[j] = kept.pick(j, mul2(f[j], gate[j]));
+      }
+    }
+    Raw<E> y;
+    y.set(f);
+    y.store(out, g, D);
+    out += pitch * 16;
+    if (++s == S) s = 0;
   }
-  if (g == 0 && end == a.T)
+  if (g == 0 && begin + rows == a.T)
     for (; noted < a.nseg; ++noted) a.seg_start[noted + 1] = (int32_t)a.T;
   if (held >= 0) flush();
 }
@@ -375,13 +428,13 @@ int dropped_of(double p) {
 }
 int kind_of(int dropped) { return dropped == 0 ? kNone : dropped < 65536 ? kSome : kAll; }
 
-// Ranges of rows of the backward: enough threads to fill the device, at least
-// 4 kRows rows each (a range costs a partial).
+// Ranges of rows of the backward: threads for one wave of blocks, with at least
+// kBwdRows rows each (a range costs a partial).
 int ranges_of(int64_t T, int32_t D, int sms) {
   const int64_t groups = (D + 7) / 8;
-  const int64_t fill = ((int64_t)sms * 1024 + groups - 1) / groups;
-  const int64_t most = (T + 4 * kRows - 1) / (4 * kRows);
-  const int64_t n = fill < most ? fill : most;
+  const int64_t wave = (int64_t)sms * kBwdBlocks * kThreads / groups;
+  const int64_t most = (T + kBwdRows - 1) / kBwdRows;
+  const int64_t n = wave < most ? wave : most;
   return (int)(n < 1 ? 1 : n);
 }
 size_t partial_bytes(int32_t D, int32_t nseg, int ranges) {
