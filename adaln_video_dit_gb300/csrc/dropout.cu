@@ -28,7 +28,8 @@
 namespace adaln {
 namespace {
 
-constexpr int kRows = 4;       // rows in flight a thread
+template <class E>
+constexpr int kRows = E::EPV == 8 ? 4 : 2;  // rows of a thread, all in flight
 constexpr int kThreads = 256;
 constexpr int kBwdBlocks = 3;  // the backward's blocks an SM
 constexpr int kBwdRows = 8;    // its least rows a thread
@@ -168,11 +169,11 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
   const uint32_t at = blockIdx.x * (uint32_t)kThreads + threadIdx.x;  // (the host checks that it fits)
   const uint32_t rows = at / (uint32_t)groups;
   const int g = (int)(at - rows * (uint32_t)groups);
-  const int64_t t0 = (int64_t)rows * kRows;
+  const int64_t t0 = (int64_t)rows * kRows<E>;
   if (t0 >= a.T) return;
-  Raw<E> h[kRows], x[kRows];
+  Raw<E> h[kRows<E>], x[kRows<E>];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
+  for (int i = 0; i < kRows<E>; ++i)
     if (t0 + i < a.T) {
       if (DROP != kAll) h[i].load(row_of<E>(a.h, t0 + i, D), g, D);
       if (ADD) x[i].load(row_of<E>(a.x, t0 + i, D), g, D);
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
   Raw<E> gate;
   int held = -1;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < kRows<E>; ++i) {
     const int64_t t = t0 + i;
     if (t >= a.T) break;
     if (GATE) {
@@ -417,7 +418,7 @@ int check(int64_t T, int32_t D, int32_t nseg, adaln_dtype_t dt, bool gate) {
   if (dt != ADALN_F32 && dt != ADALN_BF16) return ADALN_ERR_DTYPE;
   if (T < 0 || T > (int64_t)INT32_MAX) return ADALN_ERR_DIM;
   if (D < 1 || D > ADALN_DROPOUT_MAX_D || D * (dt == ADALN_BF16 ? 2 : 4) % 16 != 0) return ADALN_ERR_DIM;
-  if ((T + kRows - 1) / kRows * ((D + 7) / 8) > (int64_t)UINT32_MAX - kThreads) return ADALN_ERR_DIM;
+  if (T * ((D + 7) / 8) > ((int64_t)UINT32_MAX - kThreads)) return ADALN_ERR_DIM;
   if (gate && (nseg < 1 || nseg > ADALN_MAX_NSEG)) return ADALN_ERR_DIM;
   return ADALN_OK;
 }
@@ -466,7 +467,8 @@ int run_pass(DropArgs& a, int drop, adaln_dtype_t dt, cudaStream_t st) {
   cudaError_t e = status_word(&a.status);
   if (e != cudaSuccess) return launch_failed(e);
   void* params[1] = {&a};
-  const int64_t threads = (a.T + kRows - 1) / kRows * a.groups;
+  const int rows = dt == ADALN_BF16 ? kRows<BF16> : kRows<F32>;
+  const int64_t threads = (a.T + rows - 1) / rows * a.groups;
   void* k = dt == ADALN_BF16 ? pass_kernel<BF16>(drop, a.gate != nullptr, a.x != nullptr)
                              : pass_kernel<F32>(drop, a.gate != nullptr, a.x != nullptr);
   e = launch(k, (threads + kThreads - 1) / kThreads, params, st);

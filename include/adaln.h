@@ -437,7 +437,7 @@ ADALN_API int adaln_dropout_bwd(const void* dy, const void* h, const void* gate,
  *
  * all int32, in device memory: nothing here waits for the host.  `rows` is at least
  * adaln_route_rows: T k + min(E, T k) (align - 1), rounded down to whole `align`.
- * One launch; two above 16384 pairs, which need the workspace
+ * One launch; two above 131072 pairs, which need the workspace
  * (adaln_route_workspace_size bytes, 0 otherwise, 16-byte aligned).  An expert
  * outside [-1, E) counts as -1 and is recorded (ADALN_DEV_EXPERT_RANGE).  T = 0
  * writes starts and counts.

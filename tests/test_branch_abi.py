@@ -171,7 +171,7 @@ def test_route_refusals(lib):
     for k in ("expert", "row", "starts", "counts"):
         assert route(lib, **{k: None}) == lib.ADALN_ERR_NULL, k
         assert route(lib, **{k: A + 2}) == lib.ADALN_ERR_ALIGN, k
-    big = dict(T=20000)
+    big = dict(T=70000)
     assert route(lib, ws=None, **big) == lib.ADALN_ERR_NULL
     assert route(lib, ws=A + 8, **big) == lib.ADALN_ERR_ALIGN
     assert route(lib, wsb=16, **big) == lib.ADALN_ERR_WORKSPACE
@@ -182,7 +182,7 @@ def test_route_refusals(lib):
         assert lib.raw.adaln_route_rows(T, k, E, align, ctypes.byref(n)) == lib.ADALN_OK
         assert n.value == rows, (T, k, E, align)
     assert lib.raw.adaln_route_rows(1, 1, 1, 1, None) == lib.ADALN_ERR_NULL
-    assert lib.adaln_route_workspace_size(8192, 2, 256) == 0 < lib.adaln_route_workspace_size(8193, 2, 1)
+    assert lib.adaln_route_workspace_size(65536, 2, 256) == 0 < lib.adaln_route_workspace_size(65537, 2, 1)
 
 
 @pytest.mark.parametrize("call", [sort_fwd, sort_bwd, combine_fwd, combine_bwd])

@@ -57,8 +57,8 @@ def check_route(L, expert, E, align):
 
 @pytest.mark.parametrize("how", ["mixed", "one"])
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 2, 8), (1, 32, 256), (3, 5, 4), (31, 1, 7),
-                                   (33, 1, 64), (100, 8, 256), (1111, 6, 64), (2048, 8, 16), (16384, 1, 256),
-                                   (16385, 1, 3), (8200, 2, 256), (40000, 4, 96), (200001, 3, 8),
+                                   (33, 1, 64), (100, 8, 256), (1111, 6, 64), (2048, 8, 16), (4096, 1, 9), (4097, 1, 9), (16384, 1, 256),
+                                   (16385, 1, 3), (8200, 2, 256), (32768, 4, 96), (131073, 1, 7), (200001, 3, 8),
                                    (300000, 8, 64)])
 def test_places(adaln, T, k, E, how):
     for align in (64, 1) if T < 2048 else (64,):
@@ -72,7 +72,7 @@ def test_places_with_other_alignments(adaln, align):
 
 
 def test_experts_out_of_range_are_recorded(adaln):
-    for T in (400, 9000):
+    for T in (400, 9000, 70000):
         expert = choices(T, 2, 5, 1)
         want = expert.copy()
         for at, bad in ((3, 5), (T - 1, -2), (77, 2 ** 31 - 1), (78, -2 ** 31)):
@@ -265,8 +265,8 @@ def test_nodes(adaln):
 
 
 def test_trace_counts_the_launches(adaln):
-    expert = torch.from_numpy(choices(9000, 2, 5, 4)).cuda()
-    x, w = torch.randn(9000, 64, device="cuda"), torch.rand(9000, 2, device="cuda")
+    expert = torch.from_numpy(choices(70000, 2, 5, 4)).cuda()
+    x, w = torch.randn(70000, 64, device="cuda"), torch.rand(70000, 2, device="cuda")
     adaln.adaln_trace_begin(16)
     r = adaln.adaln_route(expert, 5)
     small = adaln.adaln_route(expert[:8], 5)
