@@ -91,9 +91,9 @@ cudaError_t blocks_of(CUtensorMap* m, const void* p, int64_t depth, int64_t rows
 cudaError_t set_problem(Problem* p, const Matrix (&a)[2], const Matrix (&b)[2], int segs, int64_t M, int N,
                         int64_t tiles_m, bool gate, const Tiling& t, int64_t k, bool by_k, int64_t depth,
                         void* out) {
-  cudaError_t e = map_of(&p->a[0], a[0], 128);
+  cudaError_t e = map_of(&p->a[0], a[0], kRowAlign);
   if (e == cudaSuccess) e = map_of(&p->b[0], b[0], t.w);
-  if (e == cudaSuccess && segs > 1) e = map_of(&p->a[1], a[1], 128);
+  if (e == cudaSuccess && segs > 1) e = map_of(&p->a[1], a[1], kRowAlign);
   if (e == cudaSuccess && b[1].p != nullptr) e = map_of(&p->b[1], b[1], t.w);
   if (e == cudaSuccess && out) e = blocks_of(&p->out, out, depth, M, N);
   p->partial = nullptr;

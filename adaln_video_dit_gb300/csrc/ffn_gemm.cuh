@@ -527,6 +527,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kb0 = sh.kb0;
       const bool a_mn = sh.a_mn, b_mn = sh.b_mn;
       const int zb = GROUPED && !sh.by_k ? u.e : 0, k_row = GROUPED ? u.k_row : 0;
+      // GROUPED: blocks of kRowAlign rows of A that this CTA stages, and the bytes that the
+      // pair does.  Those past the expert's rows are left out: they are read for nothing
+      // (2222 rows of 16 experts fill a tile to a half), and what the products make of the
+      // stage's old contents there goes into rows that nothing stores.
+      const int left = u.end - m, blocks = min(max(left, 0) / kRowAlign, 2);
+      const int pair_blocks = min((u.end - u.row) / kRowAlign, 4);
+      const uint32_t pair_bytes = GROUPED && !a_mn ? pair_blocks * (kTileBytes / 2) + 2 * w * kBK * 2
+                                                   : 2 * (kTileBytes + w * kBK * 2);
       auto load = [&](uint32_t to, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
         if constexpr (GROUPED)
           tma_load_pair(to, map, x, y, z, bar);
@@ -550,10 +558,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* mb = maps_b + seg;
         const uint32_t da = ring + s * kStageBytes, db = da + kTileBytes;
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * (kTileBytes + w * kBK * 2));
+          if (rank == 0) mbar_arrive_expect_tx(full(s), pair_bytes);
           if (a_mn) {
             load(da, ma, m, k, 0, full(s));
             load(da + kTileBytes / 2, ma, m + 64, k, 0, full(s));
+          } else if (GROUPED) {
+            if (blocks > 0) load(da, ma, k, m, 0, full(s));
+            if (blocks > 1) load(da + kTileBytes / 2, ma, k, m + kRowAlign, 0, full(s));
           } else {
             load(da, ma, k, m, 0, full(s));
           }
@@ -673,7 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int row0 = u.row + row_in;
       const uint32_t at = tmem + acc * kAccCols + ((uint32_t)lanes << 16);
-      if constexpr (KIND == kPlain) {
+      if (GROUPED && row0 >= u.end) {  // none of this warp's rows are the expert's
+        if (KIND == kGateBwd && col_of(u, 0) < sh.N) {
+#pragma unroll
+          for (int i = 0; i < kSavedVecs; ++i) in.load(at_saved, i);
+        }
+      } else if constexpr (KIND == kPlain) {
         epilogue_plain<GROUPED>(a.p[u.i], sh, u, at, row0, half, buf, lane, turn);
       } else if constexpr (kIsGate) {
         epilogue_gate<ACT, KIND == kGateSave, GROUPED>(a, sh, u, at, row0, half, buf, lane, turn);
