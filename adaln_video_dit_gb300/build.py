@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libadaln.so")
 LIB_TUNING = os.path.join(HERE, "libadaln_tuning.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
-SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "dropout.cu", "experts.cu", "ffn.cu", "ffn_skinny.cu", "host.cu", "noalloc.cu", "rope.cu",
+SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "dropout.cu", "experts.cu", "experts_few.cu", "ffn.cu", "ffn_skinny.cu", "host.cu", "noalloc.cu", "rope.cu",
            "rope_bf16.cu", "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "route.cu", "selftest.cu"]
 HEADERS = ["common.cuh", "ring.cuh", "tc.cuh", "ffn.cuh", "ffn_gemm.cuh", "rope.cuh", "internal.h"]
 
@@ -131,7 +131,7 @@ def _strip_comments(text):
 
 
 # Sources that no AdaLN kernel is made of.
-OTHER_OPERATORS = {"dropout.cu", "experts.cu", "ffn.cu", "ffn.cuh", "ffn_gemm.cuh", "ffn_skinny.cu", "rope.cu", "rope.cuh", "rope_bf16.cu",
+OTHER_OPERATORS = {"dropout.cu", "experts.cu", "experts_few.cu", "ffn.cu", "ffn.cuh", "ffn_gemm.cuh", "ffn_skinny.cu", "rope.cu", "rope.cuh", "rope_bf16.cu",
                    "rope_f32.cu", "rope_few.cu", "rope_narrow.cu", "route.cu", "tc.cuh", "binding.cpp"}
 
 

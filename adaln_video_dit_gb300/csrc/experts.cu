@@ -42,11 +42,17 @@ int64_t likely_tiles(int64_t rows, int32_t E) {
 }
 
 struct FwdPlan {
+  bool few;
   Tiling gate, y;
   size_t bytes;
 };
 FwdPlan fwd_plan(int64_t rows, int32_t E, int32_t D, int32_t F, int pairs) {
   FwdPlan p = {};
+  p.few = experts_few_serve(rows, E);
+  if (p.few) {
+    p.bytes = round256((size_t)rows * F * 2);
+    return p;
+  }
   const int64_t tiles = likely_tiles(rows, E);
   p.gate = choose_tiling(rows, tiles, F, div_up(D, kBK), true, false, false, pairs);
   p.y = choose_tiling(rows, tiles, D, div_up(F, kBK), false, false, true, pairs);
@@ -55,6 +61,7 @@ FwdPlan fwd_plan(int64_t rows, int32_t E, int32_t D, int32_t F, int pairs) {
 }
 
 struct BwdPlan {
+  bool few;
   Tiling gate, dx, dw;
   int worth;
   size_t bytes;
@@ -64,6 +71,11 @@ BwdPlan bwd_plan(int64_t rows, int32_t E, int32_t D, int32_t F, int pairs) {
   const int64_t tiles_m = likely_tiles(rows, E);
   p.gate = choose_tiling(rows, tiles_m, F, div_up(D, kBK), false, true, false, pairs);
   p.dw = {128, 1, 0};
+  p.few = experts_few_serve(rows, E);
+  if (p.few) {
+    p.bytes = 3 * round256((size_t)rows * F * 2);
+    return p;
+  }
   const double unit = unit_clocks(div_up(rows, (int64_t)E * kBK), 128);
   const int64_t tiles = 2 * tiles_of(div_up(F, kTM), D, false, 128) + tiles_of(div_up(D, kTM), F, false, 128);
   const int kb = 2 * div_up(F, kBK);
@@ -169,6 +181,10 @@ int adaln_experts_ffn_fwd(const void* xs, const void* wg, const void* wu, const 
   if ((e = status_word(&status)) != cudaSuccess) return launch_failed(e);
   GemmArgs a = args_of(rows, E, starts, status);
   char* h = static_cast<char*>(workspace);
+  if (plan.few) {
+    e = experts_few_fwd({xs, wg, wu, wd, starts, rows, E, D, F, act}, ys, saved, h, status, st);
+    return e == cudaSuccess ? ADALN_OK : launch_failed(e);
+  }
   const int64_t tiles = most_tiles(rows, E);
   const Matrix none = {}, x = {xs, 1, rows, D, false}, hk = {h, 1, rows, F, false};
   const Matrix g = {wg, E, F, D, false}, u = {wu, E, F, D, false}, d = {wd, E, D, F, false};
@@ -220,18 +236,22 @@ int adaln_experts_ffn_bwd(const void* dys, const void* xs, const void* wg, const
   const size_t rf = round256((size_t)rows * F * 2);
   char* ws = static_cast<char*>(workspace);
   char *h = ws, *dg = ws + rf, *du = ws + 2 * rf;
-  a.saved = static_cast<uint4*>(const_cast<void*>(saved));  // read only here
-  e = blocks_of(&a.h, h, 1, rows, F);
-  if (e == cudaSuccess) e = blocks_of(&a.dg, dg, 1, rows, F);
-  if (e == cudaSuccess) e = blocks_of(&a.du, du, 1, rows, F);
-  const int64_t tiles = most_tiles(rows, E);
   const Matrix none = {};
-  const Matrix dyk = {dys, 1, rows, D, false}, dn = {wd, E, D, F, true};
-  a.problems = 1;
-  if (e == cudaSuccess)
-    e = set_problem(&a.p[0], {dyk, none}, {dn, none}, 1, rows, F, tiles, false, plan.gate, D, false, 1,
-                    nullptr);
-  if (e == cudaSuccess) e = launch_gemm<true>(a, kGateBwd, act, pairs, 0, st);
+  const int64_t tiles = most_tiles(rows, E);
+  if (plan.few) {
+    e = experts_few_bwd({xs, wg, wu, wd, starts, rows, E, D, F, act}, dys, saved, h, dg, du, dxs, status, st);
+  } else {
+    a.saved = static_cast<uint4*>(const_cast<void*>(saved));  // read only here
+    e = blocks_of(&a.h, h, 1, rows, F);
+    if (e == cudaSuccess) e = blocks_of(&a.dg, dg, 1, rows, F);
+    if (e == cudaSuccess) e = blocks_of(&a.du, du, 1, rows, F);
+    const Matrix dyk = {dys, 1, rows, D, false}, dn = {wd, E, D, F, true};
+    a.problems = 1;
+    if (e == cudaSuccess)
+      e = set_problem(&a.p[0], {dyk, none}, {dn, none}, 1, rows, F, tiles, false, plan.gate, D, false, 1,
+                      nullptr);
+    if (e == cudaSuccess) e = launch_gemm<true>(a, kGateBwd, act, pairs, 0, st);
+  }
   if (e != cudaSuccess) return launch_failed(e);
 
   // dx first: its units are the longer ones.
@@ -240,17 +260,21 @@ int adaln_experts_ffn_bwd(const void* dys, const void* xs, const void* wg, const
   const Matrix dgm = {dg, 1, rows, F, true}, dum = {du, 1, rows, F, true}, hm = {h, 1, rows, F, true};
   const Matrix xm = {xs, 1, rows, D, true}, dym = {dys, 1, rows, D, true};
   const int64_t tf = div_up(F, kTM), td = div_up(D, kTM);
-  a.problems = 4;
-  e = set_problem(&a.p[0], {dgk, duk}, {gn, un}, 2, rows, D, tiles, false, plan.dx, F, false, 1, dxs);
-  a.p[0].partial = reinterpret_cast<float*>(ws + 3 * rf);
+  Problem* p = a.p;
+  if (!plan.few) {
+    e = set_problem(p, {dgk, duk}, {gn, un}, 2, rows, D, tiles, false, plan.dx, F, false, 1, dxs);
+    p->partial = reinterpret_cast<float*>(ws + 3 * rf);
+    ++p;
+  }
   if (e == cudaSuccess)
-    e = set_problem(&a.p[1], {dgm, none}, {xm, none}, 1, F, D, tf, false, plan.dw, 0, true, E, dwg);
+    e = set_problem(p++, {dgm, none}, {xm, none}, 1, F, D, tf, false, plan.dw, 0, true, E, dwg);
   if (e == cudaSuccess)
-    e = set_problem(&a.p[2], {dum, none}, {xm, none}, 1, F, D, tf, false, plan.dw, 0, true, E, dwu);
+    e = set_problem(p++, {dum, none}, {xm, none}, 1, F, D, tf, false, plan.dw, 0, true, E, dwu);
   if (e == cudaSuccess)
-    e = set_problem(&a.p[3], {dym, none}, {hm, none}, 1, D, F, td, false, plan.dw, 0, true, E, dwd);
-  if (e == cudaSuccess) e = launch_gemm<true>(a, kPlain, act, pairs, plan.worth, st);
-  if (e == cudaSuccess && plan.dx.splits > 1) e = launch_join(a.p[0], dxs, starts + E, pairs, st);
+    e = set_problem(p++, {dym, none}, {hm, none}, 1, D, F, td, false, plan.dw, 0, true, E, dwd);
+  a.problems = (int)(p - a.p);
+  if (e == cudaSuccess) e = launch_gemm<true>(a, kPlain, act, pairs, plan.few ? 1 : plan.worth, st);
+  if (e == cudaSuccess && !plan.few && plan.dx.splits > 1) e = launch_join(a.p[0], dxs, starts + E, pairs, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
 

@@ -96,4 +96,24 @@ cudaError_t skinny_fwd(const void* x, const void* wg, const void* wu, const void
                        int F, int act, void* y, void* saved, void* workspace, unsigned* status,
                        cudaStream_t st);
 
+// CTAs that share the k blocks of each of `blocks` blocks of features in the few-token
+// forms: as many as are resident at two an SM, up to a cluster.
+int choose_splits(int64_t blocks, int kb, int sms);
+
+// The experts' blocks for few rows an expert (experts_few.cu): whether it serves, the
+// forward's two launches and the backward's up to dx.  `saved` may be NULL; h, dg and
+// du are [rows, F].
+struct Experts {
+  const void *xs, *wg, *wu, *wd;
+  const int32_t* starts;
+  int64_t rows;
+  int32_t E, D, F;
+  int act;
+};
+bool experts_few_serve(int64_t rows, int32_t E);
+cudaError_t experts_few_fwd(const Experts& x, void* ys, void* saved, void* h, unsigned* status,
+                            cudaStream_t st);
+cudaError_t experts_few_bwd(const Experts& x, const void* dys, const void* saved, void* h, void* dg, void* du,
+                            void* dxs, unsigned* status, cudaStream_t st);
+
 }  // namespace adaln

@@ -288,21 +288,20 @@ cudaError_t prepare(int* sms) {
   return cudaSuccess;
 }
 
-// CTAs that share a row block's k: as many as are resident at two an SM, but
-// clusters of 7 or 8 only where one an SM holds them all: two an SM, fewer of
-// them find room in the SMs' groups (one token, D = 5120, F = 13824: 77.5 and
-// 74.7 us with 7 and 8 for the second product, 68.5 us with 6).
-int choose_splits(int blocks, int kb, int sms) {
-  int s = 2 * sms / blocks;
-  if (s > kMaxSplits) s = kMaxSplits;
-  if (s > 6 && blocks * s > sms) s = 6;
-  if (s > kb) s = kb;
-  return s < 1 ? 1 : s;
-}
-
 int tokens_of(int64_t T) { return T <= 16 ? 16 : 32; }
 
 }  // namespace
+
+// Clusters of 7 or 8 only where one CTA an SM holds them all: two an SM, fewer of
+// them find room in the SMs' groups (one token, D = 5120, F = 13824: 77.5 and
+// 74.7 us with 7 and 8 for the second product, 68.5 us with 6).
+int choose_splits(int64_t blocks, int kb, int sms) {
+  int64_t s = 2 * sms / blocks;
+  if (s > kMaxSplits) s = kMaxSplits;
+  if (s > 6 && blocks * s > sms) s = 6;
+  if (s > kb) s = kb;
+  return s < 1 ? 1 : (int)s;
+}
 
 bool skinny_serves(int64_t T) { return T <= kMaxTokens; }
 

@@ -125,6 +125,17 @@ def test_rows_about_a_tile(adaln):
     against(call(adaln, *data, "silu"), tokens, *data, "silu")
 
 
+@pytest.mark.parametrize("spare", [0, 40])
+@pytest.mark.parametrize("tokens,D,F", [([3, 0, 64, 1, 40, 63, 2, 0], 264, 520), ([5], 1536, 4096), ([1] * 20, 72, 200),
+                                        ([0, 0, 130, 0, 0, 0, 0, 7], 200, 72), ([64] * 9, 8, 8)])
+def test_few_rows(adaln, tokens, D, F, spare):
+    """The form for few rows (no spare ones) and, on the same rows with many spare ones
+    behind them, the other."""
+    data = inputs(tokens, D, F, seed=len(tokens), spare=spare)
+    for act in ACTS:
+        against(call(adaln, *data, act), tokens, *data, act)
+
+
 def test_one_expert_equals_the_block(adaln):
     """The same products in the same order: the same bits as the feed-forward block."""
     tokens = [1024]
