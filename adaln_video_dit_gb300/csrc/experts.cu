@@ -107,7 +107,7 @@ cudaError_t set_problem(Problem* p, const Matrix (&a)[2], const Matrix (&b)[2], 
   if (e == cudaSuccess) e = map_of(&p->b[0], b[0], t.w);
   if (e == cudaSuccess && segs > 1) e = map_of(&p->a[1], a[1], kRowAlign);
   if (e == cudaSuccess && b[1].p != nullptr) e = map_of(&p->b[1], b[1], t.w);
-  if (e == cudaSuccess && out) e = blocks_of(&p->out, out, depth, M, N);
+  if (e == cudaSuccess && out) e = make_map(&p->out, out, depth, M, N, 64, 32);
   p->partial = nullptr;
   Dims& s = p->s;
   s.M = (int)M;
@@ -122,6 +122,8 @@ cudaError_t set_problem(Problem* p, const Matrix (&a)[2], const Matrix (&b)[2], 
   s.a_mn = a[0].mn;
   s.b_mn = b[0].mn;
   s.by_k = by_k;
+  s.inv_each = 1.0f / (float)((by_k ? s.tiles_m : s.splits) * (int64_t)s.tiles_n);
+  s.inv_group = 1.0f / (float)(kGroupM * s.tiles_n);
   return e;
 }
 

@@ -33,7 +33,7 @@ namespace {
 constexpr int kBK = 64, kRows = 64, kFeatures = 128;
 constexpr int kHalf = 64 * kBK * 2;            // a box of 64 x 64
 constexpr int kStage = 3 * kHalf;              // two of weights, one of rows
-constexpr int kStages = 4;                     // two CTAs an SM
+constexpr int kStages = 3;                     // three CTAs an SM
 constexpr int kThreads = 128;
 constexpr int kSmem = 1024 + kStages * kStage + 256;
 constexpr int kCols = kRows;                   // of tensor memory

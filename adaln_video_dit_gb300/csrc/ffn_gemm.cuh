@@ -56,6 +56,8 @@ struct Dims {        // what the roles of a CTA read of a problem
   int first;           // first unit of the problem
   int a_mn, b_mn;      // operand layouts
   int by_k;            // GROUPED
+  float inv_each, inv_group;  // GROUPED: 1 / the units of an expert (by_k) or of a tile of
+                              // rows, 1 / (kGroupM tiles_n)
 };
 struct Problem {
   CUtensorMap a[2], b[2];
@@ -160,6 +162,18 @@ __device__ __forceinline__ int expert_of_tile(Starts starts, int experts, int v)
   return base + 31 - __clz(hit);
 }
 
+// u / d for 0 <= u < 2^24 (kMaxUnits) and d >= 1, by a rounded 1 / d and two corrections
+// by one (the product is off by at most two): units of few k blocks are over before a
+// chain of integer divisions is.
+constexpr int kMaxUnits = 1 << 24;
+__device__ __forceinline__ int quotient(int u, int d, float inv) {
+  int q = (int)((float)u * inv), r = u - q * d;
+  int fix = (r >= d) - (r < 0);
+  q += fix;
+  r -= fix * d;
+  return q + (r >= d) - (r < 0);
+}
+
 // `shapes` is the problems' copy in shared memory (reads of the kernel's
 // parameters with an index cost several hundred cycles each).
 template <bool GROUPED>
@@ -176,13 +190,13 @@ __device__ __forceinline__ Unit unit_of(const Dims* shapes, int problems, int u,
   if (GROUPED) {
     if (s.by_k) {
       const int each = tiles_m * s.tiles_n;
-      r.e = u / each;
+      r.e = quotient(u, each, s.inv_each);
       u -= r.e * each;
       r.k_row = starts.rows(r.e) * kRowAlign;
       kb = starts.rows(r.e + 1) - starts.rows(r.e);
     } else {
       const int each = s.tiles_n * s.splits;
-      r.e = expert_of_tile(starts, experts, u / each);
+      r.e = expert_of_tile(starts, experts, quotient(u, each, s.inv_each));
       u -= starts.tiles(r.e) * each;
       tiles_m = starts.tiles(r.e + 1) - starts.tiles(r.e);
       base = starts.rows(r.e) * kRowAlign;
@@ -199,9 +213,10 @@ __device__ __forceinline__ Unit unit_of(const Dims* shapes, int problems, int u,
     r.k1 = (int)((int64_t)kb * (r.split + 1) / s.splits);
   }
   const int per_group = kGroupM * s.tiles_n;
-  const int group = tile / per_group, in = tile - group * per_group;
-  const int rows = min(kGroupM, tiles_m - group * kGroupM);
-  r.n = in / rows;
+  const int group = GROUPED ? quotient(tile, per_group, s.inv_group) : tile / per_group;
+  const int in = tile - group * per_group;
+  const int rows = max(min(kGroupM, tiles_m - group * kGroupM), 1);  // (no tiles: no unit is used)
+  r.n = GROUPED ? quotient(in, rows, __fdividef(1.0f, (float)rows)) : in / rows;
   r.row = base + (group * kGroupM + in - r.n * rows) * kTM;
   return r;
 }
@@ -266,6 +281,46 @@ __device__ __forceinline__ void store_block(const CUtensorMap* m, int col, int r
     tma_store(m, col, row, z, block);
   else
     tma_store(m, col, row, block);
+}
+
+// GROUPED, plain: outputs leave in blocks of 64 columns, half as many copies as blocks of
+// 32: with few rows an expert a weight gradient's tile is a few k blocks of products,
+// and its copies out are what takes the time.
+__device__ __forceinline__ void put_wide_row(uint32_t block, int lane, const uint32_t (&w)[32]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    st_shared_v4(block + lane * 128 + ((i ^ (lane & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2],
+                 w[4 * i + 3]);
+}
+__device__ __forceinline__ void epilogue_wide(const Problem& p, const Dims& s, const Unit& u, uint32_t acc,
+                                              int row0, int half, uint32_t buf, int lane) {
+  const int N = s.N, chunks = s.w / 32, z = s.by_k ? u.e : 0;
+  const bool none = u.k0 == u.k1;  // an empty sum
+#pragma unroll 1
+  for (int c = half; c < chunks; c += 2) {
+    const int col = u.n * 2 * s.w + c * 64;
+    if (col >= N) break;
+    __syncwarp();
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t r[32];
+      tmem_ld32(acc + c * 64 + j * 32, r);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[16 * j + i] = none ? 0 : pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    }
+    bulk_wait_read<0>();  // the copy before used this block
+    __syncwarp();
+    put_wide_row(buf, lane, w);
+    fence_async_shared();
+    __syncwarp();
+    if (elect_one()) {
+      tma_store(&p.out, col, row0, z, buf);
+      bulk_commit();
+    }
+  }
 }
 
 template <bool GROUPED>
@@ -690,7 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kSavedVecs; ++i) in.load(at_saved, i);
         }
       } else if constexpr (KIND == kPlain) {
-        epilogue_plain<GROUPED>(a.p[u.i], sh, u, at, row0, half, buf, lane, turn);
+        if (GROUPED && sh.splits == 1)
+          epilogue_wide(a.p[u.i], sh, u, at, row0, half, buf, lane);
+        else
+          epilogue_plain<GROUPED>(a.p[u.i], sh, u, at, row0, half, buf, lane, turn);
       } else if constexpr (kIsGate) {
         epilogue_gate<ACT, KIND == kGateSave, GROUPED>(a, sh, u, at, row0, half, buf, lane, turn);
       } else {
@@ -883,6 +941,7 @@ cudaError_t set_problem(Problem* p, const Operand (&a)[2], const Operand (&b)[2]
   s.a_mn = a[0].mn;
   s.b_mn = b[0].mn;
   s.by_k = 0;
+  s.inv_each = s.inv_group = 0;
   return e;
 }
 
@@ -896,6 +955,7 @@ cudaError_t launch_gemm(GemmArgs& a, int kind, int act, int pairs, int worth, cu
     s.first = (int)at;  // (GROUPED: an upper bound, the kernel counts them)
     at += (int64_t)s.tiles_m * s.tiles_n * s.splits * (s.by_k ? a.experts : 1);
   }
+  if (GROUPED && at >= kMaxUnits) return cudaErrorInvalidConfiguration;
   a.units = (int)at;
   a.lead = a.problems > 1 ? a.p[1].s.first : 0;
   a.worth = worth;
