@@ -31,14 +31,17 @@ int check(int64_t rows, int32_t E, int32_t D, int32_t F, adaln_dtype_t dt, int a
 }
 
 // Tiles of rows, at most, and as many as are likely: `rows` is a route's, the pairs'
-// number and 63 for each expert that they may meet.
+// number and 63 for each expert that they may meet, and an expert's last tile is half
+// full on average.
 int64_t most_tiles(int64_t rows, int32_t E) {
   const int64_t blocks = rows / kRowAlign, met = blocks < E ? blocks : E;
   return (blocks + 3 * met) / 4;
 }
 int64_t likely_tiles(int64_t rows, int32_t E) {
-  const int64_t blocks = rows / kRowAlign;
-  return blocks <= E ? blocks : E + (blocks - E) / 4;
+  const int64_t blocks = rows / kRowAlign, pairs = rows - (kRowAlign - 1) * (int64_t)E;
+  if (blocks <= E) return blocks;
+  const int64_t tiles = pairs / kTM + E / 2;
+  return tiles > E ? tiles : E;
 }
 
 struct FwdPlan {

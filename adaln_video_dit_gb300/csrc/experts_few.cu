@@ -221,6 +221,15 @@ __global__ void __launch_bounds__(kThreads) experts_few_kernel(const __grid_cons
     grid_wait();
     grid_launch_dependents();
   }
+  if (MODE == kGradGate && warp >= 2) {  // on their way into L2 under the products
+    const int across = (a.features + 31) >> 5, left = min(kFeatures / 32, across - block * (kFeatures / 32));
+    for (int r = 0; r < kRows / 32; ++r) {
+      const unsigned char* from =
+          a.saved + (((row0 >> 5) + r) * across + block * (kFeatures / 32)) * (int64_t)kSavedBlock;
+      for (int i = (threadIdx.x - 64) * 128; i < left * kSavedBlock; i += 64 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+    }
+  }
   bool ok = true;
   if (warp == 0) {
     int s = 0;
