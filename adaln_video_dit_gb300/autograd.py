@@ -358,6 +358,8 @@ def experts_ffn(xs, wg, wu, wd, route, act="silu"):
     D], as expert_sort gives them (align a multiple of 64), with wg, wu [E, F, D], wd
     [E, D, F] (differentiable).  Rows between the experts' are zeros, here and in the
     gradients; rows from route.starts[-1] on hold nothing."""
+    if route.align % 64:
+        raise ValueError(f"the experts' rows must start at multiples of 64, not of {route.align}")
     return ExpertsFFNFunction.apply(xs, wg, wu, wd, route.starts, act, torch.is_grad_enabled())
 
 

@@ -1,13 +1,16 @@
 """A video DiT block over packed samples, with the library's operators together.
 
     python examples/dit_block.py [--dim 1536] [--heads 12] [--hidden 4096] [--steps 5]
+                                 [--experts 8] [--top-k 2] [--dropout 0.1]
 
 Packed samples of text and video tokens go through adaLN modulation, the
 query/key norm with rotary positions over (time, height, width) (text tokens
 unrotated), attention within each sample, a second modulation and the gated
 feed-forward block; the projections and the attention are torch's.  The
 example trains the block on synthetic data for a few steps, in bf16, and then
-runs one forward without gradients.
+runs one forward without gradients.  With --experts the feed-forward block is a
+mixture of experts, and both branches end in one pass each: dropout, the gate and the
+residual.
 """
 import argparse
 import os
@@ -18,7 +21,8 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from adaln_video_dit_gb300 import rotary  # noqa: E402
-from adaln_video_dit_gb300.autograd import GatedFFN, QKNormRope, adaln_modulate  # noqa: E402
+from adaln_video_dit_gb300.autograd import (  # noqa: E402
+    GatedFFN, GatedResidual, MixtureFFN, QKNormRope, adaln_modulate)
 
 
 class DiTBlock(torch.nn.Module):
@@ -48,6 +52,10 @@ class DiTBlock(torch.nn.Module):
             at += n
         return torch.cat(outs)
 
+    def residual(self, x, h, gate, seg_id):
+        """The end of a branch: x + gate * h, with each token's sample's gate."""
+        return x + gate[seg_id.long()] * h
+
     def forward(self, x, cond, seg_id, pos, lengths):
         shift1, scale1, gate1, shift2, scale2, gate2 = self.modulation(
             torch.nn.functional.silu(cond)).chunk(6, dim=1)
@@ -55,10 +63,22 @@ class DiTBlock(torch.nn.Module):
         q, k, v = self.qkv(h).view(len(x), 3, self.heads, self.head_dim).unbind(1)
         q, k = self.rope(q, k, self.table, pos)  # strided views in, contiguous out
         a = self.attend(q, k, v, lengths).reshape(x.shape)
-        rows = seg_id.long()
-        x = x + gate1[rows] * self.out(a)
+        x = self.residual(x, self.out(a), gate1, seg_id)
         h = adaln_modulate(x, shift2, scale2, seg_id)
-        return x + gate2[rows] * self.ffn(h)
+        return self.residual(x, self.ffn(h), gate2, seg_id)
+
+
+class MixtureDiTBlock(DiTBlock):
+    """The block with a mixture of experts for its feed-forward, and dropout on both
+    branches (in training mode)."""
+
+    def __init__(self, dim, heads, hidden, rows, experts, top_k=2, dropout=0.0, device="cuda"):
+        super().__init__(dim, heads, hidden, rows, device)
+        self.ffn = MixtureFFN(dim, hidden, experts, top_k, device=device)
+        self.end = GatedResidual(dropout)
+
+    def residual(self, x, h, gate, seg_id):
+        return self.end(x, h, gate, seg_id)
 
 
 def main(argv=None):
@@ -67,6 +87,9 @@ def main(argv=None):
     ap.add_argument("--heads", type=int, default=12)
     ap.add_argument("--hidden", type=int, default=4096)
     ap.add_argument("--steps", type=int, default=5)
+    ap.add_argument("--experts", type=int, default=0)
+    ap.add_argument("--top-k", type=int, default=2)
+    ap.add_argument("--dropout", type=float, default=0.0)
     a = ap.parse_args(argv)
     torch.manual_seed(0)
     samples = [(77, 4, 16, 16), (77, 1, 16, 16), (0, 2, 12, 20)]  # text, frames, height, width
@@ -74,7 +97,10 @@ def main(argv=None):
     pos = rotary.grid_positions(samples, device="cuda")
     seg_id = torch.repeat_interleave(torch.arange(len(samples), dtype=torch.int32),
                                      torch.tensor(lengths)).cuda()
-    block = DiTBlock(a.dim, a.heads, a.hidden, rows=20)
+    if a.experts:
+        block = MixtureDiTBlock(a.dim, a.heads, a.hidden, 20, a.experts, a.top_k, a.dropout)
+    else:
+        block = DiTBlock(a.dim, a.heads, a.hidden, rows=20)
     x = torch.randn(sum(lengths), a.dim, device="cuda", dtype=torch.bfloat16)
     cond = torch.randn(len(samples), a.dim, device="cuda", dtype=torch.bfloat16)
     target = torch.randn_like(x)
@@ -87,6 +113,7 @@ def main(argv=None):
         opt.step()
         losses.append(loss.item())
         print(f"step {step}: loss {losses[-1]:.5f}")
+    block.eval()
     with torch.no_grad():
         y = block(x, cond, seg_id, pos, lengths)
     print(f"{sum(lengths)} packed tokens, output rms {y.float().square().mean().sqrt():.4f}")

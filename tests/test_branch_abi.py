@@ -298,6 +298,8 @@ def test_experts_ffn_saves_only_for_a_gradient(lib, monkeypatch):
         dys * xs, wg * 1, wu * 1, wd * 1))
     m = autograd.MixtureFFN(8, 16, 4)
     r = lib.Route(None, torch.zeros(5, dtype=torch.int32), None, 64, 64)
+    with pytest.raises(ValueError, match="64"):
+        autograd.experts_ffn(torch.ones(64, 8, dtype=torch.bfloat16), m.wg, m.wu, m.wd, r._replace(align=32))
     x = torch.ones(64, 8, dtype=torch.bfloat16)
     call = lambda t: autograd.experts_ffn(t, m.wg, m.wu, m.wd, r)  # noqa: E731
     assert call(x).requires_grad
