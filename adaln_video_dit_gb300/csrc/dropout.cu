@@ -31,7 +31,10 @@ namespace {
 template <class E>
 constexpr int kRows = E::EPV == 8 ? 4 : 2;  // rows of a thread, all in flight
 constexpr int kThreads = 256;
-constexpr int kBwdBlocks = 3;  // the backward's blocks an SM
+// The backward's threads a block, and threads an SM: rings of 32 KB, three or six of them.
+template <class E>
+constexpr int kBwdThreads = E::EPV == 8 ? 256 : 128;
+constexpr int kBwdResident = 768;
 constexpr int kBwdRows = 8;    // its least rows a thread
 
 // What is dropped: nothing (the generator is not run), by chance, everything.
@@ -231,13 +234,14 @@ __device__ __forceinline__ void copy_wait() {
 // places (so nothing waits for another thread): the sums, the gate and the generator
 // leave no registers for them.
 template <class E, int DROP>
-__global__ void __launch_bounds__(kThreads, kBwdBlocks) dropout_bwd_kernel(const __grid_constant__ DropArgs a) {
-  constexpr int V = Raw<E>::V, S = V == 1 ? 4 : 3;  // stages: 32 or 48 KB a block
-  __shared__ uint4 ring[S][2 * V][kThreads];
+__global__ void __launch_bounds__(kBwdThreads<E>, kBwdResident / kBwdThreads<E>)
+    dropout_bwd_kernel(const __grid_constant__ DropArgs a) {
+  constexpr int V = Raw<E>::V, S = 4, N = kBwdThreads<E>;  // S stages of a vector or two a thread
+  __shared__ uint4 ring[S][2 * V][N];
   grid_wait();
   grid_launch_dependents();
   const int D = a.D, groups = a.groups;
-  const uint32_t at = blockIdx.x * (uint32_t)kThreads + threadIdx.x;  // (the host checks that it fits)
+  const uint32_t at = blockIdx.x * (uint32_t)N + threadIdx.x;  // (the host checks that it fits)
   const uint32_t r = at / (uint32_t)groups;
   if (r >= (uint32_t)a.ranges) return;
   const int g = (int)(at - r * (uint32_t)groups);
@@ -252,12 +256,12 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) dropout_bwd_kernel(const
   const uint32_t mine = smem_addr(&ring[0][0][threadIdx.x]);
   auto fetch = [&](int t, int s) {
     if (DROP != kAll && t < rows) {
-      const uint32_t to = mine + s * (2 * V * kThreads * 16);
+      const uint32_t to = mine + s * (2 * V * N * 16);
       copy_async(to, dys);
-      copy_async(to + V * kThreads * 16, hs);
+      copy_async(to + V * N * 16, hs);
       if (V > 1 && whole) {
-        copy_async(to + kThreads * 16, dys + 1);
-        copy_async(to + (V + 1) * kThreads * 16, hs + 1);
+        copy_async(to + N * 16, dys + 1);
+        copy_async(to + (V + 1) * N * 16, hs + 1);
       }
       dys += pitch;
       hs += pitch;
@@ -384,11 +388,11 @@ __global__ void __launch_bounds__(kThreads) dropout_gate_kernel(const float* par
 
 // ----- host side ------------------------------------------------------------------
 
-cudaError_t launch(void* kernel, int64_t grid, void** params, cudaStream_t st) {
+cudaError_t launch(void* kernel, int64_t grid, int threads, void** params, cudaStream_t st) {
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   Shape s = {};
   s.grid = (int)grid;
-  s.threads = kThreads;
+  s.threads = threads;
   return traced_launch(ADALN_KERNEL_DROPOUT, st,
                        [&] { return launch_dependent(kernel, s, params, st); });
 }
@@ -433,7 +437,7 @@ int kind_of(int dropped) { return dropped == 0 ? kNone : dropped < 65536 ? kSome
 // kBwdRows rows each (a range costs a partial).
 int ranges_of(int64_t T, int32_t D, int sms) {
   const int64_t groups = (D + 7) / 8;
-  const int64_t wave = (int64_t)sms * kBwdBlocks * kThreads / groups;
+  const int64_t wave = (int64_t)sms * kBwdResident / groups;
   const int64_t most = (T + kBwdRows - 1) / kBwdRows;
   const int64_t n = wave < most ? wave : most;
   return (int)(n < 1 ? 1 : n);
@@ -471,7 +475,7 @@ int run_pass(DropArgs& a, int drop, adaln_dtype_t dt, cudaStream_t st) {
   const int64_t threads = (a.T + rows - 1) / rows * a.groups;
   void* k = dt == ADALN_BF16 ? pass_kernel<BF16>(drop, a.gate != nullptr, a.x != nullptr)
                              : pass_kernel<F32>(drop, a.gate != nullptr, a.x != nullptr);
-  e = launch(k, (threads + kThreads - 1) / kThreads, params, st);
+  e = launch(k, (threads + kThreads - 1) / kThreads, kThreads, params, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
 
@@ -550,8 +554,9 @@ int adaln_dropout_bwd(const void* dy, const void* h, const void* gate, const int
   if ((e = status_word(&a.status)) != cudaSuccess) return launch_failed(e);
   void* params[1] = {&a};
   const int64_t threads = (int64_t)a.ranges * a.groups;
+  const int block = dtype == ADALN_BF16 ? kBwdThreads<BF16> : kBwdThreads<F32>;
   e = launch(dtype == ADALN_BF16 ? bwd_kernel<BF16>(drop) : bwd_kernel<F32>(drop),
-             (threads + kThreads - 1) / kThreads, params, st);
+             (threads + block - 1) / block, block, params, st);
   if (e != cudaSuccess) return launch_failed(e);
 
   const int64_t each = a.ranges / nseg + 1;  // partials of a segment, about
@@ -559,7 +564,7 @@ int adaln_dropout_bwd(const void* dy, const void* h, const void* gate, const int
   const int cols = kThreads / lanes, chunks = (D / 4 + cols - 1) / cols;
   const int64_t units = (int64_t)nseg * chunks, most = (int64_t)sms * 8;
   void* join[8] = {&a.partials, &a.seg_start, &a.T, &a.D, &a.nseg, &a.ranges, &lanes, &dgate};
-  e = launch((void*)dropout_gate_kernel, units < most ? units : most, join, st);
+  e = launch((void*)dropout_gate_kernel, units < most ? units : most, kThreads, join, st);
   return e == cudaSuccess ? ADALN_OK : launch_failed(e);
 }
 
