@@ -1,6 +1,7 @@
 """GB300-native operators of video diffusion transformer blocks: the fused AdaLN
-LayerNorm-Modulate, rotary positions with the norm of queries and keys, and the
-gated feed-forward block (forward and backward).
+LayerNorm-Modulate, rotary positions with the norm of queries and keys, the gated
+feed-forward block, dropout with the gate and the residual of a branch, and mixtures
+of experts (forward and backward).
 
 The compute path is libadaln.so (hand-written sm_103a CUDA behind a C ABI,
 declared in include/adaln.h); `adaln_video_dit_gb300._lib` is its thin ctypes

@@ -15,11 +15,19 @@
 //
 // A thread owns the eight elements of a generator call ("group"): one 16-byte
 // vector of bf16, two of fp32.  The forward gives it kRows rows of its column
-// group, all loads ahead of the arithmetic.  The backward with a gate gives it a
-// range of rows, over which it sums dgate in registers, one fp32 partial for each
-// (range, segment) it meets; a second launch adds the partials in a fixed order
-// (no atomics: bitwise reproducible).  The (range, segment) pairs met along the
-// rows form a monotone path, so slot = range + segment is unique for each.
+// group, all loads ahead of the arithmetic; the generator's key schedule is then
+// shared by the rows (with one row a thread it, not memory, set the time: 180 us
+// where four take 153).  The backward with a gate gives it a range of rows, over
+// which it sums dgate in registers, one fp32 partial for each (range, segment) it
+// meets; a second launch adds the partials in a fixed order (no atomics: bitwise
+// reproducible).  The (range, segment) pairs met along the rows form a monotone
+// path, so slot = range + segment is unique for each.
+//
+// Bound: memory.  Measured (one GB300, T = 32760, D = 5120, bf16, p = 0.1, one
+// segment; 1007 MB each way): forward 146 us, 6.9 TB/s; backward with dgate 166 us
+// (its rows 155, its sums the rest; with p = 0 about 10 us less: the generator keeps
+// the issue slots busy).  T = 5003, D = 1000, fp32, 37 segments, 60 MB: 12 and 21 us,
+// of which the start and end of two and three launches are a third.
 #include <cmath>
 
 #include "common.cuh"
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(kBwdThreads<E>, kBwdResident / kBwdThreads<E>)
   if (held >= 0) flush();
 }
 
-// dgate[b] = the sum of the segment's partials in slot order: kLanes groups of
+// dgate[b] = the sum of the segment's partials in slot order: `lanes` groups of
 // them, each summed in order, joined in lane order.  A block takes `lanes` groups
 // of slots x (kThreads / lanes) vectors of four columns.
 __global__ void __launch_bounds__(kThreads) dropout_gate_kernel(const float* partials,

@@ -12,8 +12,22 @@
 //
 // Starts are multiples of 64 rows with zeros between, so that a warp's 32-row block of
 // an output and a 64-row step of a weight gradient's sum are each one expert's; the
-// weight gradients' sums take the zeros in.  A tile past its expert's rows computes
-// what nothing stores.
+// weight gradients' sums take the zeros in.  A tile past its expert's rows neither
+// reads A there nor stores what comes of it.
+//
+// Few rows an expert have a form of their own (experts_few.cu), up to about one block
+// of 64 rows an expert: with 64 rows of each of 16 experts at 1000 x 2728, 8 at 1536 x
+// 4096, 64 at 2048 x 1024 and 4 at 5120 x 3584 it takes 61, 62, 137 and 80 us for the
+// forward where the tiles take 63, 70, 150 and 108; with 128 rows 95, 74, 164 and 85
+// against 81, 73, 156 and 105, with 192 rows it loses on all four.
+//
+// Bound (one GB300): the tensor cores at the power limit with thousands of rows an
+// expert (T = 32760, two of 8 experts, D = 5120, F = 13824, forward 15.9 to 16.4 ms, 1700
+// to 1750 TFLOP/s; 8192 tokens, two of 8, D = 1536, F = 4096, forward and backward 1333
+// to 1395 us, 1330 to 1390, where the gate's two kernels run at the L2 rate as the
+// block's do); the L2 rate and what a unit's start and end cost with a few hundred rows
+// (2222 rows of 16 experts, D = 1000, F = 2728, both passes 261 to 265 us for 540 MB: a
+// weight-gradient tile is two or three k blocks, and reads as much as it writes).
 #include "ffn_gemm.cuh"
 
 namespace adaln {

@@ -8,8 +8,11 @@
 // weights through a TMA ring, and multiplies them with the 64 rows at a time (an
 // accumulator holds 128 features x 64 rows).  The other form's tiles of 256 rows are
 // bound here by what they copy and multiply for empty rows, and by one tile's k loop
-// where few experts are met.  Measured (one GB300, D = 1536, F = 4096, forward):
-// eight experts met 302 MB.
+// where few experts are met.  Measured (one GB300, forward; floor from the weights at
+// the copy rate): D = 1536, F = 4096, eight experts met 62 us (45; tiles 70), two 26 us
+// (11), one 16.5 us (5.6; tiles 31.8); D = 5120, F = 13824, two experts 137 us (127); 64
+// experts of 2048 x 1024 139 us (120).  What is left is each CTA's start and end, some
+// 5 us a launch.
 //
 // Four products, alike but for their maps and epilogues:
 //   projections  [g; u] = [Wg; Wu] x'       h = act(g) u, g and u saved
@@ -20,9 +23,11 @@
 // features (MN-major): the boxes of 64 x 64 that fill a stage are the same.
 //
 // The sum over k is split over a cluster of up to 8 CTAs, as many as keep all CTAs
-// resident; the partial sums meet in shared memory of the cluster, in rank order.  Two
-// CTAs an SM keep 128 KB of weights an SM in flight.  A call's second product starts
-// to fetch its weights while the first one still runs.
+// resident at two an SM; the partial sums meet in shared memory of the cluster, in rank
+// order.  (More splits than that cost more at their joins than they fill: eight experts
+// met 62 us, 71 with at most 16 k blocks a CTA, 94 with 8.)  Three CTAs an SM of three
+// stages keep 144 KB of weights an SM in flight (two of four stages 66 us).  A call's
+// second product starts to fetch its weights while the first one still runs.
 #include <mutex>
 
 #include "ffn.cuh"

@@ -396,8 +396,8 @@ typedef struct {
  * (ADALN_DEV_SEG_RANGE, ADALN_DEV_SEG_ORDER).
  *
  * Errors: ADALN_ERR_DTYPE; ADALN_ERR_DIM for T outside [0, 2^31), D outside [1,
- * ADALN_DROPOUT_MAX_D] or not of whole 16-byte vectors, T D above about 2^37, or
- * (with a gate) a bad nseg; ADALN_ERR_ARG for p outside [0, 1]; ADALN_ERR_NULL (rng too, where the
+ * ADALN_DROPOUT_MAX_D] or not of whole 16-byte vectors, T ceil(D / 8) of 2^32 - 256
+ * or more, or (with a gate) a bad nseg; ADALN_ERR_ARG for p outside [0, 1]; ADALN_ERR_NULL (rng too, where the
  * mask is drawn); ADALN_ERR_ALIGN (16 bytes, seg_id 4).
  */
 ADALN_API int adaln_dropout_fwd(const void* h, const void* x, const void* gate,
