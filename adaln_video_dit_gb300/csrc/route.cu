@@ -19,8 +19,8 @@
 // several loads in flight.  Sums are fp32, over j in order, outputs rounded once.
 //
 // Measured (one GB300, T = 32760, D = 5120, bf16, two of 8 experts): the route 7 us,
-// sorting 146 us and back 153, combining 159 us and back 241 (1007 and 1678 MB: 98,
-// 98, 94 and 104 % of the copy rate).  The route of 6666 pairs, 64 experts, 5.6 us
+// sorting 146 us and back 153, combining 146 us and back 241 (1007 and 1678 MB: 98 to
+// 104 % of the copy rate).  The route of 6666 pairs, 64 experts, 5.6 us
 // (with the instruction that finds equal lanes in place of the votes, and the pairs
 // walked twice, 9.0), of 524288, 256 experts, 12 us (28).
 #include "ffn.cuh"
@@ -276,9 +276,9 @@ __device__ __forceinline__ uint4* vecs_of(void* p, int64_t row, int nvec) {
 }
 
 // The sorted row of this lane's choice of token t (lanes k and up: -1), and its
-// weight.
+// weight (one where there are none: a product with it is exact).
 __device__ __forceinline__ int row_of(const CopyArgs& a, int64_t t, int lane, float* w) {
-  *w = 0.0f;
+  *w = 1.0f;
   if (lane >= a.k) return -1;
   const int r = a.row[t * a.k + lane];
   if (a.weight != nullptr) *w = a.weight[t * a.k + lane];
@@ -331,57 +331,84 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(const __grid_constant__ 
 }
 
 // y[t] = sum_j w[t, j] ys[row[t, j]].  A warp takes parts of tokens' rows, as many
-// warps as are resident, the next one's indices on their way with this one's rows.
-template <class E, bool WEIGHT, int V>
+// warps as are resident, the next one's indices on their way with this one's rows: the
+// same part of TOK tokens, so that few choices keep as many vectors in flight as many
+// (TOK 2 with one or two choices, or 4 with one vector a lane: k <= 2).
+template <class E, int V, int TOK>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CopyArgs a) {
-  constexpr int kIn = V == 1 ? 8 : 4;  // choices in flight
+  constexpr int kIn = V == 1 ? 8 : 4, kEach = kIn / TOK;  // choices in flight, of a token
+  constexpr int kLanes = 32 / TOK;                        // that hold a token's indices
   grid_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, nvec = a.nvec, parts = (nvec + 32 * V - 1) / (32 * V);
-  const int64_t items = a.T * parts, step = (int64_t)gridDim.x * kWarps;
+  const int64_t items = (a.T + TOK - 1) / TOK * parts, step = (int64_t)gridDim.x * kWarps;
   int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (i >= items) return;
+  auto group = [&](int64_t item) -> int64_t {  // of TOK tokens
+    return items <= UINT32_MAX ? (int64_t)((uint32_t)item / (uint32_t)parts) : item / parts;
+  };
+  auto indices = [&](int64_t g, float* w) {
+    const int64_t t = g * TOK + lane / kLanes;
+    if (TOK > 1 && t >= a.T) {
+      *w = 1.0f;
+      return -1;
+    }
+    return row_of(a, t, lane % kLanes, w);
+  };
   float w_next;
-  int row_next = row_of(a, i / parts, lane, &w_next);
+  int64_t g_next = group(i);
+  int row_next = indices(g_next, &w_next);
   for (; i < items; i += step) {
-    const int64_t t = i / parts;
-    const int v0 = (int)(i - t * parts) * 32 * V + lane;
+    const int64_t g = g_next;
+    const int v0 = (int)(i - g * parts) * 32 * V + lane;
     const float w = w_next;
     const int row = row_next;
-    if (i + step < items) row_next = row_of(a, (i + step) / parts, lane, &w_next);
+    if (i + step < items) {
+      g_next = group(i + step);
+      row_next = indices(g_next, &w_next);
+    }
     float2 sum[V][E::EPV / 2] = {};
-    for (int j0 = 0; j0 < a.k; j0 += kIn) {
+    for (int j0 = 0; j0 < a.k; j0 += kEach) {  // (once where TOK > 1)
       uint4 in[kIn][V];
       int r[kIn];
 #pragma unroll
-      for (int j = 0; j < kIn; ++j) {
-        r[j] = __shfl_sync(~0u, row, min(j0 + j, 31));
-        if (j0 + j >= a.k) r[j] = -1;
-        if (r[j] < 0) continue;
-        const uint4* from = vecs_of(a.sorted, r[j], nvec);
+      for (int n = 0; n < kIn; ++n) {
+        const int j = j0 + n % kEach;
+        r[n] = __shfl_sync(~0u, row, n / kEach * kLanes + min(j, kLanes - 1));
+        if (j >= a.k) r[n] = -1;
+        if (r[n] < 0) continue;
+        const uint4* from = vecs_of(a.sorted, r[n], nvec);
 #pragma unroll
-        for (int n = 0; n < V; ++n)
-          if (v0 + 32 * n < nvec) in[j][n] = from[v0 + 32 * n];
+        for (int v = 0; v < V; ++v)
+          if (v0 + 32 * v < nvec) in[n][v] = from[v0 + 32 * v];
       }
 #pragma unroll
-      for (int j = 0; j < kIn; ++j) {
-        const float wj = __shfl_sync(~0u, w, min(j0 + j, 31));
-        if (r[j] < 0) continue;
+      for (int n = 0; n < kIn; ++n) {
+        const float wj = __shfl_sync(~0u, w, n / kEach * kLanes + min(j0 + n % kEach, kLanes - 1));
+        if (r[n] >= 0) {
 #pragma unroll
-        for (int n = 0; n < V; ++n) {
-          if (v0 + 32 * n >= nvec) continue;
-          float2 f[E::EPV / 2];
-          E::unpack2(in[j][n], f);
+          for (int v = 0; v < V; ++v) {
+            if (v0 + 32 * v >= nvec) continue;
+            float2 f[E::EPV / 2];
+            E::unpack2(in[n][v], f);
 #pragma unroll
-          for (int q = 0; q < E::EPV / 2; ++q)
-            sum[n][q] = WEIGHT ? fma2(f[q], splat2(wj), sum[n][q]) : add2(f[q], sum[n][q]);
+            for (int q = 0; q < E::EPV / 2; ++q)
+              sum[v][q] = fma2(f[q], splat2(wj), sum[v][q]);
+          }
         }
+        if (n % kEach + 1 < kEach || (TOK == 1 && j0 + kEach < a.k)) continue;  // more of this token
+        const int64_t t = g * TOK + n / kEach;
+        if (TOK > 1 && t >= a.T) break;
+        uint4* to = vecs_of(a.to, t, nvec);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v0 + 32 * v < nvec) {
+            st_global_cs_v4(to + v0 + 32 * v, E::pack2(sum[v]));
+#pragma unroll
+            for (int q = 0; q < E::EPV / 2; ++q) sum[v][q] = splat2(0.0f);
+          }
       }
     }
-    uint4* to = vecs_of(a.to, t, nvec);
-#pragma unroll
-    for (int n = 0; n < V; ++n)
-      if (v0 + 32 * n < nvec) st_global_cs_v4(to + v0 + 32 * n, E::pack2(sum[n]));
   }
 }
 
@@ -545,10 +572,10 @@ int vecs_a_lane(int nvec) {
   return 1;
 }
 template <class E>
-void* combine_of(bool weight, int v) {
-  return v == 4   ? weight ? (void*)combine_kernel<E, true, 4> : (void*)combine_kernel<E, false, 4>
-         : v == 2 ? weight ? (void*)combine_kernel<E, true, 2> : (void*)combine_kernel<E, false, 2>
-         : weight ? (void*)combine_kernel<E, true, 1> : (void*)combine_kernel<E, false, 1>;
+void* combine_of(int v, int tokens) {
+  return v == 4   ? tokens > 1 ? (void*)combine_kernel<E, 4, 2> : (void*)combine_kernel<E, 4, 1>
+         : v == 2 ? tokens > 1 ? (void*)combine_kernel<E, 2, 2> : (void*)combine_kernel<E, 2, 1>
+         : tokens > 1 ? (void*)combine_kernel<E, 1, 4> : (void*)combine_kernel<E, 1, 1>;
 }
 template <class E>
 void* combine_bwd_of(int v) {
@@ -563,11 +590,16 @@ int run_combine(const void* sorted, const float* weight, const int32_t* row, int
   CopyArgs a = copy_args(T, k, D, dtype, rows, row);
   a.sorted = sorted, a.weight = weight, a.to = to;
   const int v = vecs_a_lane(a.nvec);
-  void* kernel = dtype == ADALN_BF16 ? combine_of<BF16>(weight != nullptr, v) : combine_of<F32>(weight != nullptr, v);
+  const int64_t parts = parts_of(a.nvec, 32 * v);
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return launch_failed(e);
-  const int64_t blocks = blocks_for(T * parts_of(a.nvec, 32 * v)), most = (int64_t)sms * (v == 4 ? 2 : 3);
+  const int64_t most = (int64_t)sms * (v == 4 ? 2 : 3);  // resident
+  // (Several tokens to a warp only where all warps find some.)
+  const int several = v == 1 ? 4 : 2;
+  const int tokens = k <= 2 && T * parts >= several * most * kWarps ? several : 1;
+  void* kernel = dtype == ADALN_BF16 ? combine_of<BF16>(v, tokens) : combine_of<F32>(v, tokens);
+  const int64_t blocks = blocks_for((T + tokens - 1) / tokens * parts);
   return run_copy(a, kernel, blocks < most ? blocks : most, static_cast<cudaStream_t>(stream));
 }
 

@@ -94,7 +94,8 @@ def close(got, ref, bound, name):
 @pytest.mark.parametrize("T,k,E,D,align", [
     (1, 1, 1, 8, 64), (1, 2, 8, 1536, 64), (1, 32, 256, 64, 64), (5, 3, 4, 24, 1), (64, 2, 8, 5120, 64),
     (333, 6, 64, 1000, 64), (1111, 5, 16, 264, 128), (2000, 8, 96, 72, 3), (4097, 1, 3, 2056, 64),
-    (9000, 2, 8, 512, 64), (50, 4, 200, 8200, 64)])
+    (9000, 2, 8, 512, 64), (50, 4, 200, 8200, 64), (33001, 2, 8, 256, 64), (8003, 1, 5, 1536, 64),
+    (30005, 2, 4, 200, 64), (20001, 3, 4, 72, 64)])
 def test_copies_and_sums(adaln, T, k, E, D, align, dt):
     expert = choices(T, k, E, T + D)
     r, row, starts = check_route(adaln, expert, E, align)
