@@ -83,8 +83,8 @@ __device__ __forceinline__ int expert_of_row(const FewArgs& a, int64_t row) {
   int reached = 0;
   bool bad = false;
   for (int e = lane; e <= a.E; e += 32) {
-    const int s = a.starts[e], before = e > 0 ? a.starts[e - 1] : 0;
-    bad |= s < 0 || s > a.rows || s % kRows != 0 || before > s;
+    const int s = a.starts[e];
+    bad |= s > a.rows || s % kRows != 0 || (e > 0 ? a.starts[e - 1] > s : s != 0);
     reached += s <= row;
   }
   if (__any_sync(~0u, bad)) {

@@ -117,8 +117,9 @@ struct Starts {
 static_assert(kTM == 4 * kRowAlign && 3 * kMaxExperts < 1024 &&
                   ADALN_FFN_MAX_T / kRowAlign <= 1 << 18, "packed starts");
 
-// Fills `to` from a.starts, with the whole CTA; what is not a list of starts is
-// recorded and taken for one without rows.
+// Fills `to` from a.starts, with the whole CTA; what is not a list of starts (from 0, not
+// decreasing, in whole kRowAlign, within the rows) is recorded and taken for one without
+// rows.
 __device__ __forceinline__ void fetch_starts(const GemmArgs& a, int* to, int* bad) {
   const int e = threadIdx.x;
   if (e == 0) *bad = 0;
@@ -128,7 +129,7 @@ __device__ __forceinline__ void fetch_starts(const GemmArgs& a, int* to, int* ba
     to[e] = s;
   }
   __syncthreads();
-  if (e <= a.experts && (s < 0 || s > a.rows || s % kRowAlign != 0 || (e > 0 && to[e - 1] > s))) *bad = 1;
+  if (e <= a.experts && (s > a.rows || s % kRowAlign != 0 || (e > 0 ? to[e - 1] > s : s != 0))) *bad = 1;
   __syncthreads();
   if (*bad) {
     s = 0;

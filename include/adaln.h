@@ -487,7 +487,7 @@ ADALN_API int adaln_expert_combine_bwd(const void* dy, const void* ys, const flo
  *
  * xs, ys, dys, dxs [rows, D]; Wg, Wu and their gradients [E, F, D]; Wd and its
  * gradient [E, D, F], all bf16, contiguous, 16-byte aligned; starts int32 [E + 1] in
- * device memory, multiples of 64 that do not decrease, within [0, rows].  Expert e's
+ * device memory, multiples of 64 from 0 on that do not decrease, up to rows.  Expert e's
  * rows are those from starts[e] on to starts[e + 1], zero rows between the tokens'
  * and the next expert's among them: xs and dys have zeros there (as the sort and the
  * combination's backward write them), and ys and dxs get zeros.  Rows from starts[E]

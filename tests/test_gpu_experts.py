@@ -172,10 +172,13 @@ def test_an_experts_rows_do_not_depend_on_the_others(adaln):
     assert not bool(out["ys"][at[1]:at[1] + 3].isfinite().any())
 
 
-def test_bad_starts_are_recorded(adaln):
-    xs, wg, wu, wd, starts, dys = inputs([70, 3, 130], 64, 96, seed=2)
+@pytest.mark.parametrize("spare", [0, 40])
+def test_bad_starts_are_recorded(adaln, spare):
+    """In both forms: no multiple of 64, not from 0 on, decreasing, past the rows."""
+    xs, wg, wu, wd, starts, dys = inputs([70, 3, 0, 0, 60], 64, 96, seed=2, spare=spare)
     rows = len(xs)
-    for at, bad in ((1, 100), (0, -64), (2, 64), (3, rows + 64), (1, 2 ** 31 - 64), (3, 0)):
+    for at, bad in ((1, 100), (0, -64), (0, 64), (2, 64), (5, rows + 64), (1, 2 ** 31 - 64), (5, 0),
+                    (slice(0, 6), rows), (slice(0, 2), 128)):
         s = starts.clone()
         s[at] = bad
         _, saved = adaln.adaln_experts_ffn_fwd(xs, wg, wu, wd, s, save=True)
@@ -310,7 +313,8 @@ def test_a_mixture_of_experts_as_a_whole(adaln, T, E, k, D, F):
     for name, got, want in zip(("y", "dx", "dw", "dwg", "dwu", "dwd"),
                                (y, *(t.grad for t in leaves)), (ref, *grads)):
         assert bool(got.isfinite().all()), name
-        off, size = float((got.detach().double() - want).norm()), float(want.detach().norm())
+        want = want.detach()
+        off, size = float((got.detach().double() - want).norm()), float(want.norm())
         assert off <= 8e-3 * size if size > 0 else off == 0, (name, off, size)
     assert not bool(y[T // 3].any()) and not bool(x.grad[T // 3].any())
     status_ok()
