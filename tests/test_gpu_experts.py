@@ -99,6 +99,7 @@ SHAPES = [
     (8, 1111, 1000, 2728, "mixed"), (64, 700, 128, 136, "mixed"), (256, 900, 64, 72, "mixed"),
     (33, 33, 392, 328, "even"), (7, 2100, 520, 312, "one"), (2, 4100, 512, 768, "mixed"),
     (4, 256, 5120, 648, "even"), (16, 64, 200, 8200, "mixed"), (256, 1, 8, 16, "one"),
+    (3, 700, 256, 8200, "mixed"), (2, 600, 1000, 4096, "even"),  # few tiles: split sums
 ]
 
 
