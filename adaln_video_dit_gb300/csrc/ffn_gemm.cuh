@@ -277,9 +277,9 @@ __device__ __forceinline__ int end_of(const Dims& s, const Unit& u) {
 }
 
 template <bool GROUPED>
-__device__ __forceinline__ void store_block(const CUtensorMap* m, int col, int row, int z, uint32_t block) {
+__device__ __forceinline__ void store_block(const CUtensorMap* m, int col, int row, uint32_t block) {
   if constexpr (GROUPED)
-    tma_store(m, col, row, z, block);
+    tma_store(m, col, row, 0, block);
   else
     tma_store(m, col, row, block);
 }
@@ -329,8 +329,6 @@ __device__ __forceinline__ void epilogue_plain(const Problem& p, const Dims& s, 
                                                uint32_t acc, int row0, int half, uint32_t buf,
                                                int lane, int& turn) {
   const int M = s.M, N = s.N, splits = s.splits, chunks = s.w / 16, end = end_of<GROUPED>(s, u);
-  const int z = GROUPED && s.by_k ? u.e : 0;
-  const bool none = GROUPED && u.k0 == u.k1;  // an empty sum
 #pragma unroll 1
   for (int c = half; c < chunks; c += 2) {
     const int col = u.n * 2 * s.w + c * 32;
@@ -339,11 +337,7 @@ __device__ __forceinline__ void epilogue_plain(const Problem& p, const Dims& s, 
     uint32_t r[32];
     tmem_ld32(acc + c * 32, r);
     tc_wait_ld();
-    if (none) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) r[i] = 0;
-    }
-    if (splits > 1) {
+    if (GROUPED || splits > 1) {  // (GROUPED: partial sums only)
       const int left = row0 + lane < end ? N - col : 0;  // columns of this row to write
       float4* o = reinterpret_cast<float4*>(p.partial +
                                             ((int64_t)u.split * M + row0 + lane) * N + col);
@@ -365,7 +359,7 @@ __device__ __forceinline__ void epilogue_plain(const Problem& p, const Dims& s, 
       fence_async_shared();
       __syncwarp();
       if (elect_one()) {
-        if (row0 < end) store_block<GROUPED>(&p.out, col, row0, z, block);
+        if (row0 < end) tma_store(&p.out, col, row0, block);
         bulk_commit();
       }
     }
@@ -404,7 +398,7 @@ __device__ __forceinline__ void epilogue_gate(const GemmArgs& a, const Dims& s, 
     fence_async_shared();
     __syncwarp();
     if (elect_one()) {
-      if (row0 < end) store_block<GROUPED>(&a.h, col, row0, 0, block);
+      if (row0 < end) store_block<GROUPED>(&a.h, col, row0, block);
       bulk_commit();
     }
     if (SAVE && row0 < end) {
@@ -470,9 +464,9 @@ __device__ __forceinline__ void chunk_gate_bwd(const GemmArgs& a, uint32_t acc, 
   __syncwarp();
   if (elect_one()) {
     if (row0 < end) {
-      store_block<GROUPED>(&a.dg, col, row0, 0, buf);
-      store_block<GROUPED>(&a.du, col, row0, 0, buf + kBlock);
-      store_block<GROUPED>(&a.h, col, row0, 0, buf + 2 * kBlock);
+      store_block<GROUPED>(&a.dg, col, row0, buf);
+      store_block<GROUPED>(&a.du, col, row0, buf + kBlock);
+      store_block<GROUPED>(&a.h, col, row0, buf + 2 * kBlock);
     }
     bulk_commit();
   }
