@@ -19,8 +19,8 @@
 // several loads in flight.  Sums are fp32, over j in order, outputs rounded once.
 //
 // Measured (one GB300, T = 32760, D = 5120, bf16, two of 8 experts): the route 7 us,
-// sorting 146 us and back 153, combining 146 us and back 241 (1007 and 1678 MB: 98 to
-// 104 % of the copy rate).  The route of 6666 pairs, 64 experts, 5.6 us
+// sorting 143 us and back 147, combining 141 us and back 239 (1007 and 1678 MB: 102 to
+// 107 % of the copy rate, the last writes still in L2).  The route of 6666 pairs, 64 experts, 5.6 us
 // (with the instruction that finds equal lanes in place of the votes, and the pairs
 // walked twice, 9.0), of 524288, 256 experts, 12 us (28).
 #include "ffn.cuh"
