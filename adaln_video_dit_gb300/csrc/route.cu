@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
         sum += c;
       }
     }
-    padded = e < a.E ? (int)((int64_t)(total + a.align - 1) / a.align * a.align) : 0;
+    padded = e < a.E ? (int)(((int64_t)total + a.align - 1) / a.align * a.align) : 0;
     start = padded;
     for (int d = 1; d < 32; d <<= 1) {
       const int v = __shfl_up_sync(~0u, start, d);

@@ -217,6 +217,19 @@ def test_offsets_past_32_bits(adaln):
     status_ok()
 
 
+def test_as_many_pairs_as_32_bits_hold(adaln):
+    """Pairs whose number, rounded up to the alignment, only just fits: 2^31 - 2, by threes."""
+    T = 2 ** 31 - 2
+    r = adaln.adaln_route(torch.zeros(T, 1, dtype=torch.int32, device="cuda"), 1, align=3)
+    assert r.rows == T and r.starts.tolist() == [0, T] and r.counts.tolist() == [T]
+    for at in range(0, T, 1 << 28):
+        n = min(1 << 28, T - at)
+        assert torch.equal(r.row[at:at + n, 0], torch.arange(at, at + n, dtype=torch.int32, device="cuda"))
+    status_ok()
+    del r
+    torch.cuda.empty_cache()
+
+
 def test_on_streams_and_in_a_graph(adaln):
     T, k, E, D = 9000, 2, 8, 256
     expert = torch.from_numpy(choices(T, k, E, 2)).cuda()
