@@ -388,8 +388,12 @@ class MixtureFFN(torch.nn.Module):
         self.experts, self.top_k, self.act = experts, top_k, act
 
     def forward(self, x, mask=None):
-        # (The router's few products in 32 bits: its probabilities choose the experts.)
-        p, expert = (x.float() @ self.router.t()).softmax(-1).topk(self.top_k, -1)
+        # (The router's few products in 32 bits: its probabilities choose the experts.
+        # What is masked stays out of them: a NaN there would be in the router's gradient.)
+        seen = x.float()
+        if mask is not None:
+            seen = torch.where(mask[..., None], seen, 0.0)
+        p, expert = (seen @ self.router.t()).softmax(-1).topk(self.top_k, -1)
         if mask is not None:
             expert = torch.where(mask[..., None], expert, -1)
         r = route(expert, self.experts)

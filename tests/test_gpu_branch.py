@@ -194,6 +194,26 @@ def test_a_mixture_of_no_tokens(adaln):
     status_ok()
 
 
+def test_masked_tokens_take_part_in_nothing(adaln):
+    """NaN and infinities in masked tokens: outputs and gradients, the router's among
+    them, are those of the other tokens alone."""
+    from adaln_video_dit_gb300.autograd import MixtureFFN
+    torch.manual_seed(5)
+    m = MixtureFFN(64, 96, 4, device="cuda")
+    x = torch.randn(3, 40, 64, device="cuda", dtype=BF16)
+    mask = torch.rand(3, 40, device="cuda") < 0.6
+    clean, foul = torch.where(mask[..., None], x, 0.0), torch.where(mask[..., None], x, float("nan"))
+    foul[:, ::2] = torch.where(mask[:, ::2, None], x[:, ::2], float("inf"))
+    results = []
+    for t in (clean.requires_grad_(), foul.requires_grad_()):
+        y = m(t, mask)
+        results.append([y.detach(), *torch.autograd.grad(y.float().square().sum(), [t, *m.parameters()])])
+    assert not any(bool(t.isnan().any()) for t in results[0])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert not bool(results[0][0][~mask].any()) and not bool(results[0][1][~mask].any())
+    status_ok()
+
+
 def test_calls_and_refusals_keep_no_references(adaln):
     s = make(5)
     r = adaln.adaln_route(s["expert"], 6)
