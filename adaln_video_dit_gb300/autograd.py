@@ -393,7 +393,8 @@ class MixtureFFN(torch.nn.Module):
         seen = x.float()
         if mask is not None:
             seen = torch.where(mask[..., None], seen, 0.0)
-        p, expert = (seen @ self.router.t()).softmax(-1).topk(self.top_k, -1)
+        with torch.autocast(x.device.type, enabled=False):
+            p, expert = (seen @ self.router.float().t()).softmax(-1).topk(self.top_k, -1)
         if mask is not None:
             expert = torch.where(mask[..., None], expert, -1)
         r = route(expert, self.experts)

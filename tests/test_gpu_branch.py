@@ -214,6 +214,27 @@ def test_masked_tokens_take_part_in_nothing(adaln):
     status_ok()
 
 
+def test_the_router_computes_in_32_bits(adaln):
+    """Under autocast a mixture's bits are those without; one cast to bf16 as a whole runs,
+    with its rounded router's."""
+    from adaln_video_dit_gb300.autograd import MixtureFFN
+    torch.manual_seed(6)
+    m = MixtureFFN(64, 96, 4, device="cuda")
+    x = torch.randn(100, 64, device="cuda", dtype=BF16)
+    want = m(x)
+    with torch.autocast("cuda", dtype=BF16):
+        got = m(x)
+    assert torch.equal(got, want)
+    m.router.data = m.router.data.bfloat16().float()
+    want = m(x)
+    m.to(BF16)
+    got = m(x)
+    assert torch.equal(got, want)
+    got.float().sum().backward()
+    assert m.router.grad.dtype == BF16 and bool(m.router.grad.any())
+    status_ok()
+
+
 def test_calls_and_refusals_keep_no_references(adaln):
     s = make(5)
     r = adaln.adaln_route(s["expert"], 6)
