@@ -272,9 +272,13 @@ class GatedResidual(torch.nn.Module):
 
 
 def route(expert, num_experts, align=64):
-    """Where tokens go: expert [..., k] holds each token's choices (-1 for none), and
-    the Route sorts the (token, choice) pairs by expert, for expert_sort and
-    expert_combine."""
+    """Where tokens go: expert [..., k], of a signed integer type, holds each token's choices
+    (-1 for none), and the Route sorts the (token, choice) pairs by expert, for
+    expert_sort and expert_combine."""
+    if expert.dtype in (torch.bool, torch.uint8) or expert.is_floating_point() or expert.is_complex():
+        raise TypeError(f"expert must be of a signed integer type, got {expert.dtype}")
+    if expert.dtype == torch.int64:  # none wraps to an expert: what is none is refused as it is
+        expert = expert.clamp(-2, num_experts)
     return _lib.adaln_route(expert.reshape(-1, expert.shape[-1]).to(torch.int32).contiguous(), num_experts,
                             align)
 
@@ -395,6 +399,7 @@ class MixtureFFN(torch.nn.Module):
             seen = torch.where(mask[..., None], seen, 0.0)
         with torch.autocast(x.device.type, enabled=False):
             p, expert = (seen @ self.router.float().t()).softmax(-1).topk(self.top_k, -1)
+        expert = expert.int()
         if mask is not None:
             expert = torch.where(mask[..., None], expert, -1)
         r = route(expert, self.experts)

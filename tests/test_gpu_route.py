@@ -278,6 +278,18 @@ def test_nodes(adaln):
     close(weight.grad, dots, 66 * U * 2 * x.detach().double().abs().sum(-1, keepdim=True).expand(dots.shape), "dw")
 
 
+def test_wide_experts_do_not_wrap(adaln):
+    """int64 values that are experts in their lower 32 bits only are out of range."""
+    from adaln_video_dit_gb300.autograd import route
+    for e in (2 ** 32 + 1, 2 ** 40, -2 ** 32, 2 ** 32 - 1, 2 ** 63 - 1):
+        r = route(torch.tensor([[1, e]], device="cuda"), 5)
+        assert adaln.adaln_get_status() == (adaln.ADALN_ERR_EXPERT, adaln.ADALN_DEV_EXPERT_RANGE)
+        assert r.row.tolist() == [[0, -1]] and r.counts.tolist() == [0, 1, 0, 0, 0]
+    for dt in (torch.float32, torch.bool, torch.uint8):
+        with pytest.raises(TypeError):
+            route(torch.zeros(4, 2, device="cuda", dtype=dt), 5)
+
+
 def test_trace_counts_the_launches(adaln):
     expert = torch.from_numpy(choices(70000, 2, 5, 4)).cuda()
     x, w = torch.randn(70000, 64, device="cuda"), torch.rand(70000, 2, device="cuda")
