@@ -217,6 +217,7 @@ class DropoutFunction(torch.autograd.Function):
         held = torch.is_tensor(rng)
         ctx.save_for_backward(h2 if of_gate else None, gate, seg_id, rng if held else None)
         ctx.shape, ctx.p, ctx.rng = shape, p, None if held else rng
+        ctx.x_shape = x.shape if x is not None else None
         return _lib.adaln_dropout_fwd(h2, p, rng, x=x2, gate=gate, seg_id=seg_id).reshape(shape)
 
     @staticmethod
@@ -229,7 +230,7 @@ class DropoutFunction(torch.autograd.Function):
             dh, dgate = _lib.adaln_dropout_bwd(dy2, ctx.p, ctx.rng if rng is None else rng, h=h, gate=gate,
                                                seg_id=seg_id)
             dh = dh.reshape(ctx.shape)
-        return (dh, dy if ctx.needs_input_grad[1] else None,
+        return (dh, dy.reshape(ctx.x_shape) if ctx.needs_input_grad[1] else None,
                 dgate.to(gate.dtype) if dgate is not None else None, None, None, None)
 
 

@@ -308,6 +308,18 @@ def test_nodes(adaln):
     assert torch.equal(dropout(h, 0.0), h)
 
 
+def test_each_gradient_has_its_inputs_shape(adaln):
+    from adaln_video_dit_gb300.autograd import gated_residual
+    h, x, gate, seg, dy = inputs(6, 64, 2, F32, seed=5)
+    shapes = ((6, 64), (1, 6, 64), (2, 3, 64))
+    for hs in shapes:
+        for xs in shapes:
+            leaves = [x.view(xs).clone().requires_grad_(), h.view(hs).clone().requires_grad_()]
+            gated_residual(*leaves, gate, seg, 0.3, (5, 5)).backward(dy.view(hs))
+            assert leaves[0].grad.shape == xs and leaves[1].grad.shape == hs
+            assert torch.equal(leaves[0].grad.view(6, 64), dy)
+
+
 def test_trace_counts_the_launches(adaln):
     h, x, gate, seg, dy = inputs(9, 64, 2, F32)
     adaln.adaln_trace_begin(8)
