@@ -276,7 +276,7 @@ def route(expert, num_experts, align=64):
     """Where tokens go: expert [..., k], of a signed integer type, holds each token's choices
     (-1 for none), and the Route sorts the (token, choice) pairs by expert, for
     expert_sort and expert_combine."""
-    if expert.dtype in (torch.bool, torch.uint8) or expert.is_floating_point() or expert.is_complex():
+    if expert.dtype not in (torch.int8, torch.int16, torch.int32, torch.int64):
         raise TypeError(f"expert must be of a signed integer type, got {expert.dtype}")
     if expert.dtype == torch.int64:  # none wraps to an expert: what is none is refused as it is
         expert = expert.clamp(-2, num_experts)

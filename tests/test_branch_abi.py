@@ -316,3 +316,18 @@ def test_experts_ffn_saves_only_for_a_gradient(lib, monkeypatch):
     for bad in (dict(top_k=0), dict(top_k=5), dict(act="relu")):
         with pytest.raises(ValueError):
             autograd.MixtureFFN(8, 16, 4, **bad)
+
+
+def test_experts_are_of_a_signed_integer_type(lib, monkeypatch):
+    """Anything else is refused before the call: uint32 and uint64 values that fit no
+    int32 would wrap to an expert, or to -1."""
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    monkeypatch.setattr(autograd._lib, "adaln_route", lambda e, E, align: e)
+    for dt in (torch.int8, torch.int16, torch.int32, torch.int64):
+        got = autograd.route(torch.tensor([[1, -1]], dtype=dt), 5)
+        assert got.dtype == torch.int32 and got.tolist() == [[1, -1]]
+    for dt, v in ((torch.uint8, 1), (torch.uint16, 1), (torch.uint32, 2 ** 32 - 1), (torch.uint64, 2 ** 32 + 3),
+                  (torch.bool, 1), (torch.float32, 1), (torch.bfloat16, 1), (torch.complex64, 1)):
+        with pytest.raises(TypeError, match="signed integer"):
+            autograd.route(torch.tensor([[1, v]], dtype=dt), 5)
