@@ -284,6 +284,12 @@ def route(expert, num_experts, align=64):
                             align)
 
 
+def _seen_whole(name, like):
+    """{name: zeros} for a call that leaves a gradient's rows behind the last expert as they
+    were, while anomaly detection looks at whole gradients for NaN; else nothing."""
+    return {name: torch.zeros_like(like)} if torch.is_anomaly_enabled() else {}
+
+
 class ExpertSortFunction(torch.autograd.Function):
     """xs[route.row[t, j]] = x[t].  Saves the route's indices."""
 
@@ -319,14 +325,17 @@ class ExpertCombineFunction(torch.autograd.Function):
     def backward(ctx, dy):
         ys, weight, *indices = ctx.saved_tensors
         dys, dw = _lib.adaln_expert_combine_bwd(dy.reshape(-1, dy.shape[-1]).contiguous(), ys, weight,
-                                                _lib.Route(*indices, ctx.rows, ctx.align))
+                                                _lib.Route(*indices, ctx.rows, ctx.align),
+                                                **_seen_whole("dys", ys))
         return (dys, dw.reshape(ctx.weight[0]).to(ctx.weight[1])) + (None,) * 5
 
 
 def expert_sort(x, route):
     """Tokens x [..., D] sorted by expert: [route.rows, D], each at the rows of its
     choices, zeros between the experts' rows (differentiable).  Rows from
-    route.starts[-1] on hold nothing: they are not written, here or in a gradient."""
+    route.starts[-1] on hold nothing: they are not written, here or in a gradient, and
+    may hold NaN (a hook on a sorted array's gradient sees them; zeros under
+    torch.autograd.detect_anomaly)."""
     return ExpertSortFunction.apply(x, *route)
 
 
@@ -355,7 +364,7 @@ class ExpertsFFNFunction(torch.autograd.Function):
     def backward(ctx, dys):
         xs, wg, wu, wd, starts, saved = ctx.saved_tensors
         return (*_lib.adaln_experts_ffn_bwd(dys.to(xs.dtype).contiguous(), xs, wg, wu, wd, starts, saved,
-                                            act=ctx.act), None, None, None)
+                                            act=ctx.act, **_seen_whole("dxs", xs)), None, None, None)
 
 
 def experts_ffn(xs, wg, wu, wd, route, act="silu"):

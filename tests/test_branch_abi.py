@@ -331,3 +331,42 @@ def test_experts_are_of_a_signed_integer_type(lib, monkeypatch):
                   (torch.bool, 1), (torch.float32, 1), (torch.bfloat16, 1), (torch.complex64, 1)):
         with pytest.raises(TypeError, match="signed integer"):
             autograd.route(torch.tensor([[1, v]], dtype=dt), 5)
+
+
+def test_anomaly_detection_finds_nothing_in_rows_that_hold_nothing(lib, monkeypatch):
+    """The calls leave the rows behind the last expert as they were.  A gradient with NaN
+    there is no anomaly: where that is looked for, the nodes hand in zeros; elsewhere
+    nothing, which costs nothing."""
+    import torch
+    from adaln_video_dit_gb300 import autograd
+    L, given = autograd._lib, []
+    used, rows = 3, 7
+
+    def rows_of(like, out):
+        given.append(out is not None)
+        out = torch.full_like(like, float("nan")) if out is None else out
+        out[:used] = 1
+        return out
+
+    monkeypatch.setattr(L, "adaln_expert_sort_fwd", lambda x, r: torch.ones(rows, x.shape[1], dtype=x.dtype))
+    monkeypatch.setattr(L, "adaln_expert_sort_bwd", lambda d, r: d[:used] * 1)
+    monkeypatch.setattr(L, "adaln_experts_ffn_fwd", lambda xs, *a, **kw: (xs * 1, xs))
+    monkeypatch.setattr(L, "adaln_experts_ffn_bwd", lambda dys, xs, wg, wu, wd, starts, saved, act, dxs=None: (
+        rows_of(xs, dxs), wg * 0, wu * 0, wd * 0))
+    monkeypatch.setattr(L, "adaln_expert_combine_fwd", lambda ys, w, r: ys[:used] * 1)
+    monkeypatch.setattr(L, "adaln_expert_combine_bwd", lambda d, ys, w, r, dys=None: (rows_of(ys, dys), w * 0))
+    r = L.Route(torch.zeros(used, 1, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
+                torch.zeros(2, dtype=torch.int32), rows, 64)
+
+    def step():
+        given.clear()
+        x, w = torch.ones(used, 8, requires_grad=True), torch.ones(used, 1, requires_grad=True)
+        m = [torch.ones(2, 8, 8, requires_grad=True) for _ in range(3)]
+        autograd.expert_combine(autograd.experts_ffn(autograd.expert_sort(x, r), *m, r), w, r).sum().backward()
+        return x.grad
+
+    want = step()
+    assert given == [False, False]
+    with torch.autograd.detect_anomaly():
+        assert torch.equal(step(), want)
+    assert given == [True, True]

@@ -300,3 +300,27 @@ def test_gradients_of_shared_leaves_add_up(adaln):
         total = a.double() + b.double()
         assert bool(((total - c.double()).abs() <= torch.finfo(c.dtype).eps / 2 * total.abs() + 1e-30).all())
     status_ok()
+
+
+def test_a_mixtures_step_under_anomaly_detection(adaln):
+    """With NaN in all memory that is allocated, anomaly detection finds none in a step's
+    gradients, sorted ones among them, and the step's bits are those without it."""
+    from adaln_video_dit_gb300.autograd import MixtureFFN
+    torch.manual_seed(8)
+    m = MixtureFFN(64, 96, 4, device="cuda")
+    x = torch.randn(37, 64, device="cuda", dtype=BF16, requires_grad=True)
+
+    def step():
+        y = m(x)
+        return [y.detach(), *torch.autograd.grad(y.float().square().sum(), [x, *m.parameters()])]
+
+    want = step()
+    torch.use_deterministic_algorithms(True, warn_only=True)  # (fills what is allocated)
+    try:
+        assert bool(torch.empty(1000, device="cuda").isnan().all())
+        with torch.autograd.detect_anomaly():
+            got = step()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    status_ok()
