@@ -88,9 +88,11 @@ def main(argv=None):
     ap.add_argument("--hidden", type=int, default=4096)
     ap.add_argument("--steps", type=int, default=5)
     ap.add_argument("--experts", type=int, default=0)
-    ap.add_argument("--top-k", type=int, default=2)
-    ap.add_argument("--dropout", type=float, default=0.0)
+    ap.add_argument("--top-k", type=int, help="of a mixture of experts (2)")
+    ap.add_argument("--dropout", type=float, default=0.0, help="of a mixture's block")
     a = ap.parse_args(argv)
+    if not a.experts and (a.top_k is not None or a.dropout):
+        ap.error("--top-k and --dropout need --experts")
     torch.manual_seed(0)
     samples = [(77, 4, 16, 16), (77, 1, 16, 16), (0, 2, 12, 20)]  # text, frames, height, width
     lengths = [t + f * h * w for t, f, h, w in samples]
@@ -98,7 +100,8 @@ def main(argv=None):
     seg_id = torch.repeat_interleave(torch.arange(len(samples), dtype=torch.int32),
                                      torch.tensor(lengths)).cuda()
     if a.experts:
-        block = MixtureDiTBlock(a.dim, a.heads, a.hidden, 20, a.experts, a.top_k, a.dropout)
+        block = MixtureDiTBlock(a.dim, a.heads, a.hidden, 20, a.experts,
+                                2 if a.top_k is None else a.top_k, a.dropout)
     else:
         block = DiTBlock(a.dim, a.heads, a.hidden, rows=20)
     x = torch.randn(sum(lengths), a.dim, device="cuda", dtype=torch.bfloat16)
