@@ -377,3 +377,22 @@ def test_binding_refuses(adaln):
         adaln.adaln_experts_ffn_bwd(dys, xs, wg, wu, wd, starts, saved[:-300])
     with pytest.raises(ValueError):
         adaln.adaln_experts_ffn_bwd(dys, xs, wg, wu, wd, starts, None)
+
+
+@pytest.mark.parametrize("tokens,D,F,forward,backward", [
+    ([300, 500], 64, 96, 2, 2),           # tiles; sums over k as they are
+    ([250, 250, 200], 256, 8200, 3, 3),   # few tiles: both sums over F split and joined
+    ([3, 0, 64, 1], 264, 520, 2, 3),      # few rows: dh, dx, and the weight gradients
+], ids=["tiles", "split", "few"])
+def test_launches_of_each_form(adaln, tokens, D, F, forward, backward):
+    """As many as a call needs, none beside them."""
+    xs, wg, wu, wd, starts, dys = inputs(tokens, D, F, spare=0)
+    counts = []
+    for call in (lambda: adaln.adaln_experts_ffn_fwd(xs, wg, wu, wd, starts, save=True)[1],
+                 lambda: adaln.adaln_experts_ffn_bwd(dys, xs, wg, wu, wd, starts, saved)):
+        adaln.adaln_trace_begin(16)
+        saved = call()
+        adaln.adaln_trace_end()
+        counts.append(adaln.adaln_trace_get(adaln.ADALN_KERNEL_EXPERTS)[0])
+    assert counts == [forward, backward]
+    status_ok()
