@@ -355,3 +355,16 @@ def test_binding_refuses(adaln):
         b(dy, 0.1, (1, 2), h=h, gate=gate, seg_id=seg,
           workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.code == adaln.ADALN_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("where", ["first", "last", "amid"])
+def test_one_long_segment_among_many_short_ones(adaln, where):
+    """Nearly all tokens in one of 300 segments, the others with one, two or none."""
+    T, D, nseg = 30011, 264, 300
+    h, x, gate, _, dy = inputs(T, D, nseg, BF16, seed=11)
+    at = {"first": 0, "last": nseg - 1, "amid": 140}[where]
+    n = np.arange(nseg) % 3
+    n[at] = 0
+    n[at] = T - n.sum()
+    seg = torch.from_numpy(np.repeat(np.arange(nseg), n).astype(np.int32)).cuda()
+    against(call(adaln, h, x, gate, seg, dy, 0.1, (5, 6)), h, x, gate, seg, dy, 0.1, (5, 6))
