@@ -27,7 +27,9 @@
 // segment; 1007 MB each way): forward 146 us, 6.9 TB/s; backward with dgate 166 us
 // (its rows 155, its sums the rest; with p = 0 about 10 us less: the generator keeps
 // the issue slots busy).  T = 5003, D = 1000, fp32, 37 segments, 60 MB: 12 and 21 us,
-// of which the start and end of two and three launches are a third.
+// of which the start and end of two and three launches are a third.  T = 262144, D =
+// 1024, 300 segments: backward 260 us, but 525 where one of them has nearly all tokens:
+// the sums' lanes go by the average segment, and one lane then adds its 900 partials.
 #include <cmath>
 
 #include "common.cuh"

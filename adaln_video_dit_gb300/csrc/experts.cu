@@ -15,11 +15,19 @@
 // weight gradients' sums take the zeros in.  A tile past its expert's rows neither
 // reads A there nor stores what comes of it.
 //
-// Few rows an expert have a form of their own (experts_few.cu), up to about one block
-// of 64 rows an expert: with 64 rows of each of 16 experts at 1000 x 2728, 8 at 1536 x
-// 4096, 64 at 2048 x 1024 and 4 at 5120 x 3584 it takes 61, 62, 137 and 80 us for the
-// forward where the tiles take 63, 70, 150 and 108; with 128 rows 95, 74, 164 and 85
-// against 81, 73, 156 and 105, with 192 rows it loses on all four.
+// Few rows an expert have a form of their own (experts_few.cu), while the arrays hold at
+// most one block of 64 rows and a half an expert: filled with 64 rows of each of 16
+// experts at 1000 x 2728, 8 at 1536 x 4096, 64 at 2048 x 1024 and 4 at 5120 x 3584 it takes
+// 61, 62, 137 and 80 us for the forward where the tiles take 63, 70, 150 and 108; with 128
+// rows 95, 74, 164 and 85 against 81, 73, 156 and 105, with 192 rows it loses on all four.
+// The rule sees the arrays' rows only, and a route's hold 63 an expert beside its pairs:
+// a routed call leaves the form at 33 (many experts) to 40 (eight) pairs an expert on
+// average, wherever they go.  On both sides of that, spread evenly, forward and backward
+// alone from cold caches: 8 experts of 1536 x 4096 76 and 136 us with 34 pairs, 83 and 134
+// with 48; 16 of 1000 x 2728 75 and 153, 74 and 147; 64 of 2048 x 1024 154 and 324 with
+// 33, 158 and 313 with 34.  All to one expert, whose weights the form then reads again for
+// every 64 rows: 64 of 2048 x 1024 54 and 218 us with 32 pairs an expert, 37 and 250 with
+// 34; 256 of 512 x 1024 93 and 300, 38 and 269.
 //
 // Bound (one GB300): the tensor cores at the power limit with thousands of rows an
 // expert (T = 32760, two of 8 experts, D = 5120, F = 13824, forward 15.9 to 16.4 ms, 1700

@@ -8,11 +8,14 @@
 // weights through a TMA ring, and multiplies them with the 64 rows at a time (an
 // accumulator holds 128 features x 64 rows).  The other form's tiles of 256 rows are
 // bound here by what they copy and multiply for empty rows, and by one tile's k loop
-// where few experts are met.  Measured (one GB300, forward; floor from the weights at
-// the copy rate): D = 1536, F = 4096, eight experts met 62 us (45; tiles 70), two 26 us
-// (11), one 16.5 us (5.6; tiles 31.8); D = 5120, F = 13824, two experts 137 us (127); 64
-// experts of 2048 x 1024 139 us (120).  What is left is each CTA's start and end, some
-// 5 us a launch.
+// where few experts are met.  Measured (one GB300, forward, calls in a row on arrays
+// without spare rows; floor from the weights at the copy rate): D = 1536, F = 4096, eight
+// experts met 62 us (45; tiles 70), two 26 us (11), one 16.5 us (5.6; tiles 31.8); D = 5120,
+// F = 13824, two experts 137 us (127); 64 experts of 2048 x 1024 139 us (120).  What is left
+// is each CTA's start and end, some 5 us a launch.  16 pairs in a route's array for eight
+// experts (512 rows, which the splits of k are chosen by): seven met 50 us, six 46, two 25,
+// one 22.  Their backward, whose weight gradients are written for all eight: 132 us with
+// eight met (90 for the bytes), 118 with six, 87 with one (51).
 //
 // Four products, alike but for their maps and epilogues:
 //   projections  [g; u] = [Wg; Wu] x'       h = act(g) u, g and u saved
@@ -427,8 +430,9 @@ FewArgs args_of(const Experts& x, unsigned* status) {
 
 }  // namespace
 
-// Rows for which each expert has about one block of 64: pairs up to some 30 an expert
-// (the sorted arrays' capacity counts 63 rows an expert beside the pairs).
+// Arrays of at most a block and a half of 64 rows an expert: a route's up to 33 to 40 pairs
+// an expert on average (they hold 63 rows an expert beside the pairs); both sides measured
+// in experts.cu.
 bool experts_few_serve(int64_t rows, int32_t E) { return 2 * (rows / kRows) <= 3 * (int64_t)E; }
 
 cudaError_t experts_few_fwd(const Experts& x, void* ys, void* saved, void* h, unsigned* status,

@@ -492,13 +492,16 @@ ADALN_API int adaln_expert_combine_bwd(const void* dy, const void* ys, const flo
  * and the next expert's among them: xs and dys have zeros there (as the sort and the
  * combination's backward write them), and ys and dxs get zeros.  Rows from starts[E]
  * on are neither read into a result nor written.  Sums, roundings and what is saved
- * are the feed-forward block's; so are D and F; rows is at most ADALN_FFN_MAX_T.
+ * are the feed-forward block's: h, dg and du are rounded to bf16 before the products that
+ * take them, so results are off by two roundings where one is the least (of normally
+ * distributed values 2.35e-3 in the 2-norm, 1.66e-3 with none in between).  So are D and
+ * F; rows is at most ADALN_FFN_MAX_T.
  * Starts that break these rules are recorded (ADALN_DEV_EXPERT_RANGE); no access leaves
  * the arrays, and the outputs of such a call are unspecified.
  *
  * Forward: two launches (a third where few rows make it worth splitting the sum over
- * F).  Backward: two (or three) launches; the gradient of an expert without rows is
- * zeros.  No atomics: bitwise reproducible for a given device and sizes.  Errors as
+ * F).  Backward: two launches (three with few rows, or where dx's sum is split); the
+ * gradient of an expert without rows is zeros.  No atomics: bitwise reproducible for a given device and sizes.  Errors as
  * for the feed-forward block.
  */
 ADALN_API int adaln_experts_ffn_saved_size(int64_t rows, int32_t E, int32_t D, int32_t F,
