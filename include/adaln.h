@@ -501,8 +501,8 @@ ADALN_API int adaln_expert_combine_bwd(const void* dy, const void* ys, const flo
  *
  * Forward: two launches (a third where few rows make it worth splitting the sum over
  * F).  Backward: two launches (three with few rows, or where dx's sum is split); the
- * gradient of an expert without rows is zeros.  No atomics: bitwise reproducible for a given device and sizes.  Errors as
- * for the feed-forward block.
+ * gradient of an expert without rows is zeros.  No atomics: bitwise reproducible for a
+ * given device and sizes.  Errors as for the feed-forward block.
  */
 ADALN_API int adaln_experts_ffn_saved_size(int64_t rows, int32_t E, int32_t D, int32_t F,
               adaln_dtype_t dtype, size_t* bytes);
